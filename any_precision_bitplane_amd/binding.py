@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_int32, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 from typing import Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -48,6 +48,11 @@ PW_NUM_STAGES = 4
 
 PW_EVENTS_STAGES = 0
 PW_EVENTS_KERNELS = 1
+
+PW_F32 = 0
+PW_F16 = 1
+PW_BF16 = 2
+PW_E4M3 = 3
 
 
 class PwMoeShape(ctypes.Structure):
@@ -137,6 +142,28 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "pw_pager_commit": (c_int32, [c_void_p, c_void_p, c_int32, POINTER(c_int32)]),
         "pw_pager_info": (c_int32, [c_void_p, c_int32, POINTER(PwPageInfo)]),
         "pw_pager_arena_used": (c_size_t, [c_void_p]),
+        "pw_rmsnorm": (c_int32, [c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                 c_void_p, c_float, c_int32, c_void_p, c_int64, c_void_p, c_int32, c_void_p]),
+        "pw_rmsnorm_backward_workspace_bytes": (c_size_t, [c_int32, c_int32]),
+        "pw_rmsnorm_backward": (c_int32, [c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                          c_float, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_size_t,
+                                          c_void_p]),
+        "pw_moe_permute_workspace_bytes": (c_size_t, [POINTER(PwMoeShape), c_int32]),
+        "pw_moe_permute": (c_int32, [POINTER(PwMoeShape), c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int32,
+                                     c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                     c_void_p, c_size_t, c_void_p]),
+        "pw_moe_permute_backward": (c_int32, [POINTER(PwMoeShape), c_int32, c_int32, c_void_p, c_int64, c_void_p,
+                                              c_void_p, c_int64, c_void_p]),
+        "pw_moe_unpermute": (c_int32, [POINTER(PwMoeShape), c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p,
+                                       c_void_p, c_int64, c_void_p]),
+        "pw_moe_unpermute_backward": (c_int32, [POINTER(PwMoeShape), c_int32, c_int32, c_void_p, c_int64, c_void_p,
+                                                c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p]),
+        "pw_router_backward_workspace_bytes": (c_size_t, [POINTER(PwMoeShape), c_int32]),
+        "pw_router_backward": (c_int32, [POINTER(PwMoeShape), c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
+                                         c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "pw_moe_forward_block": (c_int32, [POINTER(PwMoeShape), c_int32, c_void_p, c_void_p, c_void_p, c_float,
+                                           c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                           c_size_t, POINTER(PwMoeOptions), c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -153,7 +180,10 @@ def exported_symbols() -> Sequence[str]:
             "pw_dequant_block", "pw_planes_bytes", "pw_pack_planes", "pw_get_device_status", "pw_pager_create", "pw_pager_destroy",
             "pw_pager_set_block", "pw_pager_request", "pw_pager_execute", "pw_pager_commit", "pw_pager_info",
             "pw_pager_arena_used", "pw_router_topk", "pw_moe_forward_routed", "pw_moe_forward_layers",
-            "pw_plan_bitwidths"]
+            "pw_plan_bitwidths", "pw_rmsnorm", "pw_rmsnorm_backward_workspace_bytes", "pw_rmsnorm_backward",
+            "pw_moe_permute_workspace_bytes", "pw_moe_permute", "pw_moe_permute_backward", "pw_moe_unpermute",
+            "pw_moe_unpermute_backward", "pw_router_backward_workspace_bytes", "pw_router_backward",
+            "pw_moe_forward_block"]
 
 
 # ---------------------------------------------------------------------------
@@ -320,6 +350,232 @@ def pw_moe_forward_layers(shp: PwMoeShape, T: int, x, router_ws, blocks, qs, y, 
                                       ctypes.byref(opts) if opts is not None else None, _stream(stream))
     if check:
         _check(st, "pw_moe_forward_layers")
+    return st
+
+
+# --- around the layer ------------------------------------------------------
+# These calls take torch tensors: types and row strides come from them.  What
+# the library cannot see in a pointer is checked here first (device, type, a
+# contiguous last dimension, sizes) and refused as the library would refuse it.
+_DTYPES = None
+
+
+def _dtypes():
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: PW_F32, torch.float16: PW_F16, torch.bfloat16: PW_BF16,
+                   torch.float8_e4m3fn: PW_E4M3}
+    return _DTYPES
+
+
+class _Refused(Exception):
+    pass
+
+
+class _Call:
+    """The tensors of one call: all on one GPU, which is the current one while the call runs."""
+
+    def __init__(self, first):
+        if not getattr(first, "is_cuda", False):
+            raise _Refused("tensors must be on a GPU")
+        self.index = first.device.index
+
+    def _on_device(self, t, name):
+        if not getattr(t, "is_cuda", False) or t.device.index != self.index:
+            raise _Refused(f"{name} must be on the GPU of the other tensors")
+
+    def rows(self, t, name, n, H, dtype=None):
+        """(pointer, row stride) of a matrix of at least n rows of H elements."""
+        if t is None:
+            return None, 0
+        self._on_device(t, name)
+        if t.dim() != 2 or t.shape[1] != H or t.shape[0] < n or (H > 1 and t.stride(1) != 1):
+            raise _Refused(f"{name} must have at least {n} rows of {H} elements next to each other")
+        if dtype is not None and t.dtype != dtype:
+            raise _Refused(f"{name} must be {dtype}")
+        return t.data_ptr(), t.stride(0) if n > 1 else H
+
+    def array(self, t, name, n, dtype):
+        """Pointer of a contiguous tensor of at least n elements."""
+        if t is None:
+            return None
+        self._on_device(t, name)
+        if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+            raise _Refused(f"{name} must be {n} contiguous elements of {dtype}")
+        return t.data_ptr()
+
+    def workspace(self, t):
+        if t is None:
+            return None, 0
+        self._on_device(t, "workspace")
+        if not t.is_contiguous():
+            raise _Refused("workspace must be contiguous")
+        return t.data_ptr(), t.numel() * t.element_size()
+
+    def run(self, fn, *args, stream=None):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.index).cuda_stream
+        elif not isinstance(stream, int):
+            if stream.device.index != self.index:
+                raise _Refused("stream must be one of the tensors' GPU")
+            stream = stream.cuda_stream
+        if torch.cuda.current_device() == self.index:
+            return fn(*args, stream)
+        with torch.cuda.device(self.index):
+            return fn(*args, stream)
+
+
+def _row_op(name, check, body) -> int:
+    try:
+        st = body(load())
+    except _Refused as e:
+        if check:
+            raise PwError(PW_ERR_INVALID_ARG, f"{name}: {e}") from None
+        return PW_ERR_INVALID_ARG
+    if check and st != PW_OK:
+        raise PwError(st, name)
+    return st
+
+
+def pw_rmsnorm(T: int, H: int, x, weight, eps: float, y, residual=None, residual_out=None, scale=None, group: int = 0,
+               stream=None, check: bool = True) -> int:
+    """y: x's type, or torch.float8_e4m3fn with scale fp32 [T][groups]."""
+    def body(lib):
+        import torch
+        c = _Call(x)
+        dt = x.dtype
+        groups = (H + 127) // 128 if group else 1
+        px, sx = c.rows(x, "x", T, H)
+        pr, sr = c.rows(residual, "residual", T, H, dt)
+        po, so = c.rows(residual_out, "residual_out", T, H, dt)
+        py, sy = c.rows(y, "y", T, H)
+        return c.run(lib.pw_rmsnorm, T, H, _dtypes().get(dt, -1), px, sx, pr, sr, po, so,
+                     c.array(weight, "weight", H, dt), eps, _dtypes().get(y.dtype, -1), py, sy,
+                     c.array(scale, "scale", T * groups, torch.float32), group, stream=stream)
+    return _row_op("pw_rmsnorm", check, body)
+
+
+def pw_rmsnorm_backward_workspace_bytes(T_max: int, H: int) -> int:
+    return load().pw_rmsnorm_backward_workspace_bytes(T_max, H)
+
+
+def pw_rmsnorm_backward(T: int, H: int, dy, r, weight, eps: float, dx, dweight=None, workspace=None, dresidual=None,
+                        stream=None, check: bool = True) -> int:
+    def body(lib):
+        import torch
+        c = _Call(dy)
+        dt = dy.dtype
+        pd, sd = c.rows(dy, "dy", T, H)
+        pr, sr = c.rows(r, "r", T, H, dt)
+        pa, sa = c.rows(dresidual, "dresidual", T, H, dt)
+        px, sx = c.rows(dx, "dx", T, H, dt)
+        pw, nw = c.workspace(workspace)
+        return c.run(lib.pw_rmsnorm_backward, T, H, _dtypes().get(dt, -1), pd, sd, pr, sr,
+                     c.array(weight, "weight", H, dt), eps, pa, sa, px, sx,
+                     c.array(dweight, "dweight", H, torch.float32), pw, nw, stream=stream)
+    return _row_op("pw_rmsnorm_backward", check, body)
+
+
+def pw_moe_permute_workspace_bytes(shp: PwMoeShape, T_max: int) -> int:
+    return load().pw_moe_permute_workspace_bytes(ctypes.byref(shp), T_max)
+
+
+def pw_moe_permute(shp: PwMoeShape, T: int, x, ids, xs, offsets, inv, perm, workspace, x_scale=None, xs_scale=None,
+                   status=None, stream=None, check: bool = True) -> int:
+    def body(lib):
+        import torch
+        c = _Call(x)
+        H, S = shp.hidden, T * shp.top_k
+        groups = 0
+        if x_scale is not None:
+            if x_scale.dim() != 2:
+                raise _Refused("x_scale must have a row of scales per token")
+            groups = x_scale.shape[1]
+        px, sx = c.rows(x, "x", T, H)
+        ps, ss = c.rows(xs, "xs", S, H, x.dtype)
+        pw, nw = c.workspace(workspace)
+        return c.run(lib.pw_moe_permute, ctypes.byref(shp), T, _dtypes().get(x.dtype, -1), px, sx,
+                     c.array(x_scale, "x_scale", T * groups, torch.float32), groups,
+                     c.array(ids, "ids", S, torch.int32), ps, ss,
+                     c.array(xs_scale, "xs_scale", S * groups, torch.float32),
+                     c.array(offsets, "offsets", shp.num_experts + 1, torch.int32),
+                     c.array(inv, "inv", S, torch.int32), c.array(perm, "perm", S, torch.int32),
+                     c.array(status, "status", 1, torch.int32), pw, nw, stream=stream)
+    return _row_op("pw_moe_permute", check, body)
+
+
+def pw_moe_permute_backward(shp: PwMoeShape, T: int, dxs, inv, dx, stream=None, check: bool = True) -> int:
+    def body(lib):
+        import torch
+        c = _Call(dxs)
+        S = T * shp.top_k
+        ps, ss = c.rows(dxs, "dxs", S, shp.hidden)
+        px, sx = c.rows(dx, "dx", T, shp.hidden, dxs.dtype)
+        return c.run(lib.pw_moe_permute_backward, ctypes.byref(shp), T, _dtypes().get(dxs.dtype, -1), ps, ss,
+                     c.array(inv, "inv", S, torch.int32), px, sx, stream=stream)
+    return _row_op("pw_moe_permute_backward", check, body)
+
+
+def pw_moe_unpermute(shp: PwMoeShape, T: int, rows, inv, w, y, stream=None, check: bool = True) -> int:
+    """w: fp32 [T][k], or None for ones."""
+    def body(lib):
+        import torch
+        c = _Call(rows)
+        S = T * shp.top_k
+        pr, sr = c.rows(rows, "rows", S, shp.hidden)
+        py, sy = c.rows(y, "y", T, shp.hidden, rows.dtype)
+        return c.run(lib.pw_moe_unpermute, ctypes.byref(shp), T, _dtypes().get(rows.dtype, -1), pr, sr,
+                     c.array(inv, "inv", S, torch.int32), c.array(w, "w", S, torch.float32), py, sy, stream=stream)
+    return _row_op("pw_moe_unpermute", check, body)
+
+
+def pw_moe_unpermute_backward(shp: PwMoeShape, T: int, dy, rows, inv, w, drows, dw=None, stream=None,
+                              check: bool = True) -> int:
+    """dw None: not wanted (rows may then be None)."""
+    def body(lib):
+        import torch
+        c = _Call(dy)
+        H, S = shp.hidden, T * shp.top_k
+        pd, sd = c.rows(dy, "dy", T, H)
+        pr, sr = c.rows(rows, "rows", S, H, dy.dtype)
+        po, so = c.rows(drows, "drows", S, H, dy.dtype)
+        return c.run(lib.pw_moe_unpermute_backward, ctypes.byref(shp), T, _dtypes().get(dy.dtype, -1), pd, sd, pr, sr,
+                     c.array(inv, "inv", S, torch.int32), c.array(w, "w", S, torch.float32), po, so,
+                     c.array(dw, "dw", S, torch.float32), stream=stream)
+    return _row_op("pw_moe_unpermute_backward", check, body)
+
+
+def pw_router_backward_workspace_bytes(shp: PwMoeShape, T_max: int) -> int:
+    return load().pw_router_backward_workspace_bytes(ctypes.byref(shp), T_max)
+
+
+def pw_router_backward(shp: PwMoeShape, T: int, x, router_w, ids, w, dw, dx, drouter_w, workspace, dx_add=None,
+                       stream=None, check: bool = True) -> int:
+    def body(lib):
+        import torch
+        c = _Call(x)
+        n, S, E = T * shp.hidden, T * shp.top_k, shp.num_experts * shp.hidden
+        f16, f32 = torch.float16, torch.float32
+        pw, nw = c.workspace(workspace)
+        return c.run(lib.pw_router_backward, ctypes.byref(shp), T, c.array(x, "x", n, f16),
+                     c.array(router_w, "router_w", E, f16), c.array(ids, "ids", S, torch.int32),
+                     c.array(w, "w", S, f32), c.array(dw, "dw", S, f32), c.array(dx_add, "dx_add", n, f16),
+                     c.array(dx, "dx", n, f16), c.array(drouter_w, "drouter_w", E, f32), pw, nw, stream=stream)
+    return _row_op("pw_router_backward", check, body)
+
+
+def pw_moe_forward_block(shp: PwMoeShape, T: int, x, residual, norm_w, eps: float, router_w, blocks, q, y, stat_count,
+                         stat_mass, workspace, opts: Optional[PwMoeOptions] = None, stream=None,
+                         check: bool = True) -> int:
+    ws_bytes = workspace.numel() * workspace.element_size()
+    st = load().pw_moe_forward_block(ctypes.byref(shp), T, _ptr(x), _ptr(residual), _ptr(norm_w), eps, _ptr(router_w),
+                                     _ptr(blocks), _ptr(q), _ptr(y), _ptr(stat_count), _ptr(stat_mass),
+                                     _ptr(workspace), ws_bytes, ctypes.byref(opts) if opts is not None else None,
+                                     _stream(stream))
+    if check:
+        _check(st, "pw_moe_forward_block")
     return st
 
 

@@ -243,6 +243,141 @@ hipError_t launch_combine_router(const float* o, const float* w_prev, const int3
                                  float* w, uint32_t* count, float* mass, hipStream_t s);
 hipError_t launch_status_clear(uint32_t* status, hipStream_t s);
 
+// ----- operators around the layer (strides in elements unless said) --------
+constexpr int kMaxNormHidden = 32768;   // a block of sixteen waves holds a row, four chunks a lane
+constexpr int kNormGroup = 128;         // columns per scale of the 8-bit output
+constexpr int kNormFewRows = 1024;      // up to here a row is spread over all the waves it can use
+constexpr int kNormGradBlocks = 512;    // blocks (and shares of the weight's gradient) of the norm's backward pass
+
+struct NormArgs {
+  int T, H;
+  const void* x;
+  int64_t x_stride;
+  const void* residual;       // null: none
+  int64_t residual_stride;
+  void* residual_out;         // null: the sum is not stored
+  int64_t residual_out_stride;
+  const void* weight;
+  float eps;
+  void* y;
+  int64_t y_stride;
+  float* scale;               // e4m3 output: [T][groups]
+  int group;                  // 0: one scale a row, kNormGroup: one per 128 columns
+};
+hipError_t launch_rmsnorm(const NormArgs& a, int dtype, bool e4m3, hipStream_t s);
+
+struct NormGradArgs {
+  int T, H;
+  const void* dy;
+  int64_t dy_stride;
+  const void* r;
+  int64_t r_stride;
+  const void* weight;
+  float eps;
+  const void* dresidual;      // null: none
+  int64_t dresidual_stride;
+  void* dx;
+  int64_t dx_stride;
+  float* part;                // shares of dweight, null: dweight is not wanted
+};
+// A block of the backward pass has at least four waves and a row of up to 512
+// columns takes one, so up to four shares a block.
+inline size_t norm_grad_parts(int T, int H) {
+  const size_t rows = H <= 512 ? 4 : 1;
+  const size_t blocks = ((size_t)T + rows - 1) / rows;
+  return (blocks < (size_t)kNormGradBlocks ? blocks : (size_t)kNormGradBlocks) * rows;
+}
+hipError_t launch_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, hipStream_t s);
+
+constexpr int kPermuteSmallSlots = 4096;   // one launch up to here (every block reads all ids)
+constexpr int kPermutePieces = 64;         // pieces of a larger call whose slots are counted apart
+
+struct PermuteArgs {
+  int T, k, E;
+  const uint8_t* x;
+  int64_t row_bytes, x_stride, xs_stride;   // bytes
+  uint8_t* xs;
+  const float* x_scale;
+  float* xs_scale;
+  int groups;                 // scales a row, 0: none
+  const int32_t* ids;
+  int32_t* offsets;
+  int32_t* inv;
+  int32_t* perm;              // may be null
+  uint32_t* status;           // may be null
+  int32_t* counts;            // [pieces][E]
+  int block_tokens, pieces;
+  int64_t piece_tokens;
+};
+hipError_t launch_permute(PermuteArgs a, hipStream_t s);
+
+struct UnpermuteArgs {
+  int T, H, k;
+  const void* rows;
+  int64_t rows_stride;
+  const int32_t* inv;
+  const float* w;             // null: ones
+  void* y;
+  int64_t y_stride;
+};
+hipError_t launch_unpermute(const UnpermuteArgs& a, int dtype, hipStream_t s);
+
+struct UnpermuteGradArgs {
+  int T, H, k;
+  const void* dy;
+  int64_t dy_stride;
+  const void* rows;
+  int64_t rows_stride;
+  const int32_t* inv;
+  const float* w;             // null: ones
+  void* drows;
+  int64_t drows_stride;
+  float* dw;                  // null: not wanted
+};
+hipError_t launch_unpermute_grad(const UnpermuteGradArgs& a, int dtype, hipStream_t s);
+
+struct RouterGradArgs {
+  int T, H, E, k;
+  const uint16_t* x;
+  const uint16_t* router_w;
+  const int32_t* ids;
+  const float* w;
+  const float* dw;
+  const uint16_t* dx_add;     // null: zero
+  uint16_t* dx;
+  float* drouter_w;
+  int32_t* slot_e;            // [T][k] expert of the slot, -1: no part in drouter_w
+  float* slot_dl;             // [T][k] gradient of the slot's logit
+  float* part;                // [splits][E][H]
+  int splits, split_tokens;
+};
+// Stretches of tokens whose shares of drouter_w are summed apart: enough waves
+// (one per 128 columns and stretch) to fill the chip, stretches long enough
+// that writing and reading the shares stays small beside reading x.
+struct RouterGradPlan {
+  int splits, split_tokens;
+  size_t slot_e, slot_dl, part, total;   // workspace offsets
+};
+inline RouterGradPlan router_grad_plan(int H, int E, int k, int T) {
+  RouterGradPlan p;
+  const int64_t columns = (H + 127) / 128;
+  const int64_t least = 4 * E < 16 ? 16 : 4 * E < 512 ? 4 * E : 512;
+  const int64_t fill = ((int64_t)T * columns + 2047) / 2048;
+  const int64_t tokens = fill > least ? fill : least;
+  p.split_tokens = (int)tokens;
+  p.splits = (int)((T + tokens - 1) / tokens);
+  // no T' <= T has more stretches than this, so a workspace for T serves them all
+  const int64_t by_tokens = (T + least - 1) / least, by_fill = (2048 + columns - 1) / columns;
+  const int64_t most = by_tokens < by_fill ? by_tokens : by_fill;
+  size_t off = 0;
+  p.slot_e = off;  off = align_up(off + sizeof(int32_t) * (size_t)T * k, kAlign);
+  p.slot_dl = off; off = align_up(off + sizeof(float) * (size_t)T * k, kAlign);
+  p.part = off;    off = align_up(off + sizeof(float) * (size_t)most * E * H, kAlign);
+  p.total = off;
+  return p;
+}
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
+
 // The fused layer on a caller-provided scratch area (the workspace, or the
 // allocation-free entry point's static array).  `status`, if non-null,
 // replaces the status word of the scratch header as the place device errors

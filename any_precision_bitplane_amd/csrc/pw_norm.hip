@@ -1,0 +1,331 @@
+// Root-mean-square norm of rows with the residual's addition, an optional
+// 8-bit output, and its gradient.
+//
+//   r_i = x_i + residual_i            (fp32; stored rounded to the row type)
+//   y_i = r_i g_i / sqrt(mean_h r_h^2 + eps)
+//
+// The sum of squares, the mean and y stay in fp32; y is rounded once, to the
+// row type or to e4m3 after division by its scale.  The norm is taken of the
+// fp32 sum, before the residual's own rounding.
+//
+// The work is one pass over memory: a row's chunks of eight elements stay in
+// registers between the sum of squares and the output.
+#include "pw_rows.h"
+
+namespace pw {
+
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 7.888609052210118e-31f;   // 2^-100: scales stay divisible
+constexpr unsigned kMaxGrid = 1u << 20;
+
+// Sum over a row of WPR waves.  `part` holds one value per wave of the block;
+// callers alternate between two such arrays, so one barrier per sum is enough.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* part, int wave) {
+  v = wave_sum(v);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & (kWave - 1)) == 0) part[wave] = v;
+    __syncthreads();
+    const float* p = part + wave / WPR * WPR;
+    v = p[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) v += p[i];
+  }
+  return v;
+}
+
+template <int WPR>
+__device__ __forceinline__ float row_max(float v, float* part, int wave) {
+  v = wave_max(v);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & (kWave - 1)) == 0) part[wave] = v;
+    __syncthreads();
+    const float* p = part + wave / WPR * WPR;
+    v = p[0];
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) v = fmaxf(v, p[i]);
+  }
+  return v;
+}
+
+// WPR waves share a row, each lane holding NV chunks of it; a block has at
+// least four waves, so it takes 4 / WPR rows when a row needs fewer.
+constexpr int block_waves(int WPR) { return WPR < 4 ? 4 : WPR; }
+
+template <int DT, int WPR, int NV, bool Q8>
+__global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormArgs a) {
+  using R = Row<DT>;
+  using elem = typename R::elem;
+  constexpr int kRows = block_waves(WPR) / WPR;
+  __shared__ float part[4][block_waves(WPR)];
+  const int wave = uniform((int)threadIdx.x / kWave);
+  const int lane = (int)threadIdx.x & (kWave - 1);
+  const int first = (wave % WPR) * kWave + lane;   // the lane's first chunk of its row
+  const int C = a.H / 8;
+  int parity = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows, parity ^= 1) {
+    const int64_t row = base + wave / WPR;
+    const bool live = row < a.T;
+    const elem* x = static_cast<const elem*>(a.x) + row * a.x_stride;
+    const elem* res = static_cast<const elem*>(a.residual) + row * a.residual_stride;
+    elem* out = static_cast<elem*>(a.residual_out) + row * a.residual_out_stride;
+    floatx8 v[NV];
+    float sq = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * WPR * kWave;
+      v[i] = floatx8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (!live || c >= C) continue;
+      v[i] = R::wide(R::load(x + 8 * c));
+      if (a.residual) {
+        v[i] += R::wide(R::load(res + 8 * c));
+        if (a.residual_out) R::store(out + 8 * c, R::narrow(v[i]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[i][j], v[i][j], sq);
+    sq = row_sum<WPR>(sq, part[parity], wave);
+    const float rstd = rsqrtf(sq / (float)a.H + a.eps);
+    const elem* g = static_cast<const elem*>(a.weight);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * WPR * kWave;
+      if (c < C) v[i] = v[i] * rstd * R::wide(R::load(g + 8 * c));
+    }
+    if constexpr (!Q8) {
+      elem* y = static_cast<elem*>(a.y) + row * a.y_stride;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = first + i * WPR * kWave;
+        if (live && c < C) R::store(y + 8 * c, R::narrow(v[i]));
+      }
+    } else {
+      // A NaN or an infinity counts as infinity, so it shows in the group's maximum.
+      float m[NV], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        m[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = __builtin_fabsf(v[i][j]);
+          m[i] = t < INFINITY ? fmaxf(m[i], t) : INFINITY;
+        }
+        if (a.group) m[i] = row16_max(m[i]);   // 16 chunks of 8: one group of 128
+        top = fmaxf(top, m[i]);
+      }
+      if (!a.group) top = row_max<WPR>(top, part[2 + parity], wave);
+      uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.y_stride;
+      const int groups = a.group ? (a.H + kNormGroup - 1) / kNormGroup : 1;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = first + i * WPR * kWave;
+        if (!live || c >= C) continue;
+        const float most = a.group ? m[i] : top;
+        const bool finite = most < INFINITY;
+        const float scale = finite ? fmaxf(most / kE4m3Max, kScaleMin) : __builtin_nanf("");
+        const float inv = 1.f / scale;
+        uint32_t lo = 0x7F7F7F7Fu, hi = 0x7F7F7F7Fu;
+        if (finite) {
+          floatx8 q;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(v[i][j] * inv, -kE4m3Max), kE4m3Max);
+          int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+          lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], p, true);
+          p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+          hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], p, true);
+        }
+        *reinterpret_cast<uint2*>(y + 8 * c) = make_uint2(lo, hi);
+        if (a.group ? (c % (kNormGroup / 8) == 0) : c == 0)
+          a.scale[row * groups + (a.group ? c / (kNormGroup / 8) : 0)] = scale;
+      }
+    }
+  }
+}
+
+template <int DT, int WPR, int NV, bool Q8>
+hipError_t run_norm(const NormArgs& a, hipStream_t s) {
+  constexpr int kRows = block_waves(WPR) / WPR;
+  const unsigned want = ((unsigned)a.T + kRows - 1) / kRows;
+  hipLaunchKernelGGL((rmsnorm_kernel<DT, WPR, NV, Q8>), dim3(want < kMaxGrid ? want : kMaxGrid),
+                     dim3(block_waves(WPR) * kWave), 0, s, a);
+  return hipGetLastError();
+}
+
+// Few rows: a row over as many waves as it has chunks for, so each lane waits
+// for one load.  Many rows: four chunks a lane, so a row takes few waves.
+template <int DT, bool Q8>
+hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
+  const int C = a.H / 8;
+  if (a.T <= kNormFewRows) {
+    if (C <= 64) return run_norm<DT, 1, 1, Q8>(a, s);
+    if (C <= 128) return run_norm<DT, 2, 1, Q8>(a, s);
+    if (C <= 256) return run_norm<DT, 4, 1, Q8>(a, s);
+    if (C <= 512) return run_norm<DT, 8, 1, Q8>(a, s);
+    if (C <= 1024) return run_norm<DT, 16, 1, Q8>(a, s);
+    if (C <= 2048) return run_norm<DT, 16, 2, Q8>(a, s);
+    return run_norm<DT, 16, 4, Q8>(a, s);
+  }
+  if (C <= 64) return run_norm<DT, 1, 1, Q8>(a, s);
+  if (C <= 128) return run_norm<DT, 1, 2, Q8>(a, s);
+  if (C <= 256) return run_norm<DT, 1, 4, Q8>(a, s);
+  if (C <= 512) return run_norm<DT, 2, 4, Q8>(a, s);
+  if (C <= 1024) return run_norm<DT, 4, 4, Q8>(a, s);
+  if (C <= 2048) return run_norm<DT, 8, 4, Q8>(a, s);
+  return run_norm<DT, 16, 4, Q8>(a, s);
+}
+
+// Gradient.  With s = 1 / sqrt(mean r^2 + eps) and d = sum_h g_h dy_h r_h:
+//   dx_i = s (g_i dy_i - r_i s^2 d / H) + dresidual_i
+//   dg_i = sum over rows of dy_i r_i s
+// dx is the gradient of x and of the residual alike.  s is computed again from
+// r (both sums in the same pass), so the forward keeps nothing but its
+// residual output.  A block walks every gridDim-th group of rows and keeps its
+// share of dg in registers; the shares meet in a second kernel, in a fixed
+// order.
+template <int DT, int WPR, int NV>
+__global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(NormGradArgs a) {
+  using R = Row<DT>;
+  using elem = typename R::elem;
+  constexpr int kRows = block_waves(WPR) / WPR;
+  __shared__ float part[2][2][block_waves(WPR)];
+  const int wave = uniform((int)threadIdx.x / kWave);
+  const int lane = (int)threadIdx.x & (kWave - 1);
+  const int first = (wave % WPR) * kWave + lane;
+  const int C = a.H / 8;
+  const floatx8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  floatx8 g[NV], dg[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * WPR * kWave;
+    dg[i] = zero;
+    g[i] = c < C ? R::wide(R::load(static_cast<const elem*>(a.weight) + 8 * c)) : zero;
+  }
+  int parity = 0;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows, parity ^= 1) {
+    const int64_t row = base + wave / WPR;
+    const bool live = row < a.T;
+    const elem* dy = static_cast<const elem*>(a.dy) + row * a.dy_stride;
+    const elem* rr = static_cast<const elem*>(a.r) + row * a.r_stride;
+    const elem* dres = static_cast<const elem*>(a.dresidual) + row * a.dresidual_stride;
+    elem* dx = static_cast<elem*>(a.dx) + row * a.dx_stride;
+    floatx8 r[NV], d[NV], add[NV];
+    float sq = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * WPR * kWave;
+      const bool in = live && c < C;
+      r[i] = in ? R::wide(R::load(rr + 8 * c)) : zero;
+      d[i] = in ? R::wide(R::load(dy + 8 * c)) : zero;
+      add[i] = in && a.dresidual ? R::wide(R::load(dres + 8 * c)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sq = __builtin_fmaf(r[i][j], r[i][j], sq);
+        dot = __builtin_fmaf(g[i][j] * d[i][j], r[i][j], dot);
+      }
+    sq = wave_sum(sq);
+    dot = wave_sum(dot);
+    if constexpr (WPR > 1) {
+      if (lane == 0) {
+        part[parity][0][wave] = sq;
+        part[parity][1][wave] = dot;
+      }
+      __syncthreads();
+      const int w0 = wave / WPR * WPR;
+      sq = part[parity][0][w0];
+      dot = part[parity][1][w0];
+#pragma unroll
+      for (int i = 1; i < WPR; ++i) {
+        sq += part[parity][0][w0 + i];
+        dot += part[parity][1][w0 + i];
+      }
+    }
+    const float rstd = rsqrtf(sq / (float)a.H + a.eps);
+    const float f = rstd * rstd * dot / (float)a.H;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * WPR * kWave;
+      if (!live || c >= C) continue;
+      R::store(dx + 8 * c, R::narrow(rstd * (g[i] * d[i] - r[i] * f) + add[i]));
+      dg[i] += d[i] * r[i] * rstd;
+    }
+  }
+  if (!a.part) return;
+  float* p = a.part + ((size_t)blockIdx.x * kRows + wave / WPR) * a.H;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * WPR * kWave;
+    if (c < C) Row<PW_F32>::store(p + 8 * c, dg[i]);
+  }
+}
+
+// dg = the sum of `n` partial rows: a block takes 16 columns, 64 threads of
+// four lanes apiece share the rows, and LDS joins them in a fixed order.
+__global__ __launch_bounds__(256) void join_rows_kernel(const float* __restrict__ part, int n, int H,
+                                                        float* __restrict__ out) {
+  __shared__ floatx4 sums[64][4];
+  const int q = (int)threadIdx.x & 3, rg = (int)threadIdx.x >> 2;
+  const int col = (int)blockIdx.x * 16 + 4 * q;
+  floatx4 s = {0.f, 0.f, 0.f, 0.f};
+  if (col < H)
+    for (int i = rg; i < n; i += 64) s += *reinterpret_cast<const floatx4*>(part + (size_t)i * H + col);
+  sums[rg][q] = s;
+  __syncthreads();
+  for (int w = 32; w > 0; w >>= 1) {
+    if (rg < w) sums[rg][q] += sums[rg + w][q];
+    __syncthreads();
+  }
+  if (rg == 0 && col < H) *reinterpret_cast<floatx4*>(out + col) = sums[0][q];
+}
+
+template <int DT, int WPR, int NV>
+hipError_t run_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) {
+  constexpr int kRows = block_waves(WPR) / WPR;
+  const unsigned want = ((unsigned)a.T + kRows - 1) / kRows;
+  const unsigned grid = want < (unsigned)kNormGradBlocks ? want : (unsigned)kNormGradBlocks;
+  hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, WPR, NV>), dim3(grid), dim3(block_waves(WPR) * kWave), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !dweight) return e;
+  hipLaunchKernelGGL(join_rows_kernel, dim3((a.H + 15) / 16), dim3(256), 0, s, a.part, (int)(grid * kRows), a.H,
+                     dweight);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t pick_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) {
+  const int C = a.H / 8;
+  if (C <= 64) return run_norm_grad<DT, 1, 1>(a, dweight, s);
+  if (C <= 256) return run_norm_grad<DT, 4, 1>(a, dweight, s);
+  if (C <= 512) return run_norm_grad<DT, 4, 2>(a, dweight, s);
+  if (C <= 1024) return run_norm_grad<DT, 16, 1>(a, dweight, s);
+  if (C <= 2048) return run_norm_grad<DT, 16, 2>(a, dweight, s);
+  return run_norm_grad<DT, 16, 4>(a, dweight, s);
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormArgs& a, int dtype, bool e4m3, hipStream_t s) {
+  switch (dtype) {
+    case PW_F32: return e4m3 ? pick_norm<PW_F32, true>(a, s) : pick_norm<PW_F32, false>(a, s);
+    case PW_F16: return e4m3 ? pick_norm<PW_F16, true>(a, s) : pick_norm<PW_F16, false>(a, s);
+    case PW_BF16: return e4m3 ? pick_norm<PW_BF16, true>(a, s) : pick_norm<PW_BF16, false>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, hipStream_t s) {
+  switch (dtype) {
+    case PW_F32: return pick_norm_grad<PW_F32>(a, dweight, s);
+    case PW_F16: return pick_norm_grad<PW_F16>(a, dweight, s);
+    case PW_BF16: return pick_norm_grad<PW_BF16>(a, dweight, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace pw

@@ -28,41 +28,6 @@ namespace pw {
 constexpr int kRouterTokens = 4;     // tokens per workgroup for batches above 256 tokens
 constexpr int kRouterWaves = 16;     // waves per workgroup
 
-// Wave-wide sum and max in DPP: inside each 16-lane row, partners lane ^ 1,
-// lane ^ 2, then the mirror inside 8 lanes and inside 16 lanes (each pairing
-// is symmetric, so every lane of a row ends with the same bits); then the four
-// rows' values read out of lanes 0, 16, 32, 48 and combined the same way in
-// every lane.  All 64 lanes must be active.  A shuffle-based butterfly (one
-// LDS permute per step) made the router's top-k rounds a chain of permutes.
-template <int CTRL>
-__device__ __forceinline__ float dpp_row(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
-}
-constexpr int kQuadXor1 = 0xB1;      // quad_perm [1,0,3,2]
-constexpr int kQuadXor2 = 0x4E;      // quad_perm [2,3,0,1]
-constexpr int kHalfRowMirror = 0x141;
-constexpr int kRowMirror = 0x140;
-
-__device__ __forceinline__ float row_lane(float v, int l) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-  v += dpp_row<kQuadXor1>(v);
-  v += dpp_row<kQuadXor2>(v);
-  v += dpp_row<kHalfRowMirror>(v);
-  v += dpp_row<kRowMirror>(v);
-  return (row_lane(v, 0) + row_lane(v, 16)) + (row_lane(v, 32) + row_lane(v, 48));
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-  v = fmaxf(v, dpp_row<kQuadXor1>(v));
-  v = fmaxf(v, dpp_row<kQuadXor2>(v));
-  v = fmaxf(v, dpp_row<kHalfRowMirror>(v));
-  v = fmaxf(v, dpp_row<kRowMirror>(v));
-  return fmaxf(fmaxf(row_lane(v, 0), row_lane(v, 16)), fmaxf(row_lane(v, 32), row_lane(v, 48)));
-}
-
 // Selection and softmax of token t from its logits l[e] (e < E; lane owns
 // e = lane + 64 i, E <= 256): k rounds of a wave-wide max over the live
 // logits, the lowest expert id holding it found by ballot (so equal logits

@@ -330,6 +330,160 @@ pw_status pw_moe_forward_layers(const pw_moe_shape* shape /* host */, int32_t L,
                                 const pw_moe_options* opts, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Around the layer: the norm in front of it, tokens sorted by expert and back
+ * with their weights, and the gradients, of the router too.
+ *
+ * Rows.  A matrix is T rows of H elements, its rows `*_stride` ELEMENTS apart;
+ * elements are of one of the types below.  The first row and the stride are
+ * 16-byte aligned (8-byte for the stride of an 8-bit output of the norm), else
+ * PW_ERR_ALIGNMENT.  An input's stride may be anything from 0 on, a written
+ * matrix's rows must not overlap (else PW_ERR_INVALID_ARG).  A null pointer
+ * that the comment does not allow, a negative size or an unknown type is
+ * PW_ERR_INVALID_ARG.  Unless a comment says that two arguments may be the
+ * same, what a call writes must overlap nothing else that it reads or writes.
+ *
+ * Sums, means and gradients of weights are fp32; an output is rounded once, to
+ * nearest even.  Every call is deterministic, allocates nothing, can be
+ * captured into a graph, and leaves what it does not write as it was.  Inputs
+ * that hold NaN or infinities give what the formula gives.  A workspace is
+ * 256-byte aligned and needs no initialisation; calls that may overlap in time
+ * (two streams, two captured graphs) need workspaces of their own.
+ * ---------------------------------------------------------------------- */
+#define PW_F32  0
+#define PW_F16  1
+#define PW_BF16 2
+#define PW_E4M3 3   /* 8 bits: 4 of exponent, 3 of mantissa, largest 448, no infinity */
+
+/* Root-mean-square norm with the residual's addition.
+ *     r = x + residual                       (r = x if residual is NULL)
+ *     y = r * weight / sqrt(mean_h r_h^2 + eps)
+ *   H             a multiple of 8, at most 32768 (else PW_ERR_UNSUPPORTED_SHAPE)
+ *   dtype         PW_F32, PW_F16 or PW_BF16: x, residual, residual_out, weight
+ *   residual_out  receives r rounded to dtype; may be NULL (r is not stored)
+ *                 and must be without residual; may be residual or x itself
+ *                 (same pointer and stride).  y is computed from the fp32 sum.
+ *   weight        dtype [H]
+ *   eps           0 .. 1e30
+ *   y_dtype       dtype, or PW_E4M3: then y holds codes and
+ *                     y_value = code * scale,
+ *                     scale = max(largest |y| of the group / 448, 2^-100),
+ *                 scale fp32 [T][groups], groups = 1 for group 0 (one scale a
+ *                 row) or ceil(H / 128) for group 128.  A group that holds a
+ *                 NaN or an infinity gets the scale NaN and NaN codes.
+ *                 Otherwise scale is NULL and group 0.  y may be x itself if
+ *                 they have the same type and stride.
+ * One launch.  T == 0 returns PW_OK and enqueues nothing. */
+pw_status pw_rmsnorm(int32_t T, int32_t H, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                     int64_t residual_stride, void* residual_out, int64_t residual_out_stride, const void* weight,
+                     float eps, int32_t y_dtype, void* y, int64_t y_stride, float* scale, int32_t group, void* stream);
+
+/* Workspace of pw_rmsnorm_backward for up to T_max rows (0 on a bad size). */
+size_t pw_rmsnorm_backward_workspace_bytes(int32_t T_max, int32_t H);
+
+/* Gradient of pw_rmsnorm (y in dtype).  With s = 1 / sqrt(mean_h r_h^2 + eps):
+ *     dx      = s (weight dy - r s^2 mean_h(weight dy r)) + dresidual
+ *     dweight = sum over rows of dy r s
+ *   dy         dtype [T][H]: gradient of y
+ *   r          dtype [T][H]: the forward's residual_out (x without a residual)
+ *   dresidual  dtype [T][H] or NULL: gradient that reaches r by the residual
+ *              stream
+ *   dx         dtype [T][H], overwritten: the gradient of x and of residual;
+ *              may be dy, r or dresidual itself (same pointer and stride)
+ *   dweight    fp32 [H], 16-byte aligned, overwritten (zero for T == 0); NULL:
+ *              not wanted, and then no workspace is
+ * Two launches (one without dweight). */
+pw_status pw_rmsnorm_backward(int32_t T, int32_t H, int32_t dtype, const void* dy, int64_t dy_stride, const void* r,
+                              int64_t r_stride, const void* weight, float eps, const void* dresidual,
+                              int64_t dresidual_stride, void* dx, int64_t dx_stride, float* dweight, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Workspace of pw_moe_permute for up to T_max tokens (0 on a bad shape). */
+size_t pw_moe_permute_workspace_bytes(const pw_moe_shape* shape /* host */, int32_t T_max);
+
+/* Tokens sorted by expert: slot s = t*k + j gets a place inv[s], the slots of
+ * expert 0 first, then those of expert 1, ..., each expert's in slot order, and
+ *     xs[inv[t*k + j]] = x[t]
+ * for callers that run products of their own on an expert's tokens, send them
+ * to other GPUs or collect them to measure a block's sensitivity.
+ *   shape    host; hidden, num_experts and top_k are used
+ *   dtype    PW_F32, PW_F16, PW_BF16 or PW_E4M3: x [T][H] and xs [T*k][H]
+ *   x_scale  fp32 [T][groups], moved along to xs_scale fp32 [T*k][groups];
+ *            both NULL with groups 0
+ *   ids      int32 [T][k].  An id outside [0, E) drops its slot: inv -1,
+ *            nothing is written for it (and PW_DEV_BAD_EXPERT_ID is raised in
+ *            status).  A token may list an expert more than once.
+ *   offsets  int32 [E+1]: expert e has the rows [offsets[e], offsets[e+1]);
+ *            rows from offsets[E] on are left as they were
+ *   inv      int32 [T*k];  perm  int32 [T*k] or NULL: perm[inv[s]] = s, from
+ *            offsets[E] on left as it was
+ *   status   device uint32 or NULL: PW_DEV_* bits are OR-ed into it
+ * One launch for up to 4096 slots, two above.  T == 0 sets offsets to zero. */
+pw_status pw_moe_permute(const pw_moe_shape* shape /* host */, int32_t T, int32_t dtype, const void* x,
+                         int64_t x_stride, const float* x_scale, int32_t groups, const int32_t* ids, void* xs,
+                         int64_t xs_stride, float* xs_scale, int32_t* offsets, int32_t* inv, int32_t* perm,
+                         uint32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of pw_moe_permute: dx[t] = sum_j dxs[inv[t*k + j]] (dropped slots
+ * add nothing).  dtype PW_F32, PW_F16 or PW_BF16.  One launch. */
+pw_status pw_moe_permute_backward(const pw_moe_shape* shape /* host */, int32_t T, int32_t dtype, const void* dxs,
+                                  int64_t dxs_stride, const int32_t* inv, void* dx, int64_t dx_stride, void* stream);
+
+/* Back from the experts: y[t] = sum_j w[t][j] rows[inv[t*k + j]], summed in the
+ * order of j; zero for a token without a kept slot.
+ *   dtype  PW_F32, PW_F16 or PW_BF16: rows [T*k][H], y [T][H]
+ *   inv    as pw_moe_permute wrote it; an entry outside [0, T*k) is a dropped slot
+ *   w      fp32 [T][k], used as given; NULL: ones
+ * One launch; T == 0 returns PW_OK and enqueues nothing. */
+pw_status pw_moe_unpermute(const pw_moe_shape* shape /* host */, int32_t T, int32_t dtype, const void* rows,
+                           int64_t rows_stride, const int32_t* inv, const float* w, void* y, int64_t y_stride,
+                           void* stream);
+
+/* Gradient of pw_moe_unpermute:
+ *     drows[inv[t*k + j]] = w[t][j] dy[t],   dw[t][j] = <dy[t], rows[inv[t*k + j]]>
+ *   dw    fp32 [T][k], zero for dropped slots; NULL: not wanted (rows may be
+ *         NULL then)
+ *   drows may be rows itself (same pointer and stride); no two slots may share
+ *         a place
+ * One launch. */
+pw_status pw_moe_unpermute_backward(const pw_moe_shape* shape /* host */, int32_t T, int32_t dtype, const void* dy,
+                                    int64_t dy_stride, const void* rows, int64_t rows_stride, const int32_t* inv,
+                                    const float* w, void* drows, int64_t drows_stride, float* dw, void* stream);
+
+/* Workspace of pw_router_backward for up to T_max tokens (0 on a bad shape). */
+size_t pw_router_backward_workspace_bytes(const pw_moe_shape* shape /* host */, int32_t T_max);
+
+/* Gradient of pw_router_topk with the selection held fixed: w[t] is the
+ * softmax of token t's selected logits, so
+ *     dl[t][j]      = w[t][j] (dw[t][j] - sum_i w[t][i] dw[t][i])
+ *     dx[t]         = dx_add[t] + sum_j dl[t][j] router_w[ids[t][j]]
+ *     drouter_w[e]  = sum over the slots of expert e of dl[t][j] x[t]
+ *   x, router_w, ids, w  as pw_router_topk took and wrote them (k <= 64); a
+ *              slot whose id is outside [0, E) takes no part
+ *   dw         fp32 [T][k]: gradient of w (as pw_moe_unpermute_backward writes)
+ *   dx_add     fp16 [T][H] or NULL: gradient that reaches x by other ways (as
+ *              pw_moe_permute_backward writes)
+ *   dx         fp16 [T][H], overwritten; may be dx_add itself
+ *   drouter_w  fp32 [E][H], 16-byte aligned, overwritten (zero for T == 0)
+ * Three launches. */
+pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, const uint16_t* x,
+                             const uint16_t* router_w, const int32_t* ids, const float* w, const float* dw,
+                             const uint16_t* dx_add, uint16_t* dx, float* drouter_w, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The routed half of a transformer block: norm, router and layer in one call,
+ *     residual += x;   y = layer(pw_rmsnorm(residual))
+ * The next norm's residual addition adds y.  Equal bit for bit to pw_rmsnorm
+ * (fp16, in place on residual) followed by pw_moe_forward_routed on its output.
+ *   x         fp16 [T][H];  residual  fp16 [T][H], updated;  norm_w  fp16 [H]
+ *   y         fp16 [T][H], overwritten; may be x
+ *   the rest  as for pw_rmsnorm and pw_moe_forward_routed */
+pw_status pw_moe_forward_block(const pw_moe_shape* shape /* host */, int32_t T, const uint16_t* x, uint16_t* residual,
+                               const uint16_t* norm_w, float eps, const uint16_t* router_w,
+                               const pw_block_desc* blocks, const uint8_t* q, uint16_t* y, uint32_t* stat_count,
+                               float* stat_mass, void* workspace, size_t workspace_bytes, const pw_moe_options* opts,
+                               void* stream);
+
+/* ------------------------------------------------------------------------
  * Quality-aware bitwidth planner (host code; "Technical summary: PagedWeight",
  * Core components 2: offline sensitivity per block, online routing statistics
  * with hot experts protected by higher floors and damage multipliers, a

@@ -1,0 +1,732 @@
+"""The operators around the layer on the GPU, against their 64-bit definitions.
+
+Tolerances.  U = 2^-24 is half a step of fp32.  Every result is computed in fp32
+and rounded once, so it may be off by half a step of its type relative to its
+value (plus half a subnormal step), and by U times the length of the longest
+chain of additions times the sum of the addends' magnitudes.  Chains: a row's
+sums add at most 32 values a lane, then 6 levels of a wave and 15 waves, so 64
+covers them with the few factors' roundings; the others are stated where used.
+Copies and whole numbers are equal.  Every case prints what it runs first.
+"""
+import sys
+
+import numpy as np
+import pytest
+
+import oracle.ops_oracle as oo
+import oracle.pagedweight_oracle as orc
+from any_precision_bitplane_amd import binding as B
+from any_precision_bitplane_amd import synth
+from any_precision_bitplane_amd.device import DeviceLayer
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+ROW = 64
+EPS = 1e-5
+DEV = "cuda:0"
+DTYPES = ["f32", "f16", "bf16"]
+
+
+def say(msg):
+    print(msg, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch as _t
+    if not _t.cuda.is_available():
+        pytest.fail("GPU tests need a GPU")
+    B.load()
+    return _t
+
+
+def dtype_of(torch, name):
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[name]
+
+
+def half_step(torch, name):
+    """(relative, absolute) half steps of a row type."""
+    f = torch.finfo(dtype_of(torch, name))
+    return f.eps / 2, f.smallest_normal * f.eps / 2
+
+
+def f64(t):
+    return t.detach().cpu().to(__import__("torch").float32).double().numpy()
+
+
+def rand(torch, seed, shape, name, std=1.0, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    a = torch.randn((*shape[:-1], shape[-1] + pad), generator=g) * std
+    return a.to(dtype_of(torch, name)).to(DEV)[..., :shape[-1]]
+
+
+def near(got, ref, allowed, what):
+    err = np.abs(got - ref)
+    assert np.all(np.isfinite(got)), what
+    over = err - allowed
+    worst = float(np.max(err / np.maximum(allowed, 1e-300))) if err.size else 0.0
+    say(f"  {what}: max abs {float(err.max()) if err.size else 0.0:.3e}, {worst:.2f} of what is allowed")
+    assert not err.size or over.max() <= 0, (what, worst)
+
+
+# ----- norm -----------------------------------------------------------------
+
+NORM_SIZES = [(1, 8), (3, 64), (5, 520), (1, 2048), (2, 4104), (7, 8192), (2, 16384), (1, 32768),
+              (1025, 64), (1030, 520), (1027, 1000), (1026, 2080), (1025, 4096), (1025, 8200), (1025, 16392),
+              (1025, 24576)]
+
+
+@pytest.mark.parametrize("name", DTYPES)
+@pytest.mark.parametrize("T,H", NORM_SIZES, ids=[f"{t}x{h}" for t, h in NORM_SIZES])
+def test_rmsnorm(torch, T, H, name):
+    say(f"rmsnorm {name} T={T} H={H}")
+    x, res = rand(torch, 1, (T, H), name, pad=8), rand(torch, 2, (T, H), name, 4.0)
+    g = rand(torch, 3, (1, H), name)[0]
+    out, y = torch.full_like(res, 7.0), torch.full((T, H + 16), 7.0, dtype=res.dtype, device=DEV)
+    B.pw_rmsnorm(T, H, x, g, EPS, y[:, :H], residual=res, residual_out=out)
+    plain = torch.full_like(res, 7.0)
+    B.pw_rmsnorm(T, H, x, g, EPS, plain)
+    torch.cuda.synchronize()
+    rel, ab = half_step(torch, name)
+    assert torch.equal(out, (x.float() + res.float()).to(res.dtype))
+    assert bool((y[:, H:] == 7.0).all())
+    for got, ref, what in [(y[:, :H], oo.rmsnorm(f64(x), f64(g), EPS, f64(res))[1], "y"),
+                           (plain, oo.rmsnorm(f64(x), f64(g), EPS)[1], "y without a residual")]:
+        near(f64(got), ref, np.abs(ref) * (rel + ROW * U) + ab, what)
+
+
+@pytest.mark.parametrize("name", DTYPES)
+@pytest.mark.parametrize("T,H,group", [(1, 64, 0), (1, 64, 128), (3, 136, 128), (5, 2048, 128), (4, 2080, 0),
+                                       (2, 32768, 0), (1, 32768, 128), (1030, 520, 128), (1025, 4096, 0),
+                                       (1025, 8200, 128), (1025, 16384, 0)])
+def test_rmsnorm_e4m3(torch, T, H, group, name):
+    say(f"rmsnorm e4m3 {name} T={T} H={H} group={group}")
+    x, res = rand(torch, 1, (T, H), name), rand(torch, 2, (T, H), name, 4.0, pad=8)
+    g = rand(torch, 3, (1, H), name)[0]
+    x[0, :min(H, 128)] = 0
+    res[0, :min(H, 128)] = 0                       # a group of zeros (a whole row of them where H <= 128)
+    groups = -(-H // 128) if group else 1
+    out = torch.empty_like(x)
+    y = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.full((T, groups), -1.0, device=DEV)
+    B.pw_rmsnorm(T, H, x, g, EPS, y, residual=res, residual_out=out, scale=scale, group=group)
+    torch.cuda.synchronize()
+    assert torch.equal(out, (x.float() + res.float()).to(x.dtype))
+    ref = oo.rmsnorm(f64(x), f64(g), EPS, f64(res))[1]
+    rs = oo.e4m3_scales(ref, group)
+    near(f64(scale), rs, rs * (ROW + 2) * U, "scale")
+    wide = np.repeat(f64(scale), group if group else H, axis=1)[:, :H]
+    # half a step of e4m3 (2^-4 of the value, 2^-10 of the scale below its normal numbers), and the fp32 work before it
+    near(f64(y) * wide, ref, np.maximum(np.abs(ref) * 2.0 ** -4, wide * 2.0 ** -10) + (np.abs(ref) + wide) * 2 * ROW * U,
+         "code * scale")
+    assert np.max(np.abs(f64(y))) == (448.0 if ref.any() else 0.0)
+
+
+def test_rmsnorm_in_place_and_special_rows(torch):
+    say("rmsnorm: sum and output in place, rows with NaN, infinity, zeros, largest and smallest values")
+    T, H = 6, 512
+    x, res = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (T, H), "f16")
+    g = rand(torch, 3, (1, H), "f16")[0]
+    out, y = torch.empty_like(x), torch.empty_like(x)
+    B.pw_rmsnorm(T, H, x, g, EPS, y, residual=res, residual_out=out)
+    x2, res2 = x.clone(), res.clone()
+    B.pw_rmsnorm(T, H, x2, g, EPS, x2, residual=res2, residual_out=res2)      # y over x, r over residual
+    x3 = x.clone()
+    B.pw_rmsnorm(T, H, x3, g, EPS, y3 := torch.empty_like(x), residual=res, residual_out=x3)   # r over x
+    assert torch.equal(x2, y) and torch.equal(res2, out) and torch.equal(x3, out) and torch.equal(y3, y)
+
+    x[0, 5], x[1, 7], x[2], x[3], x[4] = float("nan"), float("inf"), 0.0, 65504.0, 2.0 ** -24
+    codes = torch.zeros((T, H), dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.empty((T, 4), device=DEV)
+    B.pw_rmsnorm(T, H, x, g, EPS, y)
+    B.pw_rmsnorm(T, H, x, g, EPS, codes, scale=scale, group=128)
+    torch.cuda.synchronize()
+    assert bool(y[0].isnan().all())
+    assert bool(y[1, 7].isnan()) and bool((y[1, 8:] == 0).all())
+    assert bool((y[2] == 0).all()) and bool((scale[2] == 2.0 ** -100).all()) and bool((codes[2].float() == 0).all())
+    assert bool(scale[0].isnan().all()) and bool(codes[0].float().isnan().all())
+    assert bool(scale[1, 0].isnan()) and bool(codes[1, :128].float().isnan().all())
+    assert bool((scale[1, 1:] == 2.0 ** -100).all()) and bool((codes[1, 128:].float() == 0).all())
+    for t in (3, 4, 5):
+        ref = oo.rmsnorm(f64(x[t:t + 1]), f64(g), EPS)[1]
+        near(f64(y[t:t + 1]), ref, np.abs(ref) * (2.0 ** -11 + ROW * U) + 2.0 ** -25, f"row {t}")
+
+
+GRAD_SIZES = [(1, 8), (3, 64), (2, 32768), (5, 8200), (700, 4096), (2500, 520), (1025, 2080), (513, 8192), (514, 16384),
+              (515, 24576), (3000, 512)]
+
+
+@pytest.mark.parametrize("name", DTYPES)
+@pytest.mark.parametrize("T,H", GRAD_SIZES, ids=[f"{t}x{h}" for t, h in GRAD_SIZES])
+def test_rmsnorm_backward(torch, T, H, name):
+    say(f"rmsnorm_backward {name} T={T} H={H}")
+    dy, r = rand(torch, 1, (T, H), name, 0.1, pad=8), rand(torch, 2, (T, H), name, 3.0)
+    g, dres = rand(torch, 3, (1, H), name)[0], rand(torch, 4, (T, H), name, 0.1, pad=16)
+    ws = torch.full((B.pw_rmsnorm_backward_workspace_bytes(T, H),), 255, dtype=torch.uint8, device=DEV)
+    dx, dg = torch.empty_like(r), torch.full((H,), 7.0, device=DEV)
+    B.pw_rmsnorm_backward(T, H, dy, r, g, EPS, dx, dg, ws, dresidual=dres)
+    alone = torch.empty_like(r)
+    B.pw_rmsnorm_backward(T, H, dy, r, g, EPS, alone)
+    over = [dy.clone(), r.clone(), dres.clone()]
+    B.pw_rmsnorm_backward(T, H, over[0], r, g, EPS, over[0], dresidual=dres)
+    B.pw_rmsnorm_backward(T, H, dy, over[1], g, EPS, over[1], dresidual=dres)
+    B.pw_rmsnorm_backward(T, H, dy, r, g, EPS, over[2], dresidual=over[2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, dx) for o in over)
+    d, rr, gg, a = f64(dy), f64(r), f64(g), f64(dres)
+    rel, ab = half_step(torch, name)
+    s = 1 / np.sqrt(np.mean(rr * rr, axis=1, keepdims=True) + EPS)
+    mag = np.abs(s * gg * d) + np.abs(rr) * s ** 3 * np.sum(np.abs(gg * d * rr), axis=1, keepdims=True) / H
+    for got, add, what in [(dx, a, "dx"), (alone, np.zeros_like(a), "dx without the stream's gradient")]:
+        ref, dgr = oo.rmsnorm_backward(d, rr, gg, EPS, add)
+        near(f64(got), ref, np.abs(ref) * rel + ab + 2 * ROW * U * (mag + np.abs(add)), what)
+    # shares of at most ceil(T / 512) rows each, then at most 2048 shares: 32 a thread and six levels
+    chain = -(-T // 512) + 32 + 6 + ROW
+    near(f64(dg), dgr, chain * U * np.sum(np.abs(d * rr * s), axis=0), "dweight")
+
+
+def test_rmsnorm_backward_against_differences(torch):
+    say("rmsnorm_backward: central differences of the fp32 forward")
+    T, H, h = 3, 64, 2.0 ** -7
+    r, dy, g = rand(torch, 1, (T, H), "f32"), rand(torch, 2, (T, H), "f32"), rand(torch, 3, (1, H), "f32")[0]
+    ws = torch.empty(B.pw_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=DEV)
+    dx, dg = torch.empty_like(r), torch.empty(H, device=DEV)
+    B.pw_rmsnorm_backward(T, H, dy, r, g, EPS, dx, dg, ws)
+
+    def loss(a, b):
+        y = torch.empty_like(a)
+        B.pw_rmsnorm(T, H, a, b, EPS, y)
+        return float((y.double() * dy.double()).sum())
+
+    # |y| <= ~4, so a difference carries 2 * 192 * 4 * 64 U / (2 h) ~ 0.4 at the very worst and about 1e-4 as roundings
+    # fall; the second-order term of the difference is h^2 |y'''| / 6 ~ 1e-5 times |dy|
+    for t, c in [(0, 0), (1, 17), (2, 63)]:
+        up, down = r.clone(), r.clone()
+        up[t, c] += h
+        down[t, c] -= h
+        assert abs((loss(up, g) - loss(down, g)) / (2 * h) - float(dx[t, c])) < 5e-3
+        up, down = g.clone(), g.clone()
+        up[c] += h
+        down[c] -= h
+        assert abs((loss(r, up) - loss(r, down)) / (2 * h) - float(dg[c])) < 5e-3
+
+
+def test_rmsnorm_backward_of_no_rows(torch):
+    say("rmsnorm_backward: T = 0 clears dweight")
+    e = torch.empty((0, 64), device=DEV)
+    dg = torch.full((64,), 7.0, device=DEV)
+    B.pw_rmsnorm_backward(0, 64, e, e, torch.ones(64, device=DEV), EPS, e, dg)
+    torch.cuda.synchronize()
+    assert bool((dg == 0).all())
+
+
+# ----- sorting ----------------------------------------------------------------
+
+# name, T, H, E, k, share of dropped slots; up to 4096 slots one launch, above two
+SORT_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd", 7, 96, 5, 3, 0.3),
+              ("all_dropped", 9, 64, 8, 2, 1.0), ("E256_k64", 5, 64, 256, 64, 0.1), ("E256_k256", 2, 32, 256, 256, 0.0),
+              ("more_experts_than_tokens", 3, 64, 200, 2, 0.0), ("edge_4096", 1024, 96, 60, 4, 0.1),
+              ("above_4096", 1025, 96, 60, 4, 0.1), ("one_expert", 5000, 64, 1, 1, 0.0), ("large", 4099, 160, 8, 2, 0.05),
+              ("E256_k8", 1500, 64, 256, 8, 0.2), ("E256_k256_large", 40, 32, 256, 256, 0.1),
+              ("all_dropped_large", 5001, 32, 9, 1, 1.0), ("k7", 3001, 64, 33, 7, 0.5)]
+
+
+def draw_ids(seed, T, E, k, dropped):
+    rng = np.random.default_rng(seed)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    lost = rng.random((T, k)) < dropped
+    ids[lost] = rng.choice(np.array([-1, E, 2 ** 31 - 1, -2 ** 31], np.int64), size=int(lost.sum())).astype(np.int32)
+    return ids
+
+
+def plan(ids, E):
+    """(offsets, inv, perm) of the oracle's sort, quickly: the definition is pinned on small inputs."""
+    flat = ids.reshape(-1).astype(np.int64)
+    kept = (flat >= 0) & (flat < E)
+    perm = np.nonzero(kept)[0][np.argsort(flat[kept], kind="stable")]
+    inv = np.full(flat.shape, -1, np.int64)
+    inv[perm] = np.arange(len(perm))
+    return np.concatenate([[0], np.cumsum(np.bincount(flat[kept], minlength=E))]), inv, perm
+
+
+def run_permute(torch, x, ids, E, scale=None, stream=None, ws=None, perm=True, xs_pad=0):
+    T, H = x.shape
+    k = ids.shape[1]
+    S = T * k
+    shp = B.shape(H, 32, E, k)
+    raw = torch.full((S, H + xs_pad), 3, dtype=torch.uint8 if x.element_size() == 1 else x.dtype, device=DEV)
+    xs = raw.view(x.dtype)[:, :H]
+    offsets = torch.full((E + 1,), -9, dtype=torch.int32, device=DEV)
+    inv, pm = (torch.full((S,), -9, dtype=torch.int32, device=DEV) for _ in range(2))
+    xsc = torch.full((S, scale.shape[1]), 3.0, device=DEV) if scale is not None else None
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    if ws is None:
+        ws = torch.full((B.pw_moe_permute_workspace_bytes(shp, T),), 255, dtype=torch.uint8, device=DEV)
+    idd = torch.from_numpy(ids).to(DEV)
+    B.pw_moe_permute(shp, T, x, idd, xs, offsets, inv, pm if perm else None, ws, x_scale=scale, xs_scale=xsc,
+                     status=status, stream=stream)
+    torch.cuda.synchronize()
+    return xs, offsets, inv, pm, xsc, int(status.item()), raw
+
+
+@pytest.mark.parametrize("name,T,H,E,k,dropped", SORT_CASES, ids=[c[0] for c in SORT_CASES])
+def test_permute(torch, name, T, H, E, k, dropped):
+    ids = draw_ids(11, T, E, k, dropped)
+    offsets, inv, perm = plan(ids, E)
+    n = len(perm)
+    if T * k <= 600:
+        o = oo.sort_slots(ids, E)
+        assert all(np.array_equal(a, b) for a, b in zip(o, (offsets, inv, perm)))
+    for dt in DTYPES + ["e4m3"]:
+        say(f"permute {name} {dt} T={T} H={H} E={E} k={k}: {n} of {T * k} slots kept")
+        x = rand(torch, 5, (T, H), dt, pad=16)
+        scale = torch.rand((T, 3), device=DEV) if dt == "e4m3" else None
+        xs, off, iv, pm, xsc, status, raw = run_permute(torch, x, ids, E, scale, xs_pad=16)
+        assert np.array_equal(off.cpu().numpy(), offsets)
+        assert np.array_equal(iv.cpu().numpy(), inv)
+        assert np.array_equal(pm[:n].cpu().numpy(), perm) and bool((pm[n:] == -9).all())
+        assert status == (B.PW_DEV_BAD_EXPERT_ID if n < T * k else 0)
+        bits = lambda t: t.contiguous().view(torch.uint8)
+        tok = torch.from_numpy(perm // k).to(DEV)
+        assert torch.equal(bits(xs[:n]), bits(x).reshape(T, -1)[tok].reshape(bits(xs[:n]).shape))
+        assert bool((raw[n:] == 3).all()) and bool((raw[:, H:] == 3).all())       # left as they were
+        if scale is not None:
+            assert torch.equal(xsc[:n], scale[tok]) and bool((xsc[n:] == 3.0).all())
+    if dropped == 0.0:
+        assert run_permute(torch, x, ids, E, scale, perm=False)[3].eq(-9).all()
+
+
+def test_permute_same_expert_twice(torch):
+    say("permute: tokens that list an expert more than once")
+    for T in (50, 3000):
+        ids = np.random.default_rng(1).integers(0, 3, size=(T, 4)).astype(np.int32)
+        offsets, inv, perm = plan(ids, 4)
+        x = rand(torch, 5, (T, 64), "f16")
+        xs, off, iv, pm, _, status, _ = run_permute(torch, x, ids, 4)
+        assert status == 0 and np.array_equal(off.cpu().numpy(), offsets) and np.array_equal(iv.cpu().numpy(), inv)
+        assert np.array_equal(pm.cpu().numpy(), perm)
+        assert torch.equal(xs, x[torch.from_numpy(perm // 4).to(DEV)])
+
+
+def test_permute_of_no_tokens(torch):
+    say("permute: T = 0 clears the offsets")
+    shp = B.shape(64, 32, 8, 2)
+    e, i = torch.empty((0, 64), device=DEV), torch.empty(0, dtype=torch.int32, device=DEV)
+    off = torch.full((9,), 5, dtype=torch.int32, device=DEV)
+    B.pw_moe_permute(shp, 0, e, i, e, off, i, i, torch.empty(8192, dtype=torch.uint8, device=DEV))
+    B.pw_moe_unpermute(shp, 0, e, i, None, e)
+    torch.cuda.synchronize()
+    assert bool((off == 0).all())
+
+
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("name,T,H,E,k,dropped", SORT_CASES, ids=[c[0] for c in SORT_CASES])
+def test_unpermute_and_gradients(torch, name, T, H, E, k, dropped, dt):
+    say(f"unpermute {name} {dt} T={T} H={H} E={E} k={k}")
+    ids = draw_ids(11, T, E, k, dropped)
+    _, inv, perm = plan(ids, E)
+    S, n = T * k, len(perm)
+    shp = B.shape(H, 32, E, k)
+    iv = torch.from_numpy(inv.astype(np.int32)).to(DEV)
+    rows, dy = rand(torch, 5, (S, H), dt, pad=16), rand(torch, 6, (T, H), dt, 0.1, pad=8)
+    rows[n:] = float("nan")                          # rows without a slot are never read
+    w = rand(torch, 7, (T, k), "f32")
+    y, dx = (torch.full((T, H + 8), 7.0, dtype=dy.dtype, device=DEV) for _ in range(2))
+    drows, dw = torch.full((S, H + 8), 7.0, dtype=dy.dtype, device=DEV), torch.full((T, k), 7.0, device=DEV)
+    B.pw_moe_unpermute(shp, T, rows, iv, w, y[:, :H])
+    B.pw_moe_permute_backward(shp, T, rows, iv, dx[:, :H])
+    B.pw_moe_unpermute_backward(shp, T, dy, rows, iv, w, drows[:, :H], dw)
+    ones, only = torch.full_like(y, 7.0), torch.full_like(drows, 7.0)
+    B.pw_moe_unpermute(shp, T, rows, iv, None, ones[:, :H])
+    B.pw_moe_unpermute_backward(shp, T, dy, None, iv, w, only[:, :H])
+    place = rows.clone()
+    dw2 = torch.empty_like(dw)
+    B.pw_moe_unpermute_backward(shp, T, dy, place, iv, w, place, dw2)             # drows over rows
+    torch.cuda.synchronize()
+    assert torch.equal(ones, dx) and torch.equal(only, drows) and torch.equal(place[:n], drows[:n, :H])
+    assert torch.equal(dw2, dw)
+    assert bool((y[:, H:] == 7).all()) and bool((drows[n:] == 7).all()) and bool((drows[:, H:] == 7).all())
+    rel, ab = half_step(torch, dt)
+    R, W, D = f64(rows), f64(w), f64(dy)
+    R[n:] = 0.0
+    got = R[np.where(inv >= 0, inv, S - 1)].reshape(T, k, H) * (inv >= 0).reshape(T, k, 1)
+    for out, weights, what in [(y, W, "y"), (dx, np.ones_like(W), "dx")]:
+        ref = np.sum(got * weights[:, :, None], axis=1)
+        mag = np.sum(np.abs(got * weights[:, :, None]), axis=1)
+        if S * H <= 20000:
+            np.testing.assert_allclose(ref, oo.unpermute(R, inv, weights, T, k), rtol=0, atol=1e-12)
+        near(f64(out[:, :H]), ref, np.abs(ref) * rel + ab + (k + 1) * U * mag, what)
+    tok, kept = perm // k, (inv >= 0).reshape(T, k)
+    ref = W.reshape(-1)[perm][:, None] * D[tok]
+    near(f64(drows[:n, :H]), ref, np.abs(ref) * (rel + U) + ab, "drows")
+    refdw = np.sum(got * D[:, None, :], axis=2)
+    mag = np.sum(np.abs(got * D[:, None, :]), axis=2)
+    near(f64(dw), refdw, (8 * (-(-H // 512)) + 8) * U * mag, "dw")                # a lane's chunks, then 6 levels
+    assert np.all(f64(dw)[~kept] == 0)
+
+
+def test_unpermute_long_rows_and_bad_places(torch):
+    say("unpermute: H = 8192, entries of inv outside the rows are dropped slots")
+    T, H, k = 6, 8192, 3
+    shp = B.shape(H, 32, 8, k)
+    inv = np.arange(T * k, dtype=np.int32)
+    inv[[2, 5, 9]] = [-5, T * k, 2 ** 31 - 1]
+    iv = torch.from_numpy(inv).to(DEV)
+    rows, w, dy = rand(torch, 5, (T * k, H), "bf16"), rand(torch, 7, (T, k), "f32"), rand(torch, 6, (T, H), "bf16")
+    y, dw = torch.empty((T, H), dtype=torch.bfloat16, device=DEV), torch.empty((T, k), device=DEV)
+    drows = torch.full_like(rows, 7.0)
+    B.pw_moe_unpermute(shp, T, rows, iv, w, y)
+    B.pw_moe_unpermute_backward(shp, T, dy, rows, iv, w, drows, dw)
+    torch.cuda.synchronize()
+    ok = inv.copy()
+    ok[(inv < 0) | (inv >= T * k)] = -1
+    R, W, D = f64(rows), f64(w), f64(dy)
+    ref, mag = oo.unpermute(R, ok, W, T, k), oo.unpermute(np.abs(R), ok, np.abs(W), T, k)
+    near(f64(y), ref, np.abs(ref) * 2.0 ** -8 + (k + 1) * U * mag, "y")
+    dr, rdw = oo.unpermute_backward(D, R, ok, W, T, k)
+    assert bool((drows[[2, 5, 9]] == 7).all())
+    keep = np.setdiff1d(np.arange(T * k), [2, 5, 9])
+    near(f64(drows)[keep], dr[keep], np.abs(dr[keep]) * (2.0 ** -8 + U), "drows")
+    near(f64(dw), rdw, 256 * U * oo.unpermute_backward(np.abs(D), np.abs(R), ok, W, T, k)[1], "dw")
+
+
+def test_rows_past_32_bits(torch):
+    """Element offsets past 2^31 and byte offsets past 2^32."""
+    T, H, E, k = 150001, 8192, 8, 2
+    say(f"permute and back: {T * k} rows of {H} bf16, {T * k * H * 2 / 2 ** 30:.1f} GiB")
+    shp = B.shape(H, 32, E, k)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((T, H), generator=g, device=DEV, dtype=torch.bfloat16)
+    ids = torch.rand((T, E), generator=g, device=DEV).topk(k, dim=1).indices.int().contiguous()
+    xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=DEV)
+    off, inv = torch.empty(E + 1, dtype=torch.int32, device=DEV), torch.empty(T * k, dtype=torch.int32, device=DEV)
+    ws = torch.empty(B.pw_moe_permute_workspace_bytes(shp, T), dtype=torch.uint8, device=DEV)
+    B.pw_moe_permute(shp, T, x, ids, xs, off, inv, None, ws)
+    order = torch.argsort(ids.reshape(-1).long(), stable=True)
+    for s in range(0, T * k, 50000):
+        assert torch.equal(xs[s:s + 50000], x[order[s:s + 50000] // k])
+    y = torch.empty_like(x)
+    B.pw_moe_unpermute(shp, T, xs, inv, torch.full((T, k), 0.5, device=DEV), y)     # 0.5 x + 0.5 x
+    assert torch.equal(y, x)
+    dw = torch.empty((T, k), device=DEV)
+    B.pw_moe_unpermute_backward(shp, T, x, xs, inv, torch.full((T, k), 2.0, device=DEV), xs, dw)
+    for s in range(0, T * k, 50000):
+        assert torch.equal(xs[s:s + 50000], (2 * x[order[s:s + 50000] // k].float()).bfloat16())
+    out = torch.empty_like(x)
+    B.pw_rmsnorm(T, H, x, torch.ones(H, dtype=torch.bfloat16, device=DEV), EPS, y, residual=y, residual_out=out)
+    tail = x[-3:]
+    assert torch.equal(out[-3:], (tail.float() * 2).bfloat16())
+    ref = oo.rmsnorm(f64(tail), np.ones(H), EPS, f64(tail))[1]
+    near(f64(y[-3:]), ref, np.abs(ref) * (2.0 ** -8 + ROW * U), "last rows' norm")
+    square = np.repeat(np.sum(f64(tail) ** 2, axis=1, keepdims=True), k, axis=1)
+    near(f64(dw[-3:]), square, (H // 64 + 8) * U * square, "last dw")
+
+
+# ----- the router's gradient --------------------------------------------------
+
+ROUTER_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd", 7, 96, 5, 3, 0.3),
+                ("E256_k64", 6, 160, 256, 64, 0.1), ("qwen", 257, 2048, 60, 4, 0.05), ("mixtral", 1100, 4096, 8, 2, 0.0),
+                ("E256_k8", 1500, 288, 256, 8, 0.2), ("all_dropped", 33, 64, 8, 2, 1.0), ("large", 5001, 544, 33, 6, 0.1)]
+
+
+@pytest.mark.parametrize("name,T,H,E,k,dropped", ROUTER_CASES, ids=[c[0] for c in ROUTER_CASES])
+def test_router_backward(torch, name, T, H, E, k, dropped):
+    say(f"router_backward {name} T={T} H={H} E={E} k={k}")
+    ids = draw_ids(12, T, E, k, dropped)
+    if name == "large":
+        ids[::3, 1] = ids[::3, 0]                       # the same expert twice in a token
+    shp = B.shape(H, 32, E, k)
+    x, wr, add = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (E, H), "f16", H ** -0.5), rand(torch, 3, (T, H), "f16", 0.1)
+    w = torch.softmax(rand(torch, 4, (T, k), "f32"), dim=1).contiguous()
+    dw = rand(torch, 5, (T, k), "f32")
+    idd = torch.from_numpy(ids).to(DEV)
+    ws = torch.full((B.pw_router_backward_workspace_bytes(shp, T),), 255, dtype=torch.uint8, device=DEV)
+    dx, dwr = torch.full_like(x, 7.0), torch.full((E, H), 7.0, device=DEV)
+    B.pw_router_backward(shp, T, x, wr, idd, w, dw, dx, dwr, ws, dx_add=add)
+    alone, dwr2 = torch.full_like(x, 7.0), torch.empty_like(dwr)
+    B.pw_router_backward(shp, T, x, wr, idd, w, dw, alone, dwr2, ws)
+    over = add.clone()
+    B.pw_router_backward(shp, T, x, wr, idd, w, dw, over, dwr2, ws, dx_add=over)
+    torch.cuda.synchronize()
+    assert torch.equal(dwr, dwr2) and torch.equal(over, dx)
+    X, Wr, A, W, D = f64(x), f64(wr), f64(add), f64(w), f64(dw)
+    kept = (ids >= 0) & (ids < E)
+    dense, amag = np.zeros((T, E + 1)), np.zeros((T, E + 1))
+    mean = np.sum(W * D * kept, axis=1, keepdims=True)
+    dl = np.where(kept, W * (D - mean), 0.0)
+    dm = np.where(kept, W * (np.abs(D) + np.sum(np.abs(W * D) * kept, axis=1, keepdims=True)), 0.0)
+    for j in range(k):
+        at = np.where(kept[:, j], ids[:, j], E)
+        np.add.at(dense, (np.arange(T), at), dl[:, j])
+        np.add.at(amag, (np.arange(T), at), dm[:, j])
+    dense, amag = dense[:, :E], amag[:, :E]
+    refx, refw = dense @ Wr, dense.T @ X
+    if T * k * H < 100000:
+        ox, ow = oo.router_backward(X, Wr, ids, W, D)
+        np.testing.assert_allclose(refx, ox, rtol=0, atol=1e-11)
+        np.testing.assert_allclose(refw, ow, rtol=0, atol=1e-11)
+    magx, magw = amag @ np.abs(Wr), amag.T @ np.abs(X)
+    for got, plus, what in [(dx, A, "dx"), (alone, 0 * A, "dx with nothing to add to")]:
+        ref = refx + plus
+        near(f64(got), ref, np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + (2 * k + 8) * U * (magx + np.abs(plus)), what)
+    # a stretch adds at most 512 tokens here, at most 64 stretches follow; k + 8 roundings of dl
+    near(f64(dwr), refw, (min(T, 512) + 64 + 2 * k + 8) * U * magw, "drouter_w")
+
+
+def test_router_backward_of_no_tokens(torch):
+    say("router_backward: T = 0 clears drouter_w")
+    shp = B.shape(64, 32, 8, 2)
+    e, i, f = (torch.empty(0, dtype=d, device=DEV) for d in (torch.float16, torch.int32, torch.float32))
+    out = torch.full((8, 64), 5.0, device=DEV)
+    B.pw_router_backward(shp, 0, e, torch.zeros(8, 64, dtype=torch.float16, device=DEV), i, f, f, e, out,
+                         torch.empty(8192, dtype=torch.uint8, device=DEV))
+    torch.cuda.synchronize()
+    assert bool((out == 0).all())
+
+
+# ----- together -----------------------------------------------------------------
+
+@pytest.mark.parametrize("wl", ["tiny", "qwen_decode"])
+def test_forward_block(torch, wl):
+    say(f"forward_block {wl}: equal to norm, router and layer called apart")
+    L = synth.make_layer(synth.WORKLOADS[wl])
+    dev = DeviceLayer(L, device=DEV)
+    w = L.wl
+    x, res0 = rand(torch, 1, (w.T, w.H), "f16"), rand(torch, 2, (w.T, w.H), "f16", 2.0)
+    g = rand(torch, 3, (1, w.H), "f16")[0]
+    wr = torch.from_numpy(synth.draw_router_weights(5, w.E, w.H)).to(DEV)
+    stats = [(torch.zeros(w.E, dtype=torch.int32, device=DEV), torch.zeros(w.E, device=DEV)) for _ in range(2)]
+    res, xn, y = res0.clone(), torch.empty_like(x), torch.empty_like(x)
+    B.pw_rmsnorm(w.T, w.H, x, g, EPS, xn, residual=res, residual_out=res)
+    B.pw_moe_forward_routed(dev.shape, w.T, xn, wr, dev.blocks[0], dev.q, y, *stats[0], dev.ws)
+    res2, y2 = res0.clone(), torch.empty_like(x)
+    B.pw_moe_forward_block(dev.shape, w.T, x, res2, g, EPS, wr, dev.blocks[0], dev.q, y2, *stats[1], dev.ws)
+    x3, res3 = x.clone(), res0.clone()
+    B.pw_moe_forward_block(dev.shape, w.T, x3, res3, g, EPS, wr, dev.blocks[0], dev.q, x3, None, None, dev.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(res, res2) and torch.equal(y, y2) and torch.equal(stats[0][0], stats[1][0])
+    assert torch.equal(x3, y) and torch.equal(res3, res) and dev.status() == 0
+    assert float(y.float().abs().max()) > 0
+
+
+def experts(torch, L, e, rows):
+    """fp64 SwiGLU of expert e with its dequantized weights."""
+    gu, dn = (torch.from_numpy(orc.fp16_bits_to_f64(orc.dequant_block(L.planes[e][m], L.luts[e][m],
+                                                                      int(L.q[e][m])))).to(DEV) for m in (0, 1))
+    a = rows.double() @ gu.t().contiguous()
+    I = L.wl.I
+    return (torch.nn.functional.silu(a[:, :I]) * a[:, I:]) @ dn.t().contiguous()
+
+
+def test_sorted_products_equal_the_layer(torch):
+    """Norm, router, sort, each expert's products on its own rows, back with the
+    weights: the fused layer's output on the same routing."""
+    say("permute -> own expert products -> unpermute against pw_moe_forward")
+    L = synth.make_layer(synth.WORKLOADS["tiny"])
+    w = L.wl
+    dev = DeviceLayer(L, device=DEV)
+    x, res = rand(torch, 1, (w.T, w.H), "f16"), rand(torch, 2, (w.T, w.H), "f16")
+    xn, y = torch.empty_like(x), torch.empty_like(x)
+    B.pw_rmsnorm(w.T, w.H, x, torch.ones(w.H, dtype=torch.float16, device=DEV), EPS, xn, residual=res, residual_out=res)
+    wr = torch.from_numpy(synth.draw_router_weights(5, w.E, w.H)).to(DEV)
+    ids, wt = torch.empty((w.T, w.k), dtype=torch.int32, device=DEV), torch.empty((w.T, w.k), device=DEV)
+    B.pw_router_topk(dev.shape, w.T, xn, wr, ids, wt, None, None, dev.ws)
+    B.pw_moe_forward(dev.shape, w.T, xn, ids, wt, dev.blocks[0], dev.q, y, dev.ws)
+    xs, off, inv, _, _, status, _ = run_permute(torch, xn, ids.cpu().numpy(), w.E)
+    rows = torch.zeros((w.T * w.k, w.H), dtype=torch.float32, device=DEV)
+    ends = off.tolist()
+    for e in range(w.E):
+        if ends[e + 1] > ends[e]:
+            rows[ends[e]:ends[e + 1]] = experts(torch, L, e, xs[ends[e]:ends[e + 1]]).float()
+    mine = torch.empty((w.T, w.H), device=DEV)
+    B.pw_moe_unpermute(dev.shape, w.T, rows, inv, wt, mine)
+    torch.cuda.synchronize()
+    assert status == 0
+    rel = float((mine.double() - y.double()).norm() / y.double().norm())
+    say(f"  rel_l2 {rel:.2e}")
+    assert rel <= 1e-3                                  # the layer's own tolerance against the 64-bit oracle
+
+
+def test_gradients_through_the_chain(torch):
+    """residual + x -> norm -> router weights -> sort -> a linear map per expert ->
+    back with the weights, and the gradient of all of it, in fp32 and fp16 where
+    the library has only that; against torch's automatic gradient in 64 bits."""
+    T, H, E, k = 37, 128, 6, 2
+    say(f"gradient of the whole chain, T={T} H={H} E={E} k={k}")
+    shp = B.shape(H, 32, E, k)
+    x, res, g = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (T, H), "f16"), rand(torch, 3, (1, H), "f16")[0]
+    wr, M = rand(torch, 4, (E, H), "f16", H ** -0.5), rand(torch, 5, (E, H, H), "f16", H ** -0.5)
+    dy, dout = rand(torch, 6, (T, H), "f16"), rand(torch, 7, (T, H), "f16")
+    new = lambda *s, d=torch.float16: torch.empty(s, dtype=d, device=DEV)
+    r, xn, xs, off, inv = new(T, H), new(T, H), new(T * k, H), new(E + 1, d=torch.int32), new(T * k, d=torch.int32)
+    ids, w = new(T, k, d=torch.int32), new(T, k, d=torch.float32)
+    ws = torch.empty(max(B.pw_workspace_bytes(shp, T), B.pw_router_backward_workspace_bytes(shp, T),
+                         B.pw_moe_permute_workspace_bytes(shp, T), B.pw_rmsnorm_backward_workspace_bytes(T, H)),
+                     dtype=torch.uint8, device=DEV)
+    B.pw_rmsnorm(T, H, x, g, EPS, xn, residual=res, residual_out=r)
+    B.pw_router_topk(shp, T, xn, wr, ids, w, workspace=ws)
+    B.pw_moe_permute(shp, T, xn, ids, xs, off, inv, None, ws)
+    ends = off.tolist()
+    rows, y = new(T * k, H), new(T, H)
+    for e in range(E):
+        rows[ends[e]:ends[e + 1]] = (xs[ends[e]:ends[e + 1]].double() @ M[e].double()).half()
+    B.pw_moe_unpermute(shp, T, rows, inv, w, y)
+    drows, dw, dxs, dxn, dr = new(T * k, H), new(T, k, d=torch.float32), new(T * k, H), new(T, H), new(T, H)
+    dwr, dg = new(E, H, d=torch.float32), new(H, d=torch.float32)
+    B.pw_moe_unpermute_backward(shp, T, dy, rows, inv, w, drows, dw)
+    for e in range(E):
+        dxs[ends[e]:ends[e + 1]] = (drows[ends[e]:ends[e + 1]].double() @ M[e].double().t().contiguous()).half()
+    B.pw_moe_permute_backward(shp, T, dxs, inv, dxn)
+    B.pw_router_backward(shp, T, xn, wr, ids, w, dw, dxn, dwr, ws, dx_add=dxn)
+    B.pw_rmsnorm_backward(T, H, dxn, r, g, EPS, dr, dg, ws, dresidual=dout)
+    torch.cuda.synchronize()
+
+    leaf = lambda t: t.detach().double().cpu().requires_grad_()
+    X, G, W = leaf(x), leaf(g), leaf(wr)
+    R = X + res.double().cpu()
+    N = R / torch.sqrt((R * R).mean(1, keepdim=True) + EPS) * G
+    sel = ids.long().cpu()
+    p = torch.softmax(torch.gather(N @ W.t(), 1, sel), dim=1)
+    out = sum(p[:, j:j + 1] * torch.stack([N[t] @ M[sel[t, j]].double().cpu() for t in range(T)]) for j in range(k))
+    ((out * dy.double().cpu()).sum() + (R * dout.double().cpu()).sum()).backward()
+    # five fp16 roundings (2^-11) lie between a leaf and its gradient, each at most once per addend
+    for got, ref, what in [(y, out.detach(), "y"), (dr, X.grad, "dx"), (dg, G.grad, "dweight"), (dwr, W.grad, "drouter_w")]:
+        rel = float((got.double().cpu() - ref).norm() / ref.norm())
+        say(f"  {what}: rel_l2 {rel:.2e}")
+        assert rel <= 5 * 2.0 ** -11, what
+
+
+# ----- streams, graphs, refusals -------------------------------------------------
+
+def all_ops(torch, seed, T=1500, H=256, E=8, k=4):
+    """Buffers of one use of every operator, and the calls on them."""
+    shp = B.shape(H, 32, E, k)
+    S = T * k
+    new = lambda *s, d=torch.float16: torch.zeros(s, dtype=d, device=DEV)
+    b = {"x": rand(torch, seed, (T, H), "f16"), "res": rand(torch, seed + 1, (T, H), "f16"),
+         "g": rand(torch, seed + 2, (1, H), "f16")[0], "wr": rand(torch, seed + 3, (E, H), "f16", H ** -0.5),
+         "ids": torch.from_numpy(draw_ids(seed, T, E, k, 0.1)).to(DEV), "w": rand(torch, seed + 4, (T, k), "f32"),
+         "r": new(T, H), "y": new(T, H), "codes": torch.zeros((T, H), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn),
+         "scale": new(T, 2, d=torch.float32), "xs": new(S, H), "xs8": torch.zeros((S, H), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn),
+         "sc": new(S, 2, d=torch.float32), "off": new(E + 1, d=torch.int32), "inv": new(S, d=torch.int32),
+         "back": new(T, H), "drows": new(S, H), "dw": new(T, k, d=torch.float32), "dx": new(T, H), "dx2": new(T, H),
+         "dwr": new(E, H, d=torch.float32), "dr": new(T, H), "dg": new(H, d=torch.float32)}
+    ws = {"p": torch.empty(B.pw_moe_permute_workspace_bytes(shp, T), dtype=torch.uint8, device=DEV),
+          "r": torch.empty(B.pw_router_backward_workspace_bytes(shp, T), dtype=torch.uint8, device=DEV),
+          "n": torch.empty(B.pw_rmsnorm_backward_workspace_bytes(T, H), dtype=torch.uint8, device=DEV)}
+
+    def calls(stream=None):
+        B.pw_rmsnorm(T, H, b["x"], b["g"], EPS, b["y"], residual=b["res"], residual_out=b["r"], stream=stream)
+        B.pw_rmsnorm(T, H, b["x"], b["g"], EPS, b["codes"], residual=b["res"], scale=b["scale"], group=128, stream=stream)
+        B.pw_moe_permute(shp, T, b["codes"], b["ids"], b["xs8"], b["off"], b["inv"], None, ws["p"], x_scale=b["scale"],
+                         xs_scale=b["sc"], stream=stream)
+        B.pw_moe_permute(shp, T, b["y"], b["ids"], b["xs"], b["off"], b["inv"], None, ws["p"], stream=stream)
+        B.pw_moe_unpermute(shp, T, b["xs"], b["inv"], b["w"], b["back"], stream=stream)
+        B.pw_moe_unpermute_backward(shp, T, b["back"], b["xs"], b["inv"], b["w"], b["drows"], b["dw"], stream=stream)
+        B.pw_moe_permute_backward(shp, T, b["drows"], b["inv"], b["dx"], stream=stream)
+        B.pw_router_backward(shp, T, b["y"], b["wr"], b["ids"], b["w"], b["dw"], b["dx2"], b["dwr"], ws["r"],
+                             dx_add=b["dx"], stream=stream)
+        B.pw_rmsnorm_backward(T, H, b["dx2"], b["r"], b["g"], EPS, b["dr"], b["dg"], ws["n"], dresidual=b["dx"],
+                              stream=stream)
+
+    outs = ["r", "y", "codes", "scale", "xs8", "sc", "xs", "off", "inv", "back", "drows", "dw", "dx", "dx2", "dwr", "dr", "dg"]
+    return b, calls, outs
+
+
+def snapshot(torch, b, outs):
+    torch.cuda.synchronize()
+    return [b[o].contiguous().view(torch.uint8).clone() for o in outs]
+
+
+def test_two_streams_at_once(torch):
+    say("every operator on two streams at once, each with its own workspaces, equal to calls alone")
+    sets = [all_ops(torch, s) for s in (100, 200)]
+    want = []
+    for b, calls, outs in sets:
+        calls()
+        want.append(snapshot(torch, b, outs))
+    for b, _, outs in sets:
+        for o in outs:
+            b[o].view(torch.uint8).zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        for (b, calls, outs), st in zip(sets, streams):
+            calls(st)
+    for (b, _, outs), w in zip(sets, want):
+        assert all(torch.equal(a, c) for a, c in zip(snapshot(torch, b, outs), w))
+
+
+def test_captured_graphs(torch):
+    say("two captured graphs with their own workspaces, replayed in turn with changed inputs and eager calls between")
+    sets = [all_ops(torch, s) for s in (300, 400)]
+    graphs = []
+    for b, calls, outs in sets:
+        calls()
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            calls()
+        graphs.append(gr)
+    eager = all_ops(torch, 500)
+    for n in range(4):
+        for b, _, _ in sets:
+            b["x"].mul_(-0.5 if n % 2 else 2.0)
+            b["ids"].copy_(b["ids"].roll(n + 1, dims=0))
+        torch.cuda.synchronize()
+        for gr in graphs:
+            gr.replay()
+        eager[1]()
+        got = [snapshot(torch, b, outs) for b, _, outs in sets]
+        for (b, calls, outs), g in zip(sets, got):
+            # rows without a slot keep what an earlier replay left there; everything else is written again
+            calls()
+            again = snapshot(torch, b, outs)
+            for o, a, c in zip(outs, g, again):
+                assert torch.equal(a, c), (n, o)
+
+
+def test_binding_refusals(torch):
+    say("binding: wrong types, shapes, strides and streams are refused before any launch")
+    T, H, E, k = 4, 64, 8, 2
+    shp = B.shape(H, 32, E, k)
+    h = lambda *s: torch.zeros(s, dtype=torch.float16, device=DEV)
+    f = lambda *s: torch.zeros(s, device=DEV)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device=DEV)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    x, g, xs = h(T, H), h(H), h(T * k, H)
+    bad = [
+        lambda: B.pw_rmsnorm(T, H, x, f(H), EPS, x),                              # weight of another type
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, f(T, H)),                           # output of another type
+        lambda: B.pw_rmsnorm(T, H, h(H, T).t(), g, EPS, x),                       # columns apart
+        lambda: B.pw_rmsnorm(T + 1, H, x, g, EPS, x),                             # too few rows
+        lambda: B.pw_rmsnorm(T, H, x[:, :32], g, EPS, x),                         # too few columns
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, x, residual=f(T, H)),
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, torch.zeros((T, H), dtype=torch.float8_e4m3fn, device=DEV), scale=f(T - 1, 1)),
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, x.double()),
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, h(1, H).expand(T, H)),              # rows that overlap
+        lambda: B.pw_rmsnorm(T, H, x, g.cpu(), EPS, x),
+        lambda: B.pw_rmsnorm_backward(T, H, x, x, g, EPS, h(T, H), f(H)),         # no workspace
+        lambda: B.pw_rmsnorm_backward(T, H, x, x, g, EPS, h(T, H), f(H // 2), ws),
+        lambda: B.pw_moe_permute(shp, T, x, i(T, k).long(), xs, i(E + 1), i(T * k), None, ws),
+        lambda: B.pw_moe_permute(shp, T, x, i(T, k), h(T, H), i(E + 1), i(T * k), None, ws),
+        lambda: B.pw_moe_permute(shp, T, x, i(T, k), xs, i(E), i(T * k), None, ws),
+        lambda: B.pw_moe_permute(shp, T, x, i(T, 2 * k)[:, ::2], xs, i(E + 1), i(T * k), None, ws),
+        lambda: B.pw_moe_permute(shp, T, x, i(T, k), xs, i(E + 1), i(T * k), None, ws, x_scale=f(T, 2)),
+        lambda: B.pw_moe_unpermute(shp, T, xs, i(T * k), h(T, k), x),
+        lambda: B.pw_moe_unpermute_backward(shp, T, x, None, i(T * k), f(T, k), xs, f(T, k)),
+        lambda: B.pw_router_backward(shp, T, f(T, H), h(E, H), i(T, k), f(T, k), f(T, k), x, f(E, H), ws),
+        lambda: B.pw_router_backward(shp, T, h(T, 2 * H)[:, :H], h(E, H), i(T, k), f(T, k), f(T, k), x, f(E, H), ws),
+    ]
+    for n, call in enumerate(bad):
+        with pytest.raises(B.PwError) as e:
+            call()
+        assert e.value.status == B.PW_ERR_INVALID_ARG, n
+    with pytest.raises(B.PwError) as e:
+        B.pw_rmsnorm(T, H, h(T * H + 1)[1:].view(T, H), g, EPS, x)
+    assert e.value.status == B.PW_ERR_ALIGNMENT
+    with pytest.raises(B.PwError) as e:
+        B.pw_rmsnorm_backward(T, H, x, x, g, EPS, h(T, H), f(H), ws[:256])
+    assert e.value.status == B.PW_ERR_WORKSPACE
