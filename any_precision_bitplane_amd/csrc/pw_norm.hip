@@ -186,7 +186,12 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 // residual output.  A block walks every gridDim-th group of rows and keeps its
 // share of dg in registers; the shares meet in a second kernel, in a fixed
 // order.
-template <int DT, int WPR, int NV>
+//
+// AHEAD: the next row is requested before the current one is used (dx may be
+// written over an input: the rows in flight are the block's own later ones).
+// LEAN: the weight and dresidual are loaded where they are used, so that the
+// longest rows' chunks stay in registers.
+template <int DT, int WPR, int NV, bool AHEAD, bool LEAN>
 __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(NormGradArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
@@ -197,38 +202,66 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
   const int first = (wave % WPR) * kWave + lane;
   const int C = a.H / 8;
   const floatx8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  floatx8 g[NV], dg[NV];
+  const elem* gain = static_cast<const elem*>(a.weight);
+  typedef typename R::chunk chunk;
+  floatx8 dg[NV];
+  chunk gc[LEAN ? 1 : NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = first + i * WPR * kWave;
     dg[i] = zero;
-    g[i] = c < C ? R::wide(R::load(static_cast<const elem*>(a.weight) + 8 * c)) : zero;
+    const int c = first + i * WPR * kWave;
+    if constexpr (!LEAN) gc[i] = R::load(gain + 8 * (c < C ? c : 0));
   }
-  int parity = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows, parity ^= 1) {
-    const int64_t row = base + wave / WPR;
-    const bool live = row < a.T;
+  const bool adds = a.dresidual != nullptr;
+  // the chunks of one row of each matrix, as they lie in memory; past the row's
+  // end the first chunk again, which nothing uses
+  auto fetch = [&](int64_t row, chunk(&r)[NV], chunk(&d)[NV], chunk(&add)[NV]) {
+    if (row >= a.T) return;
     const elem* dy = static_cast<const elem*>(a.dy) + row * a.dy_stride;
     const elem* rr = static_cast<const elem*>(a.r) + row * a.r_stride;
     const elem* dres = static_cast<const elem*>(a.dresidual) + row * a.dresidual_stride;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      int c = first + i * WPR * kWave;
+      c = c < C ? c : 0;
+      r[i] = R::load(rr + 8 * c);
+      d[i] = R::load(dy + 8 * c);
+      if (!LEAN && adds) add[i] = R::load(dres + 8 * c);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t base = (int64_t)blockIdx.x * kRows;
+  chunk rn[NV], dn[NV], an[NV];
+  if constexpr (AHEAD) fetch(base + wave / WPR, rn, dn, an);
+  for (int parity = 0; base < a.T; base += step, parity ^= 1) {
+    const int64_t row = base + wave / WPR;
+    const bool live = row < a.T;
     elem* dx = static_cast<elem*>(a.dx) + row * a.dx_stride;
-    floatx8 r[NV], d[NV], add[NV];
+    const elem* dres = static_cast<const elem*>(a.dresidual) + row * a.dresidual_stride;
+    chunk rc[NV], dc[NV], ac[NV];
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        rc[i] = rn[i];
+        dc[i] = dn[i];
+        ac[i] = an[i];
+      }
+      fetch(row + step, rn, dn, an);
+    } else {
+      fetch(row, rc, dc, ac);
+    }
     float sq = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first + i * WPR * kWave;
-      const bool in = live && c < C;
-      r[i] = in ? R::wide(R::load(rr + 8 * c)) : zero;
-      d[i] = in ? R::wide(R::load(dy + 8 * c)) : zero;
-      add[i] = in && a.dresidual ? R::wide(R::load(dres + 8 * c)) : zero;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
+      if (!live || c >= C) continue;
+      const floatx8 r = R::wide(rc[i]), gd = R::wide(LEAN ? R::load(gain + 8 * c) : gc[LEAN ? 0 : i]) * R::wide(dc[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        sq = __builtin_fmaf(r[i][j], r[i][j], sq);
-        dot = __builtin_fmaf(g[i][j] * d[i][j], r[i][j], dot);
+        sq = __builtin_fmaf(r[j], r[j], sq);
+        dot = __builtin_fmaf(gd[j], r[j], dot);
       }
+    }
     sq = wave_sum(sq);
     dot = wave_sum(dot);
     if constexpr (WPR > 1) {
@@ -252,8 +285,11 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
     for (int i = 0; i < NV; ++i) {
       const int c = first + i * WPR * kWave;
       if (!live || c >= C) continue;
-      R::store(dx + 8 * c, R::narrow(rstd * (g[i] * d[i] - r[i] * f) + add[i]));
-      dg[i] += d[i] * r[i] * rstd;
+      const floatx8 r = R::wide(rc[i]), d = R::wide(dc[i]);
+      floatx8 v = rstd * (R::wide(LEAN ? R::load(gain + 8 * c) : gc[LEAN ? 0 : i]) * d - r * f);
+      if (adds) v += R::wide(LEAN ? R::load(dres + 8 * c) : ac[i]);
+      R::store(dx + 8 * c, R::narrow(v));
+      dg[i] += d * r * rstd;
     }
   }
   if (!a.part) return;
@@ -289,7 +325,10 @@ hipError_t run_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) {
   constexpr int kRows = block_waves(WPR) / WPR;
   const unsigned want = ((unsigned)a.T + kRows - 1) / kRows;
   const unsigned grid = want < (unsigned)kNormGradBlocks ? want : (unsigned)kNormGradBlocks;
-  hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, WPR, NV>), dim3(grid), dim3(block_waves(WPR) * kWave), 0, s, a);
+  // registers of a lane's chunks: 4 (16-bit) or 8 (fp32) for each of three matrices, again for the row ahead
+  constexpr int kChunkRegs = NV * (DT == PW_F32 ? 8 : 4);
+  constexpr bool kLean = WPR == 16 && kChunkRegs >= 16, kAhead = !kLean && kChunkRegs <= 16;
+  hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, WPR, NV, kAhead, kLean>), dim3(grid), dim3(block_waves(WPR) * kWave), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dweight) return e;
   hipLaunchKernelGGL(join_rows_kernel, dim3((a.H + 15) / 16), dim3(256), 0, s, a.part, (int)(grid * kRows), a.H,
