@@ -357,104 +357,111 @@ def pw_moe_forward_layers(shp: PwMoeShape, T: int, x, router_ws, blocks, qs, y, 
 # These calls take torch tensors: types and row strides come from them.  What
 # the library cannot see in a pointer is checked here first (device, type, a
 # contiguous last dimension, sizes) and refused as the library would refuse it.
-_DTYPES = None
+_torch = None
+_current_stream = None   # GPU index -> raw handle of torch's current stream there
+_DTYPES: dict = {}
 
 
-def _dtypes():
-    global _DTYPES
-    if _DTYPES is None:
+def _load_ops() -> ctypes.CDLL:
+    global _torch, _current_stream
+    if _torch is None:
         import torch
-        _DTYPES = {torch.float32: PW_F32, torch.float16: PW_F16, torch.bfloat16: PW_BF16,
-                   torch.float8_e4m3fn: PW_E4M3}
-    return _DTYPES
+        # the handle alone, without a Stream object around it (1.0 us less a call), where torch offers that
+        _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _DTYPES.update({torch.float32: PW_F32, torch.float16: PW_F16, torch.bfloat16: PW_BF16,
+                        torch.float8_e4m3fn: PW_E4M3})
+        _torch = torch
+    return _lib or load()
 
 
 class _Refused(Exception):
     pass
 
 
-class _Call:
-    """The tensors of one call: all on one GPU, which is the current one while the call runs."""
-
-    def __init__(self, first):
-        if not getattr(first, "is_cuda", False):
-            raise _Refused("tensors must be on a GPU")
-        self.index = first.device.index
-
-    def _on_device(self, t, name):
-        if not getattr(t, "is_cuda", False) or t.device.index != self.index:
-            raise _Refused(f"{name} must be on the GPU of the other tensors")
-
-    def rows(self, t, name, n, H, dtype=None):
-        """(pointer, row stride) of a matrix of at least n rows of H elements."""
-        if t is None:
-            return None, 0
-        self._on_device(t, name)
-        if t.dim() != 2 or t.shape[1] != H or t.shape[0] < n or (H > 1 and t.stride(1) != 1):
-            raise _Refused(f"{name} must have at least {n} rows of {H} elements next to each other")
-        if dtype is not None and t.dtype != dtype:
-            raise _Refused(f"{name} must be {dtype}")
-        return t.data_ptr(), t.stride(0) if n > 1 else H
-
-    def array(self, t, name, n, dtype):
-        """Pointer of a contiguous tensor of at least n elements."""
-        if t is None:
-            return None
-        self._on_device(t, name)
-        if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
-            raise _Refused(f"{name} must be {n} contiguous elements of {dtype}")
-        return t.data_ptr()
-
-    def workspace(self, t):
-        if t is None:
-            return None, 0
-        self._on_device(t, "workspace")
-        if not t.is_contiguous():
-            raise _Refused("workspace must be contiguous")
-        return t.data_ptr(), t.numel() * t.element_size()
-
-    def run(self, fn, *args, stream=None):
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.index).cuda_stream
-        elif not isinstance(stream, int):
-            if stream.device.index != self.index:
-                raise _Refused("stream must be one of the tensors' GPU")
-            stream = stream.cuda_stream
-        if torch.cuda.current_device() == self.index:
-            return fn(*args, stream)
-        with torch.cuda.device(self.index):
-            return fn(*args, stream)
+def _gpu(t) -> int:
+    """The GPU of the call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise _Refused("tensors must be on a GPU")
+    return dev
 
 
-def _row_op(name, check, body) -> int:
-    try:
-        st = body(load())
-    except _Refused as e:
-        if check:
-            raise PwError(PW_ERR_INVALID_ARG, f"{name}: {e}") from None
-        return PW_ERR_INVALID_ARG
-    if check and st != PW_OK:
+def _rows(t, name, n, H, dev, dtype):
+    """(pointer, row stride) of a matrix of at least n rows of H elements of dtype."""
+    if t is None:
+        return None, 0
+    shape = t.shape
+    if t.get_device() != dev:
+        raise _Refused(f"{name} must be on the GPU of the other tensors")
+    if len(shape) != 2 or shape[1] != H or shape[0] < n or t.dtype is not dtype:
+        raise _Refused(f"{name} must have at least {n} rows of {H} elements of {dtype}")
+    stride, inner = t.stride()
+    if inner != 1 and H > 1:
+        raise _Refused(f"the elements of a row of {name} must lie next to each other")
+    return t.data_ptr(), stride if n > 1 else H
+
+
+def _array(t, name, n, dev, dtype):
+    """Pointer of a contiguous tensor of at least n elements of dtype."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise _Refused(f"{name} must be on the GPU of the other tensors")
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+        raise _Refused(f"{name} must be {n} contiguous elements of {dtype}")
+    return t.data_ptr()
+
+
+def _scratch(t, dev):
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise _Refused("workspace must be contiguous and on the GPU of the other tensors")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _run(name, check, dev, stream, fn, *args) -> int:
+    """fn(*args, stream) with the tensors' GPU as the current one."""
+    cuda = _torch.cuda
+    if stream is None:
+        stream = _current_stream(dev)
+    elif not isinstance(stream, int):
+        if stream.device.index != dev:
+            raise _Refused("stream must be one of the tensors' GPU")
+        stream = stream.cuda_stream
+    if cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with cuda.device(dev):
+            st = fn(*args, stream)
+    if st != PW_OK and check:
         raise PwError(st, name)
     return st
+
+
+def _refuse(name, check, e) -> int:
+    if check:
+        raise PwError(PW_ERR_INVALID_ARG, f"{name}: {e}") from None
+    return PW_ERR_INVALID_ARG
 
 
 def pw_rmsnorm(T: int, H: int, x, weight, eps: float, y, residual=None, residual_out=None, scale=None, group: int = 0,
                stream=None, check: bool = True) -> int:
     """y: x's type, or torch.float8_e4m3fn with scale fp32 [T][groups]."""
-    def body(lib):
-        import torch
-        c = _Call(x)
-        dt = x.dtype
-        groups = (H + 127) // 128 if group else 1
-        px, sx = c.rows(x, "x", T, H)
-        pr, sr = c.rows(residual, "residual", T, H, dt)
-        po, so = c.rows(residual_out, "residual_out", T, H, dt)
-        py, sy = c.rows(y, "y", T, H)
-        return c.run(lib.pw_rmsnorm, T, H, _dtypes().get(dt, -1), px, sx, pr, sr, po, so,
-                     c.array(weight, "weight", H, dt), eps, _dtypes().get(y.dtype, -1), py, sy,
-                     c.array(scale, "scale", T * groups, torch.float32), group, stream=stream)
-    return _row_op("pw_rmsnorm", check, body)
+    lib = _load_ops()
+    try:
+        dev, dt = _gpu(x), x.dtype
+        px, sx = _rows(x, "x", T, H, dev, dt)
+        pr, sr = _rows(residual, "residual", T, H, dev, dt)
+        po, so = _rows(residual_out, "residual_out", T, H, dev, dt)
+        py, sy = _rows(y, "y", T, H, dev, y.dtype)
+        pc = None if scale is None else _array(scale, "scale", T * ((H + 127) // 128 if group else 1), dev,
+                                               _torch.float32)
+        return _run("pw_rmsnorm", check, dev, stream, lib.pw_rmsnorm, T, H, _DTYPES.get(dt, -1), px, sx, pr, sr, po,
+                    so, _array(weight, "weight", H, dev, dt), eps, _DTYPES.get(y.dtype, -1), py, sy, pc, group)
+    except _Refused as e:
+        return _refuse("pw_rmsnorm", check, e)
 
 
 def pw_rmsnorm_backward_workspace_bytes(T_max: int, H: int) -> int:
@@ -463,19 +470,19 @@ def pw_rmsnorm_backward_workspace_bytes(T_max: int, H: int) -> int:
 
 def pw_rmsnorm_backward(T: int, H: int, dy, r, weight, eps: float, dx, dweight=None, workspace=None, dresidual=None,
                         stream=None, check: bool = True) -> int:
-    def body(lib):
-        import torch
-        c = _Call(dy)
-        dt = dy.dtype
-        pd, sd = c.rows(dy, "dy", T, H)
-        pr, sr = c.rows(r, "r", T, H, dt)
-        pa, sa = c.rows(dresidual, "dresidual", T, H, dt)
-        px, sx = c.rows(dx, "dx", T, H, dt)
-        pw, nw = c.workspace(workspace)
-        return c.run(lib.pw_rmsnorm_backward, T, H, _dtypes().get(dt, -1), pd, sd, pr, sr,
-                     c.array(weight, "weight", H, dt), eps, pa, sa, px, sx,
-                     c.array(dweight, "dweight", H, torch.float32), pw, nw, stream=stream)
-    return _row_op("pw_rmsnorm_backward", check, body)
+    lib = _load_ops()
+    try:
+        dev, dt = _gpu(dy), dy.dtype
+        pd, sd = _rows(dy, "dy", T, H, dev, dt)
+        pr, sr = _rows(r, "r", T, H, dev, dt)
+        pa, sa = _rows(dresidual, "dresidual", T, H, dev, dt)
+        px, sx = _rows(dx, "dx", T, H, dev, dt)
+        pw, nw = _scratch(workspace, dev)
+        return _run("pw_rmsnorm_backward", check, dev, stream, lib.pw_rmsnorm_backward, T, H, _DTYPES.get(dt, -1), pd,
+                    sd, pr, sr, _array(weight, "weight", H, dev, dt), eps, pa, sa, px, sx,
+                    _array(dweight, "dweight", H, dev, _torch.float32), pw, nw)
+    except _Refused as e:
+        return _refuse("pw_rmsnorm_backward", check, e)
 
 
 def pw_moe_permute_workspace_bytes(shp: PwMoeShape, T_max: int) -> int:
@@ -484,67 +491,68 @@ def pw_moe_permute_workspace_bytes(shp: PwMoeShape, T_max: int) -> int:
 
 def pw_moe_permute(shp: PwMoeShape, T: int, x, ids, xs, offsets, inv, perm, workspace, x_scale=None, xs_scale=None,
                    status=None, stream=None, check: bool = True) -> int:
-    def body(lib):
-        import torch
-        c = _Call(x)
-        H, S = shp.hidden, T * shp.top_k
+    """perm, x_scale with xs_scale, and status may be None."""
+    lib = _load_ops()
+    try:
+        dev, dt = _gpu(x), x.dtype
+        H, S, i32, f32 = shp.hidden, T * shp.top_k, _torch.int32, _torch.float32
         groups = 0
         if x_scale is not None:
             if x_scale.dim() != 2:
                 raise _Refused("x_scale must have a row of scales per token")
             groups = x_scale.shape[1]
-        px, sx = c.rows(x, "x", T, H)
-        ps, ss = c.rows(xs, "xs", S, H, x.dtype)
-        pw, nw = c.workspace(workspace)
-        return c.run(lib.pw_moe_permute, ctypes.byref(shp), T, _dtypes().get(x.dtype, -1), px, sx,
-                     c.array(x_scale, "x_scale", T * groups, torch.float32), groups,
-                     c.array(ids, "ids", S, torch.int32), ps, ss,
-                     c.array(xs_scale, "xs_scale", S * groups, torch.float32),
-                     c.array(offsets, "offsets", shp.num_experts + 1, torch.int32),
-                     c.array(inv, "inv", S, torch.int32), c.array(perm, "perm", S, torch.int32),
-                     c.array(status, "status", 1, torch.int32), pw, nw, stream=stream)
-    return _row_op("pw_moe_permute", check, body)
+        px, sx = _rows(x, "x", T, H, dev, dt)
+        ps, ss = _rows(xs, "xs", S, H, dev, dt)
+        pw, nw = _scratch(workspace, dev)
+        return _run("pw_moe_permute", check, dev, stream, lib.pw_moe_permute, ctypes.byref(shp), T,
+                    _DTYPES.get(dt, -1), px, sx, _array(x_scale, "x_scale", T * groups, dev, f32), groups,
+                    _array(ids, "ids", S, dev, i32), ps, ss, _array(xs_scale, "xs_scale", S * groups, dev, f32),
+                    _array(offsets, "offsets", shp.num_experts + 1, dev, i32), _array(inv, "inv", S, dev, i32),
+                    _array(perm, "perm", S, dev, i32), _array(status, "status", 1, dev, i32), pw, nw)
+    except _Refused as e:
+        return _refuse("pw_moe_permute", check, e)
 
 
 def pw_moe_permute_backward(shp: PwMoeShape, T: int, dxs, inv, dx, stream=None, check: bool = True) -> int:
-    def body(lib):
-        import torch
-        c = _Call(dxs)
-        S = T * shp.top_k
-        ps, ss = c.rows(dxs, "dxs", S, shp.hidden)
-        px, sx = c.rows(dx, "dx", T, shp.hidden, dxs.dtype)
-        return c.run(lib.pw_moe_permute_backward, ctypes.byref(shp), T, _dtypes().get(dxs.dtype, -1), ps, ss,
-                     c.array(inv, "inv", S, torch.int32), px, sx, stream=stream)
-    return _row_op("pw_moe_permute_backward", check, body)
+    lib = _load_ops()
+    try:
+        dev, dt, H, S = _gpu(dxs), dxs.dtype, shp.hidden, T * shp.top_k
+        ps, ss = _rows(dxs, "dxs", S, H, dev, dt)
+        px, sx = _rows(dx, "dx", T, H, dev, dt)
+        return _run("pw_moe_permute_backward", check, dev, stream, lib.pw_moe_permute_backward, ctypes.byref(shp), T,
+                    _DTYPES.get(dt, -1), ps, ss, _array(inv, "inv", S, dev, _torch.int32), px, sx)
+    except _Refused as e:
+        return _refuse("pw_moe_permute_backward", check, e)
 
 
 def pw_moe_unpermute(shp: PwMoeShape, T: int, rows, inv, w, y, stream=None, check: bool = True) -> int:
     """w: fp32 [T][k], or None for ones."""
-    def body(lib):
-        import torch
-        c = _Call(rows)
-        S = T * shp.top_k
-        pr, sr = c.rows(rows, "rows", S, shp.hidden)
-        py, sy = c.rows(y, "y", T, shp.hidden, rows.dtype)
-        return c.run(lib.pw_moe_unpermute, ctypes.byref(shp), T, _dtypes().get(rows.dtype, -1), pr, sr,
-                     c.array(inv, "inv", S, torch.int32), c.array(w, "w", S, torch.float32), py, sy, stream=stream)
-    return _row_op("pw_moe_unpermute", check, body)
+    lib = _load_ops()
+    try:
+        dev, dt, H, S = _gpu(rows), rows.dtype, shp.hidden, T * shp.top_k
+        pr, sr = _rows(rows, "rows", S, H, dev, dt)
+        py, sy = _rows(y, "y", T, H, dev, dt)
+        return _run("pw_moe_unpermute", check, dev, stream, lib.pw_moe_unpermute, ctypes.byref(shp), T,
+                    _DTYPES.get(dt, -1), pr, sr, _array(inv, "inv", S, dev, _torch.int32),
+                    _array(w, "w", S, dev, _torch.float32), py, sy)
+    except _Refused as e:
+        return _refuse("pw_moe_unpermute", check, e)
 
 
 def pw_moe_unpermute_backward(shp: PwMoeShape, T: int, dy, rows, inv, w, drows, dw=None, stream=None,
                               check: bool = True) -> int:
     """dw None: not wanted (rows may then be None)."""
-    def body(lib):
-        import torch
-        c = _Call(dy)
-        H, S = shp.hidden, T * shp.top_k
-        pd, sd = c.rows(dy, "dy", T, H)
-        pr, sr = c.rows(rows, "rows", S, H, dy.dtype)
-        po, so = c.rows(drows, "drows", S, H, dy.dtype)
-        return c.run(lib.pw_moe_unpermute_backward, ctypes.byref(shp), T, _dtypes().get(dy.dtype, -1), pd, sd, pr, sr,
-                     c.array(inv, "inv", S, torch.int32), c.array(w, "w", S, torch.float32), po, so,
-                     c.array(dw, "dw", S, torch.float32), stream=stream)
-    return _row_op("pw_moe_unpermute_backward", check, body)
+    lib = _load_ops()
+    try:
+        dev, dt, H, S = _gpu(dy), dy.dtype, shp.hidden, T * shp.top_k
+        pd, sd = _rows(dy, "dy", T, H, dev, dt)
+        pr, sr = _rows(rows, "rows", S, H, dev, dt)
+        po, so = _rows(drows, "drows", S, H, dev, dt)
+        return _run("pw_moe_unpermute_backward", check, dev, stream, lib.pw_moe_unpermute_backward, ctypes.byref(shp),
+                    T, _DTYPES.get(dt, -1), pd, sd, pr, sr, _array(inv, "inv", S, dev, _torch.int32),
+                    _array(w, "w", S, dev, _torch.float32), po, so, _array(dw, "dw", S, dev, _torch.float32))
+    except _Refused as e:
+        return _refuse("pw_moe_unpermute_backward", check, e)
 
 
 def pw_router_backward_workspace_bytes(shp: PwMoeShape, T_max: int) -> int:
@@ -553,17 +561,18 @@ def pw_router_backward_workspace_bytes(shp: PwMoeShape, T_max: int) -> int:
 
 def pw_router_backward(shp: PwMoeShape, T: int, x, router_w, ids, w, dw, dx, drouter_w, workspace, dx_add=None,
                        stream=None, check: bool = True) -> int:
-    def body(lib):
-        import torch
-        c = _Call(x)
-        n, S, E = T * shp.hidden, T * shp.top_k, shp.num_experts * shp.hidden
-        f16, f32 = torch.float16, torch.float32
-        pw, nw = c.workspace(workspace)
-        return c.run(lib.pw_router_backward, ctypes.byref(shp), T, c.array(x, "x", n, f16),
-                     c.array(router_w, "router_w", E, f16), c.array(ids, "ids", S, torch.int32),
-                     c.array(w, "w", S, f32), c.array(dw, "dw", S, f32), c.array(dx_add, "dx_add", n, f16),
-                     c.array(dx, "dx", n, f16), c.array(drouter_w, "drouter_w", E, f32), pw, nw, stream=stream)
-    return _row_op("pw_router_backward", check, body)
+    lib = _load_ops()
+    try:
+        dev, n, S, E = _gpu(x), T * shp.hidden, T * shp.top_k, shp.num_experts * shp.hidden
+        f16, f32 = _torch.float16, _torch.float32
+        pw, nw = _scratch(workspace, dev)
+        return _run("pw_router_backward", check, dev, stream, lib.pw_router_backward, ctypes.byref(shp), T,
+                    _array(x, "x", n, dev, f16), _array(router_w, "router_w", E, dev, f16),
+                    _array(ids, "ids", S, dev, _torch.int32), _array(w, "w", S, dev, f32),
+                    _array(dw, "dw", S, dev, f32), _array(dx_add, "dx_add", n, dev, f16),
+                    _array(dx, "dx", n, dev, f16), _array(drouter_w, "drouter_w", E, dev, f32), pw, nw)
+    except _Refused as e:
+        return _refuse("pw_router_backward", check, e)
 
 
 def pw_moe_forward_block(shp: PwMoeShape, T: int, x, residual, norm_w, eps: float, router_w, blocks, q, y, stat_count,
