@@ -291,6 +291,7 @@ hipError_t launch_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight,
 
 constexpr int kPermuteSmallSlots = 4096;   // one launch up to here (every block reads all ids)
 constexpr int kPermutePieces = 64;         // pieces of a larger call whose slots are counted apart
+constexpr int64_t kPermutePieceSlots = 8192;   // a piece has no more; with more than 64 pieces a launch sums their counts
 
 struct PermuteArgs {
   int T, k, E;
@@ -309,6 +310,36 @@ struct PermuteArgs {
   int block_tokens, pieces;
   int64_t piece_tokens;
 };
+// How a call of more than kPermuteSmallSlots slots is cut: blocks of 4 to 64
+// tokens whose slots one wave ranks (64 of them at a time), pieces of whole
+// blocks.
+struct PermutePlan {
+  int block_tokens, pieces;
+  int64_t piece_tokens;
+  bool scan;
+};
+inline PermutePlan permute_plan(int64_t T, int k) {
+  PermutePlan p;
+  int64_t bt = (T + 1023) / 1024;
+  const int64_t most = 64 / k > 4 ? 64 / k : 4;
+  bt = bt < 4 ? 4 : bt > most ? most : bt;
+  const int64_t blocks = (T + bt - 1) / bt;
+  int64_t per_piece = (blocks + kPermutePieces - 1) / kPermutePieces;
+  const int64_t limit = kPermutePieceSlots / (bt * k) > 1 ? kPermutePieceSlots / (bt * k) : 1;
+  p.scan = per_piece > limit;
+  if (p.scan) per_piece = limit;
+  p.block_tokens = (int)bt;
+  p.piece_tokens = per_piece * bt;
+  p.pieces = (int)((blocks + per_piece - 1) / per_piece);
+  return p;
+}
+// Ints of the counts for up to T tokens: no T' <= T has more pieces.
+inline size_t permute_count_ints(int64_t T, int k, int E) {
+  const int64_t bt = 64 / k > 4 ? 64 / k : 4;
+  const int64_t limit = kPermutePieceSlots / (bt * k) > 1 ? kPermutePieceSlots / (bt * k) : 1;
+  const int64_t scanned = (T + limit * bt - 1) / (limit * bt);
+  return (size_t)((scanned > kPermutePieces ? scanned : kPermutePieces) + 1) * (size_t)E;
+}
 hipError_t launch_permute(PermuteArgs a, hipStream_t s);
 
 struct UnpermuteArgs {
@@ -346,34 +377,34 @@ struct RouterGradArgs {
   const uint16_t* dx_add;     // null: zero
   uint16_t* dx;
   float* drouter_w;
-  int32_t* slot_e;            // [T][k] expert of the slot, -1: no part in drouter_w
-  float* slot_dl;             // [T][k] gradient of the slot's logit
-  float* part;                // [splits][E][H]
+  float* part;                // [splits][E][H], unless there is one stretch
   int splits, split_tokens;
 };
-// Stretches of tokens whose shares of drouter_w are summed apart: enough waves
-// (one per 128 columns and stretch) to fill the chip, stretches long enough
-// that writing and reading the shares stays small beside reading x.
+// Stretches of tokens whose shares of drouter_w are summed apart.  A share
+// costs E H fp32 values written and read, so a stretch is 32 E tokens (512 at
+// least, 4096 at most): that is 16 bytes of shares for every 64 of x.  Shorter
+// ones, down to 64 tokens, where there would be fewer than 512 blocks.
 struct RouterGradPlan {
   int splits, split_tokens;
-  size_t slot_e, slot_dl, part, total;   // workspace offsets
+  size_t bytes;   // workspace
 };
-inline RouterGradPlan router_grad_plan(int H, int E, int k, int T) {
+inline RouterGradPlan router_grad_plan(int H, int E, int64_t T) {
   RouterGradPlan p;
-  const int64_t columns = (H + 127) / 128;
-  const int64_t least = 4 * E < 16 ? 16 : 4 * E < 512 ? 4 * E : 512;
-  const int64_t fill = ((int64_t)T * columns + 2047) / 2048;
-  const int64_t tokens = fill > least ? fill : least;
+  const int64_t blocks = (int64_t)E * ((H + 2047) / 2048);          // of one stretch
+  int64_t base = E <= 16 ? 512 : E <= 128 ? 32 * E : 4096;
+  if (base < (T + 4095) / 4096) base = (T + 4095) / 4096;           // at most 4096 stretches
+  const int64_t fill = (511 + blocks) / blocks;                     // stretches that make 512 blocks
+  int64_t tokens = base;
+  if ((T + base - 1) / base < fill) {
+    tokens = ((T + fill - 1) / fill + 63) / 64 * 64;
+    if (tokens < 64) tokens = 64;
+  }
   p.split_tokens = (int)tokens;
   p.splits = (int)((T + tokens - 1) / tokens);
   // no T' <= T has more stretches than this, so a workspace for T serves them all
-  const int64_t by_tokens = (T + least - 1) / least, by_fill = (2048 + columns - 1) / columns;
-  const int64_t most = by_tokens < by_fill ? by_tokens : by_fill;
-  size_t off = 0;
-  p.slot_e = off;  off = align_up(off + sizeof(int32_t) * (size_t)T * k, kAlign);
-  p.slot_dl = off; off = align_up(off + sizeof(float) * (size_t)T * k, kAlign);
-  p.part = off;    off = align_up(off + sizeof(float) * (size_t)most * E * H, kAlign);
-  p.total = off;
+  const int64_t by_fill = fill < (T + 63) / 64 ? fill : (T + 63) / 64, by_base = (T + base - 1) / base;
+  const int64_t most = by_fill > by_base ? by_fill : by_base;
+  p.bytes = align_up(sizeof(float) * (size_t)most * E * H + 1, kAlign);
   return p;
 }
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);

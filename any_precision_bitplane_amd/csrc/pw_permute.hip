@@ -24,27 +24,35 @@ __device__ __forceinline__ uint32_t expert_of(int32_t id, int E) {
   return (uint32_t)id < (uint32_t)E ? (uint32_t)id : kDropped;
 }
 
-// Copies token t's row (and its scales) to the places pos[0..k), -1: none.
-// `lanes` threads share the row.
-__device__ __forceinline__ void scatter_row(const PermuteArgs& a, int t, const int* pos, int lane, int lanes) {
-  const uint8_t* src = a.x + (int64_t)t * a.x_stride;
-  constexpr int U = 4;   // chunks requested together
-  const int64_t step = 16 * (int64_t)lanes;
-  for (int64_t c0 = 16 * (int64_t)lane; c0 < a.row_bytes; c0 += U * step) {
-    uint4 v[U];
+constexpr int kUnroll = 4;   // 16-byte pieces of a row requested together
+typedef uint32_t piece_t __attribute__((ext_vector_type(4)));
+
+// Up to kUnroll pieces of token t's row, `lanes` threads apart, from byte c0 on.
+__device__ __forceinline__ void load_pieces(const PermuteArgs& a, int64_t t, int64_t c0, int lanes,
+                                            piece_t (&v)[kUnroll]) {
+  const uint8_t* src = a.x + t * a.x_stride + c0;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + u * step < a.row_bytes) v[u] = *reinterpret_cast<const uint4*>(src + c0 + u * step);
-    for (int j = 0; j < a.k; ++j) {
-      if (pos[j] < 0) continue;
-      uint8_t* dst = a.xs + pos[j] * a.xs_stride + c0;
+  for (int u = 0; u < kUnroll; ++u)
+    v[u] = c0 + u * 16 * lanes < a.row_bytes ? *reinterpret_cast<const piece_t*>(src + u * 16 * lanes)
+                                             : piece_t{0u, 0u, 0u, 0u};
+}
+
+// ... and their copies at the places pos[0..k), -1: none.
+__device__ __forceinline__ void store_pieces(const PermuteArgs& a, const int* pos, int64_t c0, int lanes,
+                                             const piece_t (&v)[kUnroll]) {
+  for (int j = 0; j < a.k; ++j) {
+    const int p = uniform(pos[j]);
+    if (p < 0) continue;
+    uint8_t* dst = a.xs + p * a.xs_stride + c0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (c0 + u * step < a.row_bytes) *reinterpret_cast<uint4*>(dst + u * step) = v[u];
-    }
+    for (int u = 0; u < kUnroll; ++u)
+      if (c0 + u * 16 * lanes < a.row_bytes) *reinterpret_cast<piece_t*>(dst + u * 16 * lanes) = v[u];
   }
+}
+
+__device__ __forceinline__ void scatter_scales(const PermuteArgs& a, int64_t t, const int* pos, int lane, int lanes) {
   for (int g = lane; g < a.groups; g += lanes) {
-    const float v = a.x_scale[(int64_t)t * a.groups + g];
+    const float v = a.x_scale[t * a.groups + g];
     for (int j = 0; j < a.k; ++j)
       if (pos[j] >= 0) a.xs_scale[(int64_t)pos[j] * a.groups + g] = v;
   }
@@ -53,7 +61,7 @@ __device__ __forceinline__ void scatter_row(const PermuteArgs& a, int t, const i
 // Few slots: one launch.  Every block takes one token and finds its slots'
 // places itself, by counting the slots that sort before each (ids in LDS, one
 // wave per place).  The E + 1 expert offsets are counted the same way, spread
-// over the blocks.
+// over the blocks.  The row is requested before any of that.
 __global__ __launch_bounds__(kThreads) void permute_small_kernel(PermuteArgs a) {
   extern __shared__ uint32_t shared[];
   uint32_t* ids = shared;                                  // [S rounded up to a wave]
@@ -62,6 +70,8 @@ __global__ __launch_bounds__(kThreads) void permute_small_kernel(PermuteArgs a) 
   int* pos = reinterpret_cast<int*>(shared + padded);      // [k]
   const int t = blockIdx.x;
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
+  piece_t v[kUnroll];
+  load_pieces(a, t, 16 * (int64_t)threadIdx.x, kThreads, v);
   bool bad = false;
   for (int i = threadIdx.x; i < padded; i += kThreads) {
     const uint32_t e = i < S ? expert_of(a.ids[i], a.E) : kDropped;
@@ -91,7 +101,12 @@ __global__ __launch_bounds__(kThreads) void permute_small_kernel(PermuteArgs a) 
     }
   }
   __syncthreads();
-  scatter_row(a, t, pos, threadIdx.x, kThreads);
+  constexpr int64_t kPiece = (int64_t)kUnroll * kThreads * 16;
+  for (int64_t c0 = 16 * (int64_t)threadIdx.x; c0 < a.row_bytes; c0 += kPiece) {
+    if (c0 >= kPiece) load_pieces(a, t, c0, kThreads, v);
+    store_pieces(a, pos, c0, kThreads, v);
+  }
+  scatter_scales(a, t, pos, threadIdx.x, kThreads);
 }
 
 // Many slots, first launch: slots per expert in each of the pieces.
@@ -110,40 +125,67 @@ __global__ __launch_bounds__(1024) void permute_count_kernel(PermuteArgs a) {
   }
   if (bad && a.status) raise_status(a.status, PW_DEV_BAD_EXPERT_ID);
   __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += 1024) a.counts[blockIdx.x * a.E + e] = count[e];
+  for (int e = threadIdx.x; e < a.E; e += 1024) a.counts[(int64_t)blockIdx.x * a.E + e] = count[e];
 }
 
-// Second launch: a block takes block_tokens tokens of one piece.  An expert's
+// With many pieces their counts become sums in a launch of its own, a wave per
+// expert: counts[p][e] turns into the expert's slots in the pieces before p, and
+// one more row, counts[pieces][e], holds its slots in all of them.
+__global__ __launch_bounds__(kWave) void permute_scan_kernel(PermuteArgs a) {
+  const int e = blockIdx.x, lane = threadIdx.x;
+  int carry = 0;
+  for (int p0 = 0; p0 < a.pieces; p0 += kWave) {
+    const int p = p0 + lane;
+    const int c = p < a.pieces ? a.counts[(int64_t)p * a.E + e] : 0;
+    int inclusive = c;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int y = __shfl_up(inclusive, d, kWave);
+      if (lane >= d) inclusive += y;
+    }
+    if (p < a.pieces) a.counts[(int64_t)p * a.E + e] = carry + inclusive - c;
+    carry += __shfl(inclusive, kWave - 1, kWave);
+  }
+  if (lane == 0) a.counts[(int64_t)a.pieces * a.E + e] = carry;
+}
+
+// Last launch: a block takes block_tokens tokens of one piece.  An expert's
 // slots of this block start at its offset plus its slots in earlier pieces and
 // in earlier blocks of the piece (counted again here); inside the block a
-// slot's rank is its position among the equal ids, found by ballots.
+// slot's rank is its position among the equal ids, found by ballots of one
+// wave.  Each wave requests its first token's row before all that.
+template <bool SCANNED>
 __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a) {
-  __shared__ int total[kWaves][kMaxExperts];
-  __shared__ int before[kWaves][kMaxExperts];
-  __shared__ int next[kMaxExperts];          // the expert's next place in this block
-  __shared__ int wcnt[kWaves][kMaxExperts];
+  __shared__ int total[kMaxExperts];         // the expert's slots
+  __shared__ int next[kMaxExperts];          // its slots before this block, then its next place
   extern __shared__ uint32_t shared[];
   int* pos = reinterpret_cast<int*>(shared); // [block_tokens * k]
   const int tid = threadIdx.x;
   const int wave = uniform(tid / kWave), lane = tid & (kWave - 1);
   const int64_t t0 = (int64_t)blockIdx.x * a.block_tokens;
   const int nt = (int)(a.T - t0 < a.block_tokens ? a.T - t0 : a.block_tokens);
-  const int piece = (int)(t0 / a.piece_tokens);
+  const int slots = nt * a.k;
+  const int64_t piece = t0 / a.piece_tokens;
 
-  for (int e = lane; e < a.E; e += kWave) {
-    int all = 0, prior = 0;
-#pragma unroll 8
-    for (int p = wave; p < a.pieces; p += kWaves) {
-      const int c = a.counts[p * a.E + e];
-      all += c;
-      prior += p < piece ? c : 0;
-    }
-    total[wave][e] = all;
-    before[wave][e] = prior;
+  piece_t v[kUnroll];
+  if (wave < nt) load_pieces(a, t0 + wave, 16 * (int64_t)lane, kWave, v);
+  for (int e = tid; e < a.E; e += kThreads) {
+    total[e] = SCANNED ? a.counts[(int64_t)a.pieces * a.E + e] : 0;
+    next[e] = SCANNED ? a.counts[piece * a.E + e] : 0;
   }
-  for (int e = tid; e < a.E; e += kThreads) next[e] = 0;
   __syncthreads();
-  for (int64_t s = (int64_t)piece * a.piece_tokens * a.k + tid; s < t0 * a.k; s += kThreads) {
+  if constexpr (!SCANNED) {
+    const int n = a.pieces * a.E, mine = (int)piece * a.E;   // at most 64 pieces
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThreads) {
+      const int c = a.counts[i], e = i % a.E;
+      if (c == 0) continue;
+      atomicAdd(&total[e], c);
+      if (i < mine) atomicAdd(&next[e], c);
+    }
+  }
+#pragma unroll 4
+  for (int64_t s = piece * a.piece_tokens * a.k + tid; s < t0 * a.k; s += kThreads) {
     const uint32_t e = expert_of(a.ids[s], a.E);
     if (e != kDropped) atomicAdd(&next[e], 1);
   }
@@ -153,10 +195,7 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = 4 * lane + i;
-      c[i] = 0;
-      if (e < a.E)
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) c[i] += total[w][e];
+      c[i] = e < a.E ? total[e] : 0;
       sum += c[i];
     }
     int inclusive = sum;
@@ -171,51 +210,42 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
       const int e = 4 * lane + i;
       if (e < a.E) {
         if (blockIdx.x == 0) a.offsets[e] = off;
-        int start = off + next[e];
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) start += before[w][e];
-        next[e] = start;
+        next[e] += off;
       }
       off += c[i];
     }
     if (lane == kWave - 1 && blockIdx.x == 0) a.offsets[a.E] = inclusive;
+    __builtin_amdgcn_wave_barrier();
+    for (int r0 = 0; r0 < slots; r0 += kWave) {
+      const int s = r0 + lane;
+      const uint32_t e = s < slots ? expert_of(a.ids[t0 * a.k + s], a.E) : kDropped;
+      unsigned long long same = __ballot(e != kDropped);
+      for (int bit = 0; (1 << bit) < a.E; ++bit) {
+        const unsigned long long ones = __ballot(e != kDropped && ((e >> bit) & 1));
+        same &= ((e >> bit) & 1) ? ones : ~ones;
+      }
+      const int rank = __popcll(same & ((1ull << lane) - 1ull));
+      const int start = e != kDropped ? next[e] : 0;
+      __builtin_amdgcn_wave_barrier();
+      if (e != kDropped && rank == 0) next[e] = start + __popcll(same);
+      __builtin_amdgcn_wave_barrier();
+      if (s < slots) {
+        const int p = e == kDropped ? -1 : start + rank;
+        pos[s] = p;
+        a.inv[t0 * a.k + s] = p;
+        if (p >= 0 && a.perm) a.perm[p] = (int32_t)(t0 * a.k + s);
+      }
+    }
   }
   __syncthreads();
-
-  const int slots = nt * a.k;
-  for (int r0 = 0; r0 < slots; r0 += kThreads) {
-    for (int i = tid; i < kWaves * a.E; i += kThreads) wcnt[i / a.E][i % a.E] = 0;
-    __syncthreads();
-    const int s = r0 + tid;
-    const uint32_t e = s < slots ? expert_of(a.ids[t0 * a.k + s], a.E) : kDropped;
-    unsigned long long same = __ballot(e != kDropped);
-    for (int bit = 0; (1 << bit) < a.E; ++bit) {
-      const unsigned long long ones = __ballot(e != kDropped && ((e >> bit) & 1));
-      same &= ((e >> bit) & 1) ? ones : ~ones;
+  constexpr int64_t kPiece = (int64_t)kUnroll * kWave * 16;
+  for (int t = wave; t < nt; t += kWaves) {
+    for (int64_t c0 = 16 * (int64_t)lane; c0 - 16 * lane < a.row_bytes; c0 += kPiece) {
+      if (t != wave || c0 >= kPiece) load_pieces(a, t0 + t, c0, kWave, v);
+      store_pieces(a, pos + t * a.k, c0, kWave, v);
     }
-    const int rank = __popcll(same & ((1ull << lane) - 1ull));
-    if (e != kDropped && rank == 0) wcnt[wave][e] = __popcll(same);
-    __syncthreads();
-    for (int x = tid; x < a.E; x += kThreads) {
-      int run = next[x];
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const int c = wcnt[w][x];
-        wcnt[w][x] = run;
-        run += c;
-      }
-      next[x] = run;
-    }
-    __syncthreads();
-    if (s < slots) {
-      const int p = e == kDropped ? -1 : wcnt[wave][e] + rank;
-      pos[s] = p;
-      a.inv[t0 * a.k + s] = p;
-      if (p >= 0 && a.perm) a.perm[p] = (int32_t)(t0 * a.k + s);
-    }
-    __syncthreads();
+    if (a.groups) scatter_scales(a, t0 + t, pos + t * a.k, lane, kWave);
   }
-  for (int t = wave; t < nt; t += kWaves) scatter_row(a, (int)t0 + t, pos + t * a.k, lane, kWave);
 }
 
 // y[t] = sum_j w[t][j] rows[inv[t k + j]]; w null: ones.  `lanes` threads (a
@@ -278,7 +308,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_grad_kernel(UnpermuteGradA
       const elem* dy = static_cast<const elem*>(a.dy) + s / a.k * a.dy_stride;
       const elem* row = static_cast<const elem*>(a.rows) + p * a.rows_stride;
       elem* drow = static_cast<elem*>(a.drows) + p * a.drows_stride;
-      constexpr int U = 4;   // chunks requested together
+      constexpr int U = DT == PW_F32 ? 2 : 4;   // chunks requested together (fp32: registers)
       for (int c0 = lane; c0 < C; c0 += U * lanes) {
         typename R::chunk d[U], r[U];
 #pragma unroll
@@ -344,20 +374,23 @@ hipError_t launch_permute(PermuteArgs a, hipStream_t s) {
     hipLaunchKernelGGL(permute_small_kernel, dim3(a.T), dim3(kThreads), lds, s, a);
     return hipGetLastError();
   }
-  // about 1024 blocks of at least two and at most 32 tokens (positions in LDS), pieces of whole blocks
-  int64_t bt = ((int64_t)a.T + 1023) / 1024;
-  bt = bt < 2 ? 2 : bt > 32 ? 32 : bt;
-  if (bt < a.T / (int64_t)kMaxGrid) bt = a.T / (int64_t)kMaxGrid + 1;
-  const int64_t blocks = (a.T + bt - 1) / bt;
-  const int64_t per_piece = (blocks + kPermutePieces - 1) / kPermutePieces;
-  a.block_tokens = (int)bt;
-  a.piece_tokens = per_piece * bt;
-  a.pieces = (int)((blocks + per_piece - 1) / per_piece);
-  hipLaunchKernelGGL(permute_count_kernel, dim3(a.pieces), dim3(1024), 0, s, a);
+  const PermutePlan p = permute_plan(a.T, a.k);
+  a.block_tokens = p.block_tokens;
+  a.piece_tokens = p.piece_tokens;
+  a.pieces = p.pieces;
+  const int64_t blocks = ((int64_t)a.T + p.block_tokens - 1) / p.block_tokens;
+  hipLaunchKernelGGL(permute_count_kernel, dim3(p.pieces), dim3(1024), 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(permute_scatter_kernel, dim3((unsigned)blocks), dim3(kThreads), (size_t)bt * a.k * sizeof(int), s,
-                     a);
+  const size_t lds = (size_t)p.block_tokens * a.k * sizeof(int);
+  if (!p.scan) {
+    hipLaunchKernelGGL(permute_scatter_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(permute_scan_kernel, dim3(a.E), dim3(kWave), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(permute_scatter_kernel<true>, dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
   return hipGetLastError();
 }
 

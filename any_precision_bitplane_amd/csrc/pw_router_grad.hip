@@ -8,99 +8,166 @@
 // in fp32.  A dropped slot (id outside [0, E)) takes no part, in the inner sum
 // either.
 //
-// Three kernels.  dx: one pass over dx_add and dx, the router's rows coming
-// from L2; it leaves each slot's dl and expert behind.  dWr: a wave owns 128
-// columns and a stretch of tokens and keeps dWr[0..E) of its columns in LDS,
-// so x is read once whatever k is and no two lanes ever add to the same
-// word (no atomics: the same inputs give the same bits).  Then the stretches'
-// shares are summed in order.
+// One launch for both.  dWr: a block takes one expert, 2048 columns and a
+// stretch of tokens; its waves list the tokens that the expert serves, with
+// their dl, in LDS, then each sums 512 columns of the listed rows in registers
+// (no atomics: the same inputs give the same bits).  A row is read by each of
+// its k experts, so the blocks of one stretch and its columns go to one XCD,
+// whose L2 serves all but the first.  dx: a wave takes a token; the router's
+// rows come from L2.  With several stretches a second launch sums their shares
+// in order.
 #include "pw_rows.h"
 
 namespace pw {
 
 namespace {
 
-constexpr unsigned kMaxGrid = 1u << 20;
 constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / kWave;
+constexpr int kListed = 512;             // tokens whose matches a block lists at a time
+constexpr int kSegment = kListed / kWaves;
+constexpr int kXcds = 8;                 // consecutive blocks go to the XCDs in turn
 
-__global__ __launch_bounds__(kThreads) void router_grad_x_kernel(RouterGradArgs a, int shift) {
+struct Listed {
+  int32_t t;
+  float dl;
+};
+
+// The token's dl for expert e, summed over the slots that hold e (`hit`: there is one).
+__device__ __forceinline__ float token_dl(const RouterGradArgs& a, int64_t t, int e, bool& hit) {
+  const int32_t* ids = a.ids + t * a.k;
+  const float* w = a.w + t * a.k;
+  const float* dw = a.dw + t * a.k;
+  hit = false;
+  float mean = 0.f, sum_w = 0.f, sum_wdw = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < a.k; ++j) {
+    const int32_t id = ids[j];
+    const float wj = w[j], wdw = wj * dw[j];
+    if ((uint32_t)id < (uint32_t)a.E) mean += wdw;
+    if (id == e) {
+      hit = true;
+      sum_w += wj;
+      sum_wdw += wdw;
+    }
+  }
+  return sum_wdw - sum_w * mean;
+}
+
+__device__ __forceinline__ void router_grad_w(const RouterGradArgs& a, int block) {
   using R = Row<PW_F16>;
-  const int C = a.H / 8;
-  const int lanes = 1 << shift;
-  const int per_block = kThreads >> shift;
-  const int lane = (int)threadIdx.x & (lanes - 1);
-  for (int64_t t = (int64_t)blockIdx.x * per_block + ((int)threadIdx.x >> shift); t < a.T;
-       t += (int64_t)gridDim.x * per_block) {
-    const int32_t* ids = a.ids + t * a.k;
-    const float* w = a.w + t * a.k;
-    const float* dw = a.dw + t * a.k;
-    float mean = 0.f;
-    for (int j = 0; j < a.k; ++j)
-      if ((uint32_t)ids[j] < (uint32_t)a.E) mean = __builtin_fmaf(w[j], dw[j], mean);
-    for (int c = lane; c < C; c += lanes) {
-      floatx8 acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (a.dx_add) acc = R::wide(R::load(reinterpret_cast<const _Float16*>(a.dx_add) + t * a.H + 8 * c));
-      for (int j = 0; j < a.k; ++j) {
-        const int32_t e = ids[j];
-        if ((uint32_t)e >= (uint32_t)a.E) continue;
-        const float dl = w[j] * (dw[j] - mean);
-        acc += dl * R::wide(R::load(reinterpret_cast<const _Float16*>(a.router_w) + (int64_t)e * a.H + 8 * c));
-      }
-      R::store(reinterpret_cast<_Float16*>(a.dx) + t * a.H + 8 * c, R::narrow(acc));
-    }
-    // a token that lists an expert twice keeps the sum in the first of the two slots
-    for (int j = lane; j < a.k; j += lanes) {
-      int32_t e = (uint32_t)ids[j] < (uint32_t)a.E ? ids[j] : -1;
+  __shared__ Listed list[kWaves][kSegment];
+  __shared__ int listed[kWaves];
+  const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
+  const int columns = (a.H + 2047) / 2048;
+  const int r = block / kXcds;
+  const int e = r % a.E;
+  const int tile = r / a.E * kXcds + block % kXcds;
+  if (tile >= columns * a.splits) return;
+  const int split = tile / columns;
+  const int col = (tile % columns) * 2048 + wave * 512 + 8 * lane;
+  const bool in = col < a.H;
+  const int64_t t0 = (int64_t)split * a.split_tokens;
+  const int64_t t1 = t0 + a.split_tokens < a.T ? t0 + a.split_tokens : a.T;
+  const _Float16* x = reinterpret_cast<const _Float16*>(a.x) + (in ? col : 0);
+  floatx8 sum = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t c0 = t0; c0 < t1; c0 += kListed) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kSegment / kWave; ++i) {
+      const int64_t t = c0 + wave * kSegment + i * kWave + lane;
+      bool hit = false;
       float dl = 0.f;
-      for (int i = 0; i < a.k; ++i) {
-        if (e < 0 || ids[i] != e) continue;
-        if (i < j) {
-          e = -1;
-          break;
-        }
-        dl += w[i] * (dw[i] - mean);
-      }
-      a.slot_e[t * a.k + j] = e;
-      a.slot_dl[t * a.k + j] = dl;
+      if (t < t1) dl = token_dl(a, t, e, hit);
+      const unsigned long long mask = __ballot(hit);
+      if (hit) list[wave][n + __popcll(mask & ((1ull << lane) - 1ull))] = Listed{(int32_t)t, dl};
+      n += __popcll(mask);
     }
+    if (lane == 0) listed[wave] = n;
+    __syncthreads();
+    floatx8 acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};   // of at most kListed rows
+    for (int s = 0; s < kWaves; ++s) {
+      const int m = uniform(listed[s]);
+      constexpr int U = 8;   // rows requested together
+      for (int i = 0; i < m; i += U) {
+        typename R::chunk v[U];
+        float dl[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const Listed l = list[s][i + u < m ? i + u : m - 1];
+          dl[u] = i + u < m ? l.dl : 0.f;
+          v[u] = R::load(x + (int64_t)uniform(l.t) * a.H);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (i + u < m) acc += dl[u] * R::wide(v[u]);
+      }
+    }
+    sum += acc;
+    __syncthreads();
+  }
+  if (in) Row<PW_F32>::store((a.splits > 1 ? a.part : a.drouter_w) + ((int64_t)split * a.E + e) * a.H + col, sum);
+}
+
+// Lane j holds slot j (k <= 64): its expert and dl, handed to the wave one by one.
+__device__ __forceinline__ void router_grad_x(const RouterGradArgs& a, int64_t t) {
+  using R = Row<PW_F16>;
+  const int lane = (int)threadIdx.x & (kWave - 1);
+  const int C = a.H / 8;
+  int32_t id = -1;
+  float w = 0.f, wdw = 0.f;
+  if (lane < a.k) {
+    id = a.ids[t * a.k + lane];
+    w = a.w[t * a.k + lane];
+    wdw = w * a.dw[t * a.k + lane];
+  }
+  const bool kept = (uint32_t)id < (uint32_t)a.E;
+  const _Float16* add = reinterpret_cast<const _Float16*>(a.dx_add) + t * a.H;
+  const _Float16* wr = reinterpret_cast<const _Float16*>(a.router_w);
+  _Float16* dx = reinterpret_cast<_Float16*>(a.dx) + t * a.H;
+  constexpr int U = 4;   // chunks of a row requested together
+  typename R::chunk v[U];
+  if (a.dx_add)
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (lane + u * kWave < C) v[u] = R::load(add + 8 * (lane + u * kWave));
+  const float mean = wave_sum(kept ? wdw : 0.f);
+  const float dl = kept ? wdw - w * mean : 0.f;
+  for (int c0 = lane; c0 - lane < C; c0 += U * kWave) {
+    floatx8 acc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (a.dx_add && c0 >= U * kWave && c0 + u * kWave < C) v[u] = R::load(add + 8 * (c0 + u * kWave));
+      acc[u] = floatx8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (a.dx_add && c0 + u * kWave < C) acc[u] = R::wide(v[u]);
+    }
+    for (int j = 0; j < a.k; ++j) {
+      const int32_t e = __builtin_amdgcn_readlane(id, j);
+      if ((uint32_t)e >= (uint32_t)a.E) continue;
+      const float f = row_lane(dl, j);
+      const _Float16* row = wr + (int64_t)e * a.H;
+      typename R::chunk m[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * kWave < C) m[u] = R::load(row + 8 * (c0 + u * kWave));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * kWave < C) acc[u] += f * R::wide(m[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * kWave < C) R::store(dx + 8 * (c0 + u * kWave), R::narrow(acc[u]));
   }
 }
 
-// One wave: columns [128 cb, 128 cb + 128), two a lane, tokens [t0, t1).
-__global__ __launch_bounds__(kWave) void router_grad_w_kernel(RouterGradArgs a) {
-  extern __shared__ float acc[];   // [E][128]
-  typedef float floatx2 __attribute__((ext_vector_type(2)));
-  constexpr int U = 16;            // tokens requested together
-  const int lane = threadIdx.x;
-  const int col = (int)blockIdx.x * 128 + 2 * lane;
-  const bool in = col < a.H;
-  const int64_t t0 = (int64_t)blockIdx.y * a.split_tokens;
-  const int64_t t1 = t0 + a.split_tokens < a.T ? t0 + a.split_tokens : a.T;
-  floatx2* mine = reinterpret_cast<floatx2*>(acc) + lane;
-  for (int e = 0; e < a.E; ++e) mine[e * kWave] = floatx2{0.f, 0.f};
-  const _Float16* x = reinterpret_cast<const _Float16*>(a.x) + (in ? col : 0);
-  for (int64_t tb = t0; tb < t1; tb += U) {
-    half2_t v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t t = tb + u < t1 ? tb + u : t1 - 1;
-      v[u] = *reinterpret_cast<const half2_t*>(x + t * a.H);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (tb + u >= t1) break;
-      const floatx2 xv = {(float)v[u][0], (float)v[u][1]};
-      const int64_t s = (tb + u) * a.k;
-      for (int j = 0; j < a.k; ++j) {
-        const int e = a.slot_e[s + j];
-        if (e < 0) continue;
-        mine[e * kWave] += a.slot_dl[s + j] * xv;
-      }
-    }
+__global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradArgs a, int w_blocks) {
+  if ((int)blockIdx.x < w_blocks) {
+    router_grad_w(a, (int)blockIdx.x);
+    return;
   }
-  if (!in) return;
-  float* out = a.part + (size_t)blockIdx.y * a.E * a.H + col;
-  for (int e = 0; e < a.E; ++e) *reinterpret_cast<floatx2*>(out + (size_t)e * a.H) = mine[e * kWave];
+  const int64_t step = (int64_t)(gridDim.x - w_blocks) * kWaves;
+  for (int64_t t = (int64_t)(blockIdx.x - w_blocks) * kWaves + uniform((int)threadIdx.x / kWave); t < a.T; t += step)
+    router_grad_x(a, t);
 }
 
 __global__ __launch_bounds__(kThreads) void router_grad_join_kernel(RouterGradArgs a) {
@@ -116,18 +183,14 @@ __global__ __launch_bounds__(kThreads) void router_grad_join_kernel(RouterGradAr
 }  // namespace
 
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
-  int shift = 0;
-  while ((1 << shift) < a.H / 8 && (1 << shift) < kThreads) ++shift;
-  const int per_block = kThreads >> shift;
-  const int64_t blocks = ((int64_t)a.T + per_block - 1) / per_block;
-  hipLaunchKernelGGL(router_grad_x_kernel, dim3((unsigned)(blocks < (int64_t)kMaxGrid ? blocks : (int64_t)kMaxGrid)),
-                     dim3(kThreads), 0, s, a, shift);
+  const int columns = (a.H + 2047) / 2048;
+  const int w_blocks = (columns * a.splits + kXcds - 1) / kXcds * kXcds * a.E;
+  const int64_t x_blocks = ((int64_t)a.T + kWaves - 1) / kWaves;
+  constexpr int64_t kMost = 1 << 20;
+  hipLaunchKernelGGL(router_grad_kernel, dim3((unsigned)(w_blocks + (x_blocks < kMost ? x_blocks : kMost))),
+                     dim3(kThreads), 0, s, a, w_blocks);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(router_grad_w_kernel, dim3((a.H + 127) / 128, a.splits), dim3(kWave),
-                     (size_t)a.E * 128 * sizeof(float), s, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || a.splits == 1) return e;
   const int64_t quads = (int64_t)a.E * a.H / 4;
   hipLaunchKernelGGL(router_grad_join_kernel, dim3((unsigned)((quads + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
                      a);

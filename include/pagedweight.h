@@ -417,7 +417,8 @@ size_t pw_moe_permute_workspace_bytes(const pw_moe_shape* shape /* host */, int3
  *   inv      int32 [T*k];  perm  int32 [T*k] or NULL: perm[inv[s]] = s, from
  *            offsets[E] on left as it was
  *   status   device uint32 or NULL: PW_DEV_* bits are OR-ed into it
- * One launch for up to 4096 slots, two above.  T == 0 sets offsets to zero. */
+ * One launch for up to 4096 slots, two above (three from about half a million
+ * on).  T == 0 sets offsets to zero. */
 pw_status pw_moe_permute(const pw_moe_shape* shape /* host */, int32_t T, int32_t dtype, const void* x,
                          int64_t x_stride, const float* x_scale, int32_t groups, const int32_t* ids, void* xs,
                          int64_t xs_stride, float* xs_scale, int32_t* offsets, int32_t* inv, int32_t* perm,
@@ -464,7 +465,7 @@ size_t pw_router_backward_workspace_bytes(const pw_moe_shape* shape /* host */, 
  *              pw_moe_permute_backward writes)
  *   dx         fp16 [T][H], overwritten; may be dx_add itself
  *   drouter_w  fp32 [E][H], 16-byte aligned, overwritten (zero for T == 0)
- * Three launches. */
+ * Two launches (one for up to 64 tokens). */
 pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, const uint16_t* x,
                              const uint16_t* router_w, const int32_t* ids, const float* w, const float* dw,
                              const uint16_t* dx_add, uint16_t* dx, float* drouter_w, void* workspace,

@@ -230,7 +230,8 @@ SORT_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd"
               ("more_experts_than_tokens", 3, 64, 200, 2, 0.0), ("edge_4096", 1024, 96, 60, 4, 0.1),
               ("above_4096", 1025, 96, 60, 4, 0.1), ("one_expert", 5000, 64, 1, 1, 0.0), ("large", 4099, 160, 8, 2, 0.05),
               ("E256_k8", 1500, 64, 256, 8, 0.2), ("E256_k256_large", 40, 32, 256, 256, 0.1),
-              ("all_dropped_large", 5001, 32, 9, 1, 1.0), ("k7", 3001, 64, 33, 7, 0.5)]
+              ("all_dropped_large", 5001, 32, 9, 1, 1.0), ("k7", 3001, 64, 33, 7, 0.5),
+              ("scanned", 140003, 32, 60, 4, 0.1), ("scanned_k64", 9001, 32, 256, 64, 0.1)]
 
 
 def draw_ids(seed, T, E, k, dropped):
