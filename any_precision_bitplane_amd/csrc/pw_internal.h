@@ -378,32 +378,42 @@ struct RouterGradArgs {
   uint16_t* dx;
   float* drouter_w;
   float* part;                // [splits][E][H], unless there is one stretch
-  int splits, split_tokens;
+  int splits;
+  int64_t split_slots;
+  int shift;                  // log2 of the lanes that share a row (H < 512)
+  int cshift;                 // log2 of a block's waves that take different columns
 };
-// Stretches of tokens whose shares of drouter_w are summed apart.  A share
-// costs E H fp32 values written and read, so a stretch is 32 E tokens (512 at
-// least, 4096 at most): that is 16 bytes of shares for every 64 of x.  Shorter
-// ones, down to 64 tokens, where there would be fewer than 512 blocks.
+// How drouter_w is cut.  A block takes an expert, 512 << cshift columns and one
+// stretch of the slots; the stretches' shares are summed apart.
+// - Columns: with up to 8192 slots a block's four waves share the rows of 512
+//   columns (a few-block call is as long as its longest list: skewed T = 256,
+//   E = 60: 9 us against 19), above they take 512 columns each, so that the
+//   ids are looked through once for 2048 (T = 16384, E = 256, top-8: 99 us
+//   against 214).
+// - Stretches: as many as make 4096 blocks (2048: T = 32768, E = 60 with skewed
+//   routing 177 us against 146), but of at least 1024 slots (512: 10.6 us
+//   against 8.2 at T = 256), and of at least 4 E tokens, since a share is E H fp32
+//   values written and read (none: T = 2970, E = 155 37 us against 27).
 struct RouterGradPlan {
-  int splits, split_tokens;
+  int splits;
+  int64_t split_slots;
+  int shift, cshift;
   size_t bytes;   // workspace
 };
-inline RouterGradPlan router_grad_plan(int H, int E, int64_t T) {
+inline RouterGradPlan router_grad_plan(int H, int E, int k, int64_t T) {
   RouterGradPlan p;
-  const int64_t blocks = (int64_t)E * ((H + 2047) / 2048);          // of one stretch
-  int64_t base = E <= 16 ? 512 : E <= 128 ? 32 * E : 4096;
-  if (base < (T + 4095) / 4096) base = (T + 4095) / 4096;           // at most 4096 stretches
-  const int64_t fill = (511 + blocks) / blocks;                     // stretches that make 512 blocks
-  int64_t tokens = base;
-  if ((T + base - 1) / base < fill) {
-    tokens = ((T + fill - 1) / fill + 63) / 64 * 64;
-    if (tokens < 64) tokens = 64;
-  }
-  p.split_tokens = (int)tokens;
-  p.splits = (int)((T + tokens - 1) / tokens);
+  const int64_t S = T * k, by_shares = (int64_t)4 * E * k, least = by_shares > 1024 ? by_shares : 1024;
+  p.shift = 0;
+  while (p.shift < 6 && (8 << p.shift) < H) ++p.shift;
+  p.cshift = S <= 8192 ? 0 : 2;
+  while (p.cshift > 0 && (512 << p.cshift) / 2 >= H) --p.cshift;
+  const int64_t blocks = (int64_t)E * ((H + (512 << p.cshift) - 1) / (512 << p.cshift));          // of one stretch
+  const int64_t fill = (4095 + blocks) / blocks;
+  p.split_slots = (S + fill - 1) / fill;
+  p.split_slots = p.split_slots < least ? least : (p.split_slots + 255) / 256 * 256;
+  p.splits = (int)((S + p.split_slots - 1) / p.split_slots);
   // no T' <= T has more stretches than this, so a workspace for T serves them all
-  const int64_t by_fill = fill < (T + 63) / 64 ? fill : (T + 63) / 64, by_base = (T + base - 1) / base;
-  const int64_t most = by_fill > by_base ? by_fill : by_base;
+  const int64_t most = (S + least - 1) / least < 4096 ? (S + least - 1) / least : 4096;
   p.bytes = align_up(sizeof(float) * (size_t)most * E * H + 1, kAlign);
   return p;
 }

@@ -190,7 +190,7 @@ pw_status pw_moe_unpermute_backward(const pw_moe_shape* shape, int32_t T, int32_
 
 size_t pw_router_backward_workspace_bytes(const pw_moe_shape* shape, int32_t T_max) {
   if (pw_check_shape(shape, T_max) != PW_OK) return 0;
-  return router_grad_plan(shape->hidden, shape->num_experts, T_max).bytes;
+  return router_grad_plan(shape->hidden, shape->num_experts, shape->top_k, T_max).bytes;
 }
 
 pw_status pw_router_backward(const pw_moe_shape* shape, int32_t T, const uint16_t* x, const uint16_t* router_w,
@@ -206,10 +206,10 @@ pw_status pw_router_backward(const pw_moe_shape* shape, int32_t T, const uint16_
   if (!aligned(x, 16) || !aligned(router_w, 16) || !aligned(dx_add, 16) || !aligned(dx, 16) || !aligned(ids, 4) ||
       !aligned(w, 4) || !aligned(dw, 4) || !aligned(workspace, kAlign))
     return PW_ERR_ALIGNMENT;
-  const RouterGradPlan p = router_grad_plan(H, E, T);
+  const RouterGradPlan p = router_grad_plan(H, E, k, T);
   if (workspace_bytes < p.bytes) return PW_ERR_WORKSPACE;
   RouterGradArgs a{T, H, E, k, x, router_w, ids, w, dw, dx_add, dx, drouter_w, static_cast<float*>(workspace),
-                   p.splits, p.split_tokens};
+                   p.splits, p.split_slots, p.shift, p.cshift};
   return hip_status(launch_router_grad(a, (hipStream_t)stream));
 }
 

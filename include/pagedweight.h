@@ -465,7 +465,7 @@ size_t pw_router_backward_workspace_bytes(const pw_moe_shape* shape /* host */, 
  *              pw_moe_permute_backward writes)
  *   dx         fp16 [T][H], overwritten; may be dx_add itself
  *   drouter_w  fp32 [E][H], 16-byte aligned, overwritten (zero for T == 0)
- * Two launches (one for up to 64 tokens). */
+ * Two launches (one for up to 1024 slots). */
 pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, const uint16_t* x,
                              const uint16_t* router_w, const int32_t* ids, const float* w, const float* dw,
                              const uint16_t* dx_add, uint16_t* dx, float* drouter_w, void* workspace,
