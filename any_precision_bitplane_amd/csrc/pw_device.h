@@ -389,6 +389,15 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (row_lane(v, 0) + row_lane(v, 16)) + (row_lane(v, 32) + row_lane(v, 48));
 }
 
+__device__ __forceinline__ int wave_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, kQuadXor1, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kQuadXor2, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kHalfRowMirror, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, kRowMirror, 0xF, 0xF, false);
+  return (__builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16)) +
+         (__builtin_amdgcn_readlane(v, 32) + __builtin_amdgcn_readlane(v, 48));
+}
+
 __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp_row<kQuadXor1>(v));
   v = fmaxf(v, dpp_row<kQuadXor2>(v));

@@ -280,17 +280,13 @@ struct NormGradArgs {
   int64_t dx_stride;
   float* part;                // shares of dweight, null: dweight is not wanted
 };
-// A block of the backward pass has at least four waves and a row of up to 512
-// columns takes one, so up to four shares a block.
-inline size_t norm_grad_parts(int T, int H) {
-  const size_t rows = H <= 512 ? 4 : 1;
-  const size_t blocks = ((size_t)T + rows - 1) / rows;
-  return (blocks < (size_t)kNormGradBlocks ? blocks : (size_t)kNormGradBlocks) * rows;
-}
+// Shares of dweight: one a block, and a block takes at least one row.
+inline size_t norm_grad_parts(int T) { return T < kNormGradBlocks ? (size_t)T : (size_t)kNormGradBlocks; }
 hipError_t launch_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, hipStream_t s);
 
-constexpr int kPermuteSmallSlots = 4096;   // one launch up to here (every block reads all ids)
-constexpr int kPermutePieces = 64;         // pieces of a larger call whose slots are counted apart
+// One launch up to here: its blocks read all ids (S = 5360: 10.3 us against 17.4 of two launches; 7584: 16.4 against 14.5).
+constexpr int kPermuteSmallSlots = 6144;
+constexpr int kPermutePieces = 64;         // most pieces of a larger call whose slots are counted apart, unless a scan follows
 constexpr int64_t kPermutePieceSlots = 8192;   // a piece has no more; with more than 64 pieces a launch sums their counts
 
 struct PermuteArgs {
@@ -318,13 +314,16 @@ struct PermutePlan {
   int64_t piece_tokens;
   bool scan;
 };
-inline PermutePlan permute_plan(int64_t T, int k) {
+inline PermutePlan permute_plan(int64_t T, int k, int E) {
   PermutePlan p;
   int64_t bt = (T + 1023) / 1024;
   const int64_t most = 64 / k > 4 ? 64 / k : 4;
   bt = bt < 4 ? 4 : bt > most ? most : bt;
   const int64_t blocks = (T + bt - 1) / bt;
-  int64_t per_piece = (blocks + kPermutePieces - 1) / kPermutePieces;
+  // a block reads pieces * E counts and, on average, half a piece's ids: about the least together
+  int64_t want = 8;
+  while (want < kPermutePieces && want * want * 2 * E < T * k) want *= 2;
+  int64_t per_piece = (blocks + want - 1) / want;
   const int64_t limit = kPermutePieceSlots / (bt * k) > 1 ? kPermutePieceSlots / (bt * k) : 1;
   p.scan = per_piece > limit;
   if (p.scan) per_piece = limit;

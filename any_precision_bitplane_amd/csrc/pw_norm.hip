@@ -20,11 +20,36 @@ constexpr float kE4m3Max = 448.f;
 constexpr float kScaleMin = 7.888609052210118e-31f;   // 2^-100: scales stay divisible
 constexpr unsigned kMaxGrid = 1u << 20;
 
-// Sum over a row of WPR waves.  `part` holds one value per wave of the block;
-// callers alternate between two such arrays, so one barrier per sum is enough.
-template <int WPR>
+// Sum and maximum over the LPR lanes that share a row (all 64 of a wave, or 8,
+// 16 or 32 of them), the same bits in each.
+template <int LPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (LPR == kWave) return wave_sum(v);
+  v += dpp_row<kQuadXor1>(v);
+  v += dpp_row<kQuadXor2>(v);
+  v += dpp_row<kHalfRowMirror>(v);
+  if constexpr (LPR >= 16) v += dpp_row<kRowMirror>(v);
+  if constexpr (LPR >= 32) v += __shfl_xor(v, 16, kWave);
+  return v;
+}
+
+template <int LPR>
+__device__ __forceinline__ float lanes_max(float v) {
+  if constexpr (LPR == kWave) return wave_max(v);
+  v = fmaxf(v, dpp_row<kQuadXor1>(v));
+  v = fmaxf(v, dpp_row<kQuadXor2>(v));
+  v = fmaxf(v, dpp_row<kHalfRowMirror>(v));
+  if constexpr (LPR >= 16) v = fmaxf(v, dpp_row<kRowMirror>(v));
+  if constexpr (LPR >= 32) v = fmaxf(v, __shfl_xor(v, 16, kWave));
+  return v;
+}
+
+// Sum over a row of WPR waves or LPR lanes.  `part` holds one value per wave of
+// the block; callers alternate between two such arrays, so one barrier per sum
+// is enough.
+template <int LPR, int WPR>
 __device__ __forceinline__ float row_sum(float v, float* part, int wave) {
-  v = wave_sum(v);
+  v = lanes_sum<LPR>(v);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & (kWave - 1)) == 0) part[wave] = v;
     __syncthreads();
@@ -36,9 +61,9 @@ __device__ __forceinline__ float row_sum(float v, float* part, int wave) {
   return v;
 }
 
-template <int WPR>
+template <int LPR, int WPR>
 __device__ __forceinline__ float row_max(float v, float* part, int wave) {
-  v = wave_max(v);
+  v = lanes_max<LPR>(v);
   if constexpr (WPR > 1) {
     if ((threadIdx.x & (kWave - 1)) == 0) part[wave] = v;
     __syncthreads();
@@ -50,23 +75,27 @@ __device__ __forceinline__ float row_max(float v, float* part, int wave) {
   return v;
 }
 
-// WPR waves share a row, each lane holding NV chunks of it; a block has at
-// least four waves, so it takes 4 / WPR rows when a row needs fewer.
+// WPR waves (or, of one wave, LPR lanes) share a row, each lane holding NV
+// chunks of it; a block has at least four waves, so it takes several rows when
+// a row needs fewer.
 constexpr int block_waves(int WPR) { return WPR < 4 ? 4 : WPR; }
+constexpr int block_rows(int LPR, int WPR) { return block_waves(WPR) / WPR * (kWave / LPR); }
 
-template <int DT, int WPR, int NV, bool Q8>
+template <int DT, int LPR, int WPR, int NV, bool Q8>
 __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int kRows = block_waves(WPR) / WPR;
+  constexpr int kRows = block_rows(LPR, WPR);
+  static_assert(LPR == kWave || WPR == 1, "lanes of one wave, or whole waves");
   __shared__ float part[4][block_waves(WPR)];
   const int wave = uniform((int)threadIdx.x / kWave);
   const int lane = (int)threadIdx.x & (kWave - 1);
-  const int first = (wave % WPR) * kWave + lane;   // the lane's first chunk of its row
+  const int own = wave / WPR * (kWave / LPR) + (LPR == kWave ? 0 : lane / LPR);   // the lane's row of the block
+  const int first = (wave % WPR) * kWave + (lane & (LPR - 1));                    // its first chunk of that row
   const int C = a.H / 8;
   int parity = 0;
   for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows, parity ^= 1) {
-    const int64_t row = base + wave / WPR;
+    const int64_t row = base + own;
     const bool live = row < a.T;
     const elem* x = static_cast<const elem*>(a.x) + row * a.x_stride;
     const elem* res = static_cast<const elem*>(a.residual) + row * a.residual_stride;
@@ -88,7 +117,7 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[i][j], v[i][j], sq);
-    sq = row_sum<WPR>(sq, part[parity], wave);
+    sq = row_sum<LPR, WPR>(sq, part[parity], wave);
     const float rstd = rsqrtf(sq / (float)a.H + a.eps);
     const elem* g = static_cast<const elem*>(a.weight);
 #pragma unroll
@@ -114,10 +143,10 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
           const float t = __builtin_fabsf(v[i][j]);
           m[i] = t < INFINITY ? fmaxf(m[i], t) : INFINITY;
         }
-        if (a.group) m[i] = row16_max(m[i]);   // 16 chunks of 8: one group of 128
+        if (a.group) m[i] = lanes_max<LPR < 16 ? LPR : 16>(m[i]);   // 16 chunks of 8: one group of 128
         top = fmaxf(top, m[i]);
       }
-      if (!a.group) top = row_max<WPR>(top, part[2 + parity], wave);
+      if (!a.group) top = row_max<LPR, WPR>(top, part[2 + parity], wave);
       uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.y_stride;
       const int groups = a.group ? (a.H + kNormGroup - 1) / kNormGroup : 1;
 #pragma unroll
@@ -146,11 +175,11 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
   }
 }
 
-template <int DT, int WPR, int NV, bool Q8>
+template <int DT, int LPR, int WPR, int NV, bool Q8>
 hipError_t run_norm(const NormArgs& a, hipStream_t s) {
-  constexpr int kRows = block_waves(WPR) / WPR;
+  constexpr int kRows = block_rows(LPR, WPR);
   const unsigned want = ((unsigned)a.T + kRows - 1) / kRows;
-  hipLaunchKernelGGL((rmsnorm_kernel<DT, WPR, NV, Q8>), dim3(want < kMaxGrid ? want : kMaxGrid),
+  hipLaunchKernelGGL((rmsnorm_kernel<DT, LPR, WPR, NV, Q8>), dim3(want < kMaxGrid ? want : kMaxGrid),
                      dim3(block_waves(WPR) * kWave), 0, s, a);
   return hipGetLastError();
 }
@@ -160,22 +189,24 @@ hipError_t run_norm(const NormArgs& a, hipStream_t s) {
 template <int DT, bool Q8>
 hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
   const int C = a.H / 8;
+  if (C <= 8) return run_norm<DT, 8, 1, 1, Q8>(a, s);
+  if (C <= 16) return run_norm<DT, 16, 1, 1, Q8>(a, s);
+  if (C <= 32) return run_norm<DT, 32, 1, 1, Q8>(a, s);
+  if (C <= 64) return run_norm<DT, 64, 1, 1, Q8>(a, s);
   if (a.T <= kNormFewRows) {
-    if (C <= 64) return run_norm<DT, 1, 1, Q8>(a, s);
-    if (C <= 128) return run_norm<DT, 2, 1, Q8>(a, s);
-    if (C <= 256) return run_norm<DT, 4, 1, Q8>(a, s);
-    if (C <= 512) return run_norm<DT, 8, 1, Q8>(a, s);
-    if (C <= 1024) return run_norm<DT, 16, 1, Q8>(a, s);
-    if (C <= 2048) return run_norm<DT, 16, 2, Q8>(a, s);
-    return run_norm<DT, 16, 4, Q8>(a, s);
+    if (C <= 128) return run_norm<DT, 64, 2, 1, Q8>(a, s);
+    if (C <= 256) return run_norm<DT, 64, 4, 1, Q8>(a, s);
+    if (C <= 512) return run_norm<DT, 64, 8, 1, Q8>(a, s);
+    if (C <= 1024) return run_norm<DT, 64, 16, 1, Q8>(a, s);
+    if (C <= 2048) return run_norm<DT, 64, 16, 2, Q8>(a, s);
+    return run_norm<DT, 64, 16, 4, Q8>(a, s);
   }
-  if (C <= 64) return run_norm<DT, 1, 1, Q8>(a, s);
-  if (C <= 128) return run_norm<DT, 1, 2, Q8>(a, s);
-  if (C <= 256) return run_norm<DT, 1, 4, Q8>(a, s);
-  if (C <= 512) return run_norm<DT, 2, 4, Q8>(a, s);
-  if (C <= 1024) return run_norm<DT, 4, 4, Q8>(a, s);
-  if (C <= 2048) return run_norm<DT, 8, 4, Q8>(a, s);
-  return run_norm<DT, 16, 4, Q8>(a, s);
+  if (C <= 128) return run_norm<DT, 64, 1, 2, Q8>(a, s);
+  if (C <= 256) return run_norm<DT, 64, 1, 4, Q8>(a, s);
+  if (C <= 512) return run_norm<DT, 64, 2, 4, Q8>(a, s);
+  if (C <= 1024) return run_norm<DT, 64, 4, 4, Q8>(a, s);
+  if (C <= 2048) return run_norm<DT, 64, 8, 4, Q8>(a, s);
+  return run_norm<DT, 64, 16, 4, Q8>(a, s);
 }
 
 // Gradient.  With s = 1 / sqrt(mean r^2 + eps) and d = sum_h g_h dy_h r_h:
@@ -191,15 +222,16 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 // written over an input: the rows in flight are the block's own later ones).
 // LEAN: the weight and dresidual are loaded where they are used, so that the
 // longest rows' chunks stay in registers.
-template <int DT, int WPR, int NV, bool AHEAD, bool LEAN>
+template <int DT, int LPR, int WPR, int NV, bool AHEAD, bool LEAN>
 __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(NormGradArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int kRows = block_waves(WPR) / WPR;
+  constexpr int kRows = block_rows(LPR, WPR);
   __shared__ float part[2][2][block_waves(WPR)];
   const int wave = uniform((int)threadIdx.x / kWave);
   const int lane = (int)threadIdx.x & (kWave - 1);
-  const int first = (wave % WPR) * kWave + lane;
+  const int own = wave / WPR * (kWave / LPR) + (LPR == kWave ? 0 : lane / LPR);
+  const int first = (wave % WPR) * kWave + (lane & (LPR - 1));
   const int C = a.H / 8;
   const floatx8 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const elem* gain = static_cast<const elem*>(a.weight);
@@ -232,9 +264,9 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t base = (int64_t)blockIdx.x * kRows;
   chunk rn[NV], dn[NV], an[NV];
-  if constexpr (AHEAD) fetch(base + wave / WPR, rn, dn, an);
+  if constexpr (AHEAD) fetch(base + own, rn, dn, an);
   for (int parity = 0; base < a.T; base += step, parity ^= 1) {
-    const int64_t row = base + wave / WPR;
+    const int64_t row = base + own;
     const bool live = row < a.T;
     elem* dx = static_cast<elem*>(a.dx) + row * a.dx_stride;
     const elem* dres = static_cast<const elem*>(a.dresidual) + row * a.dresidual_stride;
@@ -262,8 +294,8 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
         dot = __builtin_fmaf(gd[j], r[j], dot);
       }
     }
-    sq = wave_sum(sq);
-    dot = wave_sum(dot);
+    sq = lanes_sum<LPR>(sq);
+    dot = lanes_sum<LPR>(dot);
     if constexpr (WPR > 1) {
       if (lane == 0) {
         part[parity][0][wave] = sq;
@@ -293,11 +325,24 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
     }
   }
   if (!a.part) return;
-  float* p = a.part + ((size_t)blockIdx.x * kRows + wave / WPR) * a.H;
+  float* p = a.part + (size_t)blockIdx.x * a.H;
+  if constexpr (kRows == 1) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = first + i * WPR * kWave;
-    if (c < C) Row<PW_F32>::store(p + 8 * c, dg[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = first + i * WPR * kWave;
+      if (c < C) Row<PW_F32>::store(p + 8 * c, dg[i]);
+    }
+  } else {
+    // several rows at a time: their lanes' shares meet first
+    static_assert(kRows == 1 || (NV == 1 && WPR == 1), "one chunk a lane");
+    __shared__ floatx8 sums[kRows * LPR];
+    sums[threadIdx.x] = dg[0];
+    __syncthreads();
+    if ((int)threadIdx.x < LPR && (int)threadIdx.x < C) {
+      floatx8 s = dg[0];
+      for (int i = 1; i < kRows; ++i) s += sums[i * LPR + threadIdx.x];
+      Row<PW_F32>::store(p + 8 * threadIdx.x, s);
+    }
   }
 }
 
@@ -320,31 +365,34 @@ __global__ __launch_bounds__(256) void join_rows_kernel(const float* __restrict_
   if (rg == 0 && col < H) *reinterpret_cast<floatx4*>(out + col) = sums[0][q];
 }
 
-template <int DT, int WPR, int NV>
+template <int DT, int LPR, int WPR, int NV>
 hipError_t run_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) {
-  constexpr int kRows = block_waves(WPR) / WPR;
+  constexpr int kRows = block_rows(LPR, WPR);
   const unsigned want = ((unsigned)a.T + kRows - 1) / kRows;
   const unsigned grid = want < (unsigned)kNormGradBlocks ? want : (unsigned)kNormGradBlocks;
   // registers of a lane's chunks: 4 (16-bit) or 8 (fp32) for each of three matrices, again for the row ahead
   constexpr int kChunkRegs = NV * (DT == PW_F32 ? 8 : 4);
   constexpr bool kLean = WPR == 16 && kChunkRegs >= 16, kAhead = !kLean && kChunkRegs <= 16;
-  hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, WPR, NV, kAhead, kLean>), dim3(grid), dim3(block_waves(WPR) * kWave), 0, s, a);
+  hipLaunchKernelGGL((rmsnorm_grad_kernel<DT, LPR, WPR, NV, kAhead, kLean>), dim3(grid), dim3(block_waves(WPR) * kWave),
+                     0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dweight) return e;
-  hipLaunchKernelGGL(join_rows_kernel, dim3((a.H + 15) / 16), dim3(256), 0, s, a.part, (int)(grid * kRows), a.H,
-                     dweight);
+  hipLaunchKernelGGL(join_rows_kernel, dim3((a.H + 15) / 16), dim3(256), 0, s, a.part, (int)grid, a.H, dweight);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t pick_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) {
   const int C = a.H / 8;
-  if (C <= 64) return run_norm_grad<DT, 1, 1>(a, dweight, s);
-  if (C <= 256) return run_norm_grad<DT, 4, 1>(a, dweight, s);
-  if (C <= 512) return run_norm_grad<DT, 4, 2>(a, dweight, s);
-  if (C <= 1024) return run_norm_grad<DT, 16, 1>(a, dweight, s);
-  if (C <= 2048) return run_norm_grad<DT, 16, 2>(a, dweight, s);
-  return run_norm_grad<DT, 16, 4>(a, dweight, s);
+  if (C <= 8) return run_norm_grad<DT, 8, 1, 1>(a, dweight, s);
+  if (C <= 16) return run_norm_grad<DT, 16, 1, 1>(a, dweight, s);
+  if (C <= 32) return run_norm_grad<DT, 32, 1, 1>(a, dweight, s);
+  if (C <= 64) return run_norm_grad<DT, 64, 1, 1>(a, dweight, s);
+  if (C <= 256) return run_norm_grad<DT, 64, 4, 1>(a, dweight, s);
+  if (C <= 512) return run_norm_grad<DT, 64, 4, 2>(a, dweight, s);
+  if (C <= 1024) return run_norm_grad<DT, 64, 16, 1>(a, dweight, s);
+  if (C <= 2048) return run_norm_grad<DT, 64, 16, 2>(a, dweight, s);
+  return run_norm_grad<DT, 64, 16, 4>(a, dweight, s);
 }
 
 }  // namespace

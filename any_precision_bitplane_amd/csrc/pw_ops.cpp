@@ -84,7 +84,7 @@ pw_status pw_rmsnorm(int32_t T, int32_t H, int32_t dtype, const void* x, int64_t
 
 size_t pw_rmsnorm_backward_workspace_bytes(int32_t T, int32_t H) {
   if (T < 0 || H <= 0 || H % 8 || H > kMaxNormHidden) return 0;
-  return align_up(norm_grad_parts(T, H) * (size_t)H * sizeof(float) + 1, kAlign);
+  return align_up(norm_grad_parts(T) * (size_t)H * sizeof(float) + 1, kAlign);
 }
 
 pw_status pw_rmsnorm_backward(int32_t T, int32_t H, int32_t dtype, const void* dy, int64_t dy_stride, const void* r,

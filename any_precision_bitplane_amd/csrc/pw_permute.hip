@@ -24,28 +24,35 @@ __device__ __forceinline__ uint32_t expert_of(int32_t id, int E) {
   return (uint32_t)id < (uint32_t)E ? (uint32_t)id : kDropped;
 }
 
+constexpr int kLaneOffsetSlots = 256;
+constexpr int kItems = 4;    // places a wave counts at a time
+constexpr int kIdLoads = 8;  // ids a thread requests together
+
 constexpr int kUnroll = 4;   // 16-byte pieces of a row requested together
 typedef uint32_t piece_t __attribute__((ext_vector_type(4)));
 
-// Up to kUnroll pieces of token t's row, `lanes` threads apart, from byte c0 on.
+// Up to N pieces of token t's row, `lanes` threads apart, from byte c0 on.
+template <int N>
 __device__ __forceinline__ void load_pieces(const PermuteArgs& a, int64_t t, int64_t c0, int lanes,
                                             piece_t (&v)[kUnroll]) {
   const uint8_t* src = a.x + t * a.x_stride + c0;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u)
+  for (int u = 0; u < N; ++u)
     v[u] = c0 + u * 16 * lanes < a.row_bytes ? *reinterpret_cast<const piece_t*>(src + u * 16 * lanes)
                                              : piece_t{0u, 0u, 0u, 0u};
 }
 
-// ... and their copies at the places pos[0..k), -1: none.
+// ... and their copies at the places pos[0..k), -1: none.  WAVE: all lanes of a
+// wave have the same places.
+template <int N, bool WAVE>
 __device__ __forceinline__ void store_pieces(const PermuteArgs& a, const int* pos, int64_t c0, int lanes,
                                              const piece_t (&v)[kUnroll]) {
   for (int j = 0; j < a.k; ++j) {
-    const int p = uniform(pos[j]);
+    const int p = WAVE ? uniform(pos[j]) : pos[j];
     if (p < 0) continue;
     uint8_t* dst = a.xs + p * a.xs_stride + c0;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
+    for (int u = 0; u < N; ++u)
       if (c0 + u * 16 * lanes < a.row_bytes) *reinterpret_cast<piece_t*>(dst + u * 16 * lanes) = v[u];
   }
 }
@@ -58,55 +65,118 @@ __device__ __forceinline__ void scatter_scales(const PermuteArgs& a, int64_t t, 
   }
 }
 
-// Few slots: one launch.  Every block takes one token and finds its slots'
-// places itself, by counting the slots that sort before each (ids in LDS, one
-// wave per place).  The E + 1 expert offsets are counted the same way, spread
-// over the blocks.  The row is requested before any of that.
-__global__ __launch_bounds__(kThreads) void permute_small_kernel(PermuteArgs a) {
+// Few slots: one launch.  A block takes one to four tokens, 1 << shift threads
+// each, and finds their slots' places itself, by counting the slots that sort
+// before each (ids in LDS, one wave per place).  The E + 1 expert offsets are
+// counted the same way, spread over the blocks; or, where there are fewer slots
+// than a wave has to look at one by one, a lane per offset.  The rows are
+// requested before any of that.
+__global__ __launch_bounds__(kThreads) void permute_small_kernel(PermuteArgs a, int shift) {
   extern __shared__ uint32_t shared[];
-  uint32_t* ids = shared;                                  // [S rounded up to a wave]
   const int S = a.T * a.k;
-  const int padded = (S + kWave - 1) / kWave * kWave;
-  int* pos = reinterpret_cast<int*>(shared + padded);      // [k]
-  const int t = blockIdx.x;
+  const int padded = (S + 4 * kWave - 1) / (4 * kWave) * (4 * kWave);
+  uint32_t* ids = shared;                                  // [padded]
+  int* pos = reinterpret_cast<int*>(shared + padded);      // [tokens * k]
+  const int lanes = 1 << shift, tokens = kThreads >> shift;
+  const int t0 = (int)blockIdx.x * tokens;
+  const int nt = a.T - t0 < tokens ? a.T - t0 : tokens;
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
+  const int own = uniform((int)threadIdx.x >> shift);      // this thread's token
+  const int64_t own_c = 16 * (int64_t)((int)threadIdx.x & (lanes - 1));
   piece_t v[kUnroll];
-  load_pieces(a, t, 16 * (int64_t)threadIdx.x, kThreads, v);
+  if (own < nt) load_pieces<kUnroll>(a, t0 + own, own_c, lanes, v);
   bool bad = false;
-  for (int i = threadIdx.x; i < padded; i += kThreads) {
-    const uint32_t e = i < S ? expert_of(a.ids[i], a.E) : kDropped;
-    bad |= i < S && e == kDropped;
-    ids[i] = e;
-  }
-  if (bad && t == 0 && a.status) raise_status(a.status, PW_DEV_BAD_EXPERT_ID);
-  __syncthreads();
-  const int mine = t <= a.E ? (a.E - t) / a.T + 1 : 0;     // offsets of experts t, t + T, ... <= E
-  for (int item = wave; item < a.k + mine; item += kWaves) {
-    const bool slot = item < a.k;
-    const int s = slot ? t * a.k + item : 0;               // an offset counts the slots of lower experts only
-    const uint32_t e = slot ? ids[s] : (uint32_t)(t + (item - a.k) * a.T);
-    int before = 0;
-    for (int i = lane; i < padded; i += kWave) {
-      const uint32_t o = ids[i];
-      before += __popcll(__ballot(o < e || (o == e && i < s)));
+  for (int i0 = threadIdx.x; i0 < padded; i0 += kIdLoads * kThreads) {
+    int32_t id[kIdLoads];
+#pragma unroll
+    for (int u = 0; u < kIdLoads; ++u) {
+      const int i = i0 + u * kThreads;
+      id[u] = a.ids[i < S ? i : S - 1];
     }
-    if (lane != 0) continue;
-    if (slot) {
-      const int p = e == kDropped ? -1 : before;
-      pos[item] = p;
-      a.inv[s] = p;
-      if (p >= 0 && a.perm) a.perm[p] = s;
-    } else {
+#pragma unroll
+    for (int u = 0; u < kIdLoads; ++u) {
+      const int i = i0 + u * kThreads;
+      const uint32_t e = i < S ? expert_of(id[u], a.E) : kDropped;
+      bad |= i < S && e == kDropped;
+      if (i < padded) ids[i] = e;
+    }
+  }
+  if (bad && blockIdx.x == 0 && a.status) raise_status(a.status, PW_DEV_BAD_EXPERT_ID);
+  __syncthreads();
+  const bool by_lane = S <= kLaneOffsetSlots;
+  const int slots = nt * a.k;
+  // offsets of experts b, b + blocks, ... <= E
+  const int b = blockIdx.x, blocks = gridDim.x;
+  const int mine = by_lane || b > a.E ? 0 : (a.E - b) / blocks + 1;
+  // kItems places or offsets at a time: ids before the block's own slots count
+  // if they are at most e, those behind them if they are less
+  const int lo = t0 * a.k;
+  const int mixed0 = lo / (4 * kWave) * (4 * kWave);
+  const int mixed1 = (lo + slots + 4 * kWave - 1) / (4 * kWave) * (4 * kWave);
+  for (int item0 = wave * kItems; item0 < slots + mine; item0 += kWaves * kItems) {
+    int at[kItems], before[kItems];
+    uint32_t e[kItems], upto[kItems];
+#pragma unroll
+    for (int g = 0; g < kItems; ++g) {
+      const int item = item0 + g;
+      at[g] = item < slots ? lo + item : 0;
+      e[g] = item < slots ? ids[at[g]] : (uint32_t)(b + (item - slots) * blocks);
+      upto[g] = item < slots ? e[g] + 1 : e[g];            // an offset counts the slots of lower experts only
+      before[g] = 0;
+    }
+    auto count = [&](int from, int to, const uint32_t(&below)[kItems]) {
+#pragma unroll 2
+      for (int i = from + 4 * lane; i < to; i += 4 * kWave) {
+        const piece_t o = *reinterpret_cast<const piece_t*>(ids + i);
+#pragma unroll
+        for (int g = 0; g < kItems; ++g)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) before[g] += o[u] < below[g] ? 1 : 0;
+      }
+    };
+    count(0, mixed0, upto);
+    for (int i = mixed0 + 4 * lane; i < mixed1; i += 4 * kWave) {
+      const piece_t o = *reinterpret_cast<const piece_t*>(ids + i);
+#pragma unroll
+      for (int g = 0; g < kItems; ++g)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) before[g] += o[u] < (i + u < at[g] ? upto[g] : e[g]) ? 1 : 0;
+    }
+    count(mixed1, padded, e);
+#pragma unroll
+    for (int g = 0; g < kItems; ++g) {
+      const int item = item0 + g;
+      const int n = wave_sum(before[g]);
+      if (lane != 0 || item >= slots + mine) continue;
+      if (item < slots) {
+        const int p = e[g] == kDropped ? -1 : n;
+        pos[item] = p;
+        a.inv[at[g]] = p;
+        if (p >= 0 && a.perm) a.perm[p] = at[g];
+      } else {
+        a.offsets[e[g]] = n;
+      }
+    }
+  }
+  if (by_lane)
+    for (int e = b * kThreads + (int)threadIdx.x; e <= a.E; e += blocks * kThreads) {
+      int before = 0;
+      for (int i = 0; i < S; i += 4) {
+        const piece_t o = *reinterpret_cast<const piece_t*>(ids + i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) before += o[u] < (uint32_t)e ? 1 : 0;
+      }
       a.offsets[e] = before;
     }
-  }
   __syncthreads();
-  constexpr int64_t kPiece = (int64_t)kUnroll * kThreads * 16;
-  for (int64_t c0 = 16 * (int64_t)threadIdx.x; c0 < a.row_bytes; c0 += kPiece) {
-    if (c0 >= kPiece) load_pieces(a, t, c0, kThreads, v);
-    store_pieces(a, pos, c0, kThreads, v);
+  if (own >= nt) return;
+  const int64_t piece = (int64_t)kUnroll * lanes * 16;
+  const int* mypos = pos + own * a.k;
+  for (int64_t c0 = own_c; c0 < a.row_bytes; c0 += piece) {
+    if (c0 >= piece) load_pieces<kUnroll>(a, t0 + own, c0, lanes, v);
+    store_pieces<kUnroll, true>(a, mypos, c0, lanes, v);
   }
-  scatter_scales(a, t, pos, threadIdx.x, kThreads);
+  scatter_scales(a, t0 + own, mypos, (int)threadIdx.x & (lanes - 1), lanes);
 }
 
 // Many slots, first launch: slots per expert in each of the pieces.
@@ -154,8 +224,10 @@ __global__ __launch_bounds__(kWave) void permute_scan_kernel(PermuteArgs a) {
 // in earlier blocks of the piece (counted again here); inside the block a
 // slot's rank is its position among the equal ids, found by ballots of one
 // wave.  Each wave requests its first token's row before all that.
-template <bool SCANNED>
-__global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a) {
+//
+// NARROW (rows of up to 512 bytes): 1 << shift threads take a token.
+template <bool SCANNED, bool NARROW>
+__global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a, int shift) {
   __shared__ int total[kMaxExperts];         // the expert's slots
   __shared__ int next[kMaxExperts];          // its slots before this block, then its next place
   extern __shared__ uint32_t shared[];
@@ -167,8 +239,10 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
   const int slots = nt * a.k;
   const int64_t piece = t0 / a.piece_tokens;
 
+  const int own = NARROW ? tid >> shift : wave, groups = NARROW ? kThreads >> shift : kWaves;
+  const int lanes = NARROW ? 1 << shift : kWave, in_row = tid & (lanes - 1);
   piece_t v[kUnroll];
-  if (wave < nt) load_pieces(a, t0 + wave, 16 * (int64_t)lane, kWave, v);
+  if (own < nt) load_pieces<NARROW ? 1 : kUnroll>(a, t0 + own, 16 * (int64_t)in_row, lanes, v);
   for (int e = tid; e < a.E; e += kThreads) {
     total[e] = SCANNED ? a.counts[(int64_t)a.pieces * a.E + e] : 0;
     next[e] = SCANNED ? a.counts[piece * a.E + e] : 0;
@@ -239,50 +313,57 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
   }
   __syncthreads();
   constexpr int64_t kPiece = (int64_t)kUnroll * kWave * 16;
-  for (int t = wave; t < nt; t += kWaves) {
-    for (int64_t c0 = 16 * (int64_t)lane; c0 - 16 * lane < a.row_bytes; c0 += kPiece) {
-      if (t != wave || c0 >= kPiece) load_pieces(a, t0 + t, c0, kWave, v);
-      store_pieces(a, pos + t * a.k, c0, kWave, v);
+  for (int t = own; t < nt; t += groups) {
+    const int* mypos = pos + t * a.k;
+    if constexpr (NARROW) {
+      if (t != own) load_pieces<1>(a, t0 + t, 16 * (int64_t)in_row, lanes, v);
+      store_pieces<1, false>(a, mypos, 16 * (int64_t)in_row, lanes, v);
+    } else {
+      for (int64_t c0 = 16 * (int64_t)lane; c0 - 16 * lane < a.row_bytes; c0 += kPiece) {
+        if (t != own || c0 >= kPiece) load_pieces<kUnroll>(a, t0 + t, c0, kWave, v);
+        store_pieces<kUnroll, true>(a, mypos, c0, kWave, v);
+      }
     }
-    if (a.groups) scatter_scales(a, t0 + t, pos + t * a.k, lane, kWave);
+    if (a.groups) scatter_scales(a, t0 + t, mypos, in_row, lanes);
   }
 }
 
 // y[t] = sum_j w[t][j] rows[inv[t k + j]]; w null: ones.  `lanes` threads (a
-// power of two) share a token, each taking chunks of eight columns; the rows
-// of four slots are requested together.
+// power of two) share a token, or one of the pieces of a longer row, each
+// taking one chunk of eight columns; the rows of four slots are requested
+// together.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a, int shift) {
+__global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a, int shift, int pieces) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  const int C = a.H / 8;
   const int lanes = 1 << shift;
   const int per_block = kThreads >> shift;
   const int lane = (int)threadIdx.x & (lanes - 1);
-  const int64_t S = (int64_t)a.T * a.k;
-  for (int64_t t = (int64_t)blockIdx.x * per_block + ((int)threadIdx.x >> shift); t < a.T;
-       t += (int64_t)gridDim.x * per_block) {
-    for (int c = lane; c < C; c += lanes) {
-      floatx8 acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int j0 = 0; j0 < a.k; j0 += 4) {
-        float w[4];
-        bool in[4];
-        typename R::chunk v[4];
+  const int64_t S = (int64_t)a.T * a.k, n = (int64_t)a.T * pieces;
+  for (int64_t i = (int64_t)blockIdx.x * per_block + ((int)threadIdx.x >> shift); i < n;
+       i += (int64_t)gridDim.x * per_block) {
+    const int64_t t = pieces == 1 ? i : i / pieces;
+    const int c = (int)(i - t * pieces) * lanes + lane;
+    if (8 * c >= a.H) continue;
+    floatx8 acc = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < a.k; j0 += 4) {
+      float w[4];
+      bool in[4];
+      typename R::chunk v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t s = t * a.k + j0 + i;
-          const int32_t p = j0 + i < a.k ? a.inv[s] : -1;
-          in[i] = p >= 0 && p < S;
-          if (!in[i]) continue;
-          w[i] = a.w ? a.w[s] : 1.f;
-          v[i] = R::load(static_cast<const elem*>(a.rows) + p * a.rows_stride + 8 * c);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (in[i]) acc += w[i] * R::wide(v[i]);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t s = t * a.k + j0 + u;
+        const int32_t p = j0 + u < a.k ? a.inv[s] : -1;
+        in[u] = p >= 0 && p < S;
+        if (!in[u]) continue;
+        w[u] = a.w ? a.w[s] : 1.f;
+        v[u] = R::load(static_cast<const elem*>(a.rows) + p * a.rows_stride + 8 * c);
       }
-      R::store(static_cast<elem*>(a.y) + t * a.y_stride + 8 * c, R::narrow(acc));
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (in[u]) acc += w[u] * R::wide(v[u]);
     }
+    R::store(static_cast<elem*>(a.y) + t * a.y_stride + 8 * c, R::narrow(acc));
   }
 }
 
@@ -350,9 +431,9 @@ unsigned grid_for(int64_t blocks) { return (unsigned)(blocks < (int64_t)kMaxGrid
 template <int DT>
 hipError_t run_unpermute(const UnpermuteArgs& a, hipStream_t s) {
   const int shift = lanes_shift(a.H / 8, kThreads);
-  const int per_block = kThreads >> shift;
-  hipLaunchKernelGGL((unpermute_kernel<DT>), dim3(grid_for(((int64_t)a.T + per_block - 1) / per_block)),
-                     dim3(kThreads), 0, s, a, shift);
+  const int per_block = kThreads >> shift, pieces = (a.H / 8 + (1 << shift) - 1) >> shift;
+  hipLaunchKernelGGL((unpermute_kernel<DT>), dim3(grid_for(((int64_t)a.T * pieces + per_block - 1) / per_block)),
+                     dim3(kThreads), 0, s, a, shift, pieces);
   return hipGetLastError();
 }
 
@@ -370,11 +451,14 @@ hipError_t run_unpermute_grad(const UnpermuteGradArgs& a, hipStream_t s) {
 hipError_t launch_permute(PermuteArgs a, hipStream_t s) {
   const int64_t S = (int64_t)a.T * a.k;
   if (S <= kPermuteSmallSlots) {
-    const size_t lds = ((size_t)(S + kWave - 1) / kWave * kWave + a.k) * sizeof(uint32_t);
-    hipLaunchKernelGGL(permute_small_kernel, dim3(a.T), dim3(kThreads), lds, s, a);
+    const int shift = a.T <= 512 ? 8 : a.T <= 1024 ? 7 : 6;
+    const int tokens = kThreads >> shift;
+    const size_t padded = (size_t)(S + 4 * kWave - 1) / (4 * kWave) * (4 * kWave);
+    hipLaunchKernelGGL(permute_small_kernel, dim3((a.T + tokens - 1) / tokens), dim3(kThreads),
+                       (padded + (size_t)tokens * a.k) * sizeof(uint32_t), s, a, shift);
     return hipGetLastError();
   }
-  const PermutePlan p = permute_plan(a.T, a.k);
+  const PermutePlan p = permute_plan(a.T, a.k, a.E);
   a.block_tokens = p.block_tokens;
   a.piece_tokens = p.piece_tokens;
   a.pieces = p.pieces;
@@ -383,14 +467,18 @@ hipError_t launch_permute(PermuteArgs a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t lds = (size_t)p.block_tokens * a.k * sizeof(int);
-  if (!p.scan) {
-    hipLaunchKernelGGL(permute_scatter_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
-    return hipGetLastError();
+  if (p.scan) {
+    hipLaunchKernelGGL(permute_scan_kernel, dim3(a.E), dim3(kWave), 0, s, a);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(permute_scan_kernel, dim3(a.E), dim3(kWave), 0, s, a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(permute_scatter_kernel<true>, dim3((unsigned)blocks), dim3(kThreads), lds, s, a);
+  const bool narrow = a.row_bytes <= 512;
+  const int shift = lanes_shift((int)(a.row_bytes / 16), kWave);
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  if (p.scan && narrow) hipLaunchKernelGGL((permute_scatter_kernel<true, true>), grid, block, lds, s, a, shift);
+  else if (p.scan) hipLaunchKernelGGL((permute_scatter_kernel<true, false>), grid, block, lds, s, a, shift);
+  else if (narrow) hipLaunchKernelGGL((permute_scatter_kernel<false, true>), grid, block, lds, s, a, shift);
+  else hipLaunchKernelGGL((permute_scatter_kernel<false, false>), grid, block, lds, s, a, shift);
   return hipGetLastError();
 }
 

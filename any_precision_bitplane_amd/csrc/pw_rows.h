@@ -32,13 +32,4 @@ struct Row {
   static __device__ __forceinline__ chunk narrow(floatx8 v) { return __builtin_convertvector(v, chunk); }
 };
 
-// Largest value of each 16-lane row of the wave, in every lane of it.
-__device__ __forceinline__ float row16_max(float v) {
-  v = fmaxf(v, dpp_row<kQuadXor1>(v));
-  v = fmaxf(v, dpp_row<kQuadXor2>(v));
-  v = fmaxf(v, dpp_row<kHalfRowMirror>(v));
-  v = fmaxf(v, dpp_row<kRowMirror>(v));
-  return v;
-}
-
 }  // namespace pw

@@ -417,8 +417,8 @@ size_t pw_moe_permute_workspace_bytes(const pw_moe_shape* shape /* host */, int3
  *   inv      int32 [T*k];  perm  int32 [T*k] or NULL: perm[inv[s]] = s, from
  *            offsets[E] on left as it was
  *   status   device uint32 or NULL: PW_DEV_* bits are OR-ed into it
- * One launch for up to 4096 slots, two above (three from about half a million
- * on).  T == 0 sets offsets to zero. */
+ * One launch for up to 6144 slots, two above, three from some hundred thousand
+ * on.  T == 0 sets offsets to zero. */
 pw_status pw_moe_permute(const pw_moe_shape* shape /* host */, int32_t T, int32_t dtype, const void* x,
                          int64_t x_stride, const float* x_scale, int32_t groups, const int32_t* ids, void* xs,
                          int64_t xs_stride, float* xs_scale, int32_t* offsets, int32_t* inv, int32_t* perm,

@@ -73,7 +73,7 @@ def near(got, ref, allowed, what):
 
 # ----- norm -----------------------------------------------------------------
 
-NORM_SIZES = [(1, 8), (3, 64), (5, 520), (1, 2048), (2, 4104), (7, 8192), (2, 16384), (1, 32768),
+NORM_SIZES = [(1, 8), (37, 40), (2050, 128), (19, 136), (1500, 256), (3, 64), (5, 520), (1, 2048), (2, 4104), (7, 8192), (2, 16384), (1, 32768),
               (1025, 64), (1030, 520), (1027, 1000), (1026, 2080), (1025, 4096), (1025, 8200), (1025, 16392),
               (1025, 24576)]
 
@@ -98,7 +98,8 @@ def test_rmsnorm(torch, T, H, name):
 
 
 @pytest.mark.parametrize("name", DTYPES)
-@pytest.mark.parametrize("T,H,group", [(1, 64, 0), (1, 64, 128), (3, 136, 128), (5, 2048, 128), (4, 2080, 0),
+@pytest.mark.parametrize("T,H,group", [(1, 64, 0), (1, 64, 128), (70, 40, 128), (70, 40, 0), (2049, 128, 128), (9, 128, 0), (1026, 256, 128),
+                                       (33, 232, 0), (3, 136, 128), (5, 2048, 128), (4, 2080, 0),
                                        (2, 32768, 0), (1, 32768, 128), (1030, 520, 128), (1025, 4096, 0),
                                        (1025, 8200, 128), (1025, 16384, 0)])
 def test_rmsnorm_e4m3(torch, T, H, group, name):
@@ -154,7 +155,7 @@ def test_rmsnorm_in_place_and_special_rows(torch):
         near(f64(y[t:t + 1]), ref, np.abs(ref) * (2.0 ** -11 + ROW * U) + 2.0 ** -25, f"row {t}")
 
 
-GRAD_SIZES = [(1, 8), (3, 64), (2, 32768), (5, 8200), (700, 4096), (2500, 520), (1025, 2080), (513, 8192), (514, 16384),
+GRAD_SIZES = [(1, 8), (6007, 40), (9000, 128), (4500, 200), (2050, 256), (3, 64), (2, 32768), (5, 8200), (700, 4096), (2500, 520), (1025, 2080), (513, 8192), (514, 16384),
               (515, 24576), (3000, 512)]
 
 
@@ -182,8 +183,8 @@ def test_rmsnorm_backward(torch, T, H, name):
     for got, add, what in [(dx, a, "dx"), (alone, np.zeros_like(a), "dx without the stream's gradient")]:
         ref, dgr = oo.rmsnorm_backward(d, rr, gg, EPS, add)
         near(f64(got), ref, np.abs(ref) * rel + ab + 2 * ROW * U * (mag + np.abs(add)), what)
-    # shares of at most ceil(T / 512) rows each, then at most 2048 shares: 32 a thread and six levels
-    chain = -(-T // 512) + 32 + 6 + ROW
+    # a lane adds at most ceil(T / 512) rows, a block at most 32 lanes' shares, then 512 blocks: 8 a thread and six levels
+    chain = -(-T // 512) + 32 + 8 + 6 + ROW
     near(f64(dg), dgr, chain * U * np.sum(np.abs(d * rr * s), axis=0), "dweight")
 
 
@@ -224,10 +225,10 @@ def test_rmsnorm_backward_of_no_rows(torch):
 
 # ----- sorting ----------------------------------------------------------------
 
-# name, T, H, E, k, share of dropped slots; up to 4096 slots one launch, above two
+# name, T, H, E, k, share of dropped slots; up to 6144 slots one launch, above two, from about half a million three
 SORT_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd", 7, 96, 5, 3, 0.3),
               ("all_dropped", 9, 64, 8, 2, 1.0), ("E256_k64", 5, 64, 256, 64, 0.1), ("E256_k256", 2, 32, 256, 256, 0.0),
-              ("more_experts_than_tokens", 3, 64, 200, 2, 0.0), ("edge_4096", 1024, 96, 60, 4, 0.1),
+              ("more_experts_than_tokens", 3, 64, 200, 2, 0.0), ("edge_4096", 1024, 96, 60, 4, 0.1), ("edge_6144", 1536, 96, 60, 4, 0.1), ("above_6144", 1537, 320, 60, 4, 0.1),
               ("above_4096", 1025, 96, 60, 4, 0.1), ("one_expert", 5000, 64, 1, 1, 0.0), ("large", 4099, 160, 8, 2, 0.05),
               ("E256_k8", 1500, 64, 256, 8, 0.2), ("E256_k256_large", 40, 32, 256, 256, 0.1),
               ("all_dropped_large", 5001, 32, 9, 1, 1.0), ("k7", 3001, 64, 33, 7, 0.5),
