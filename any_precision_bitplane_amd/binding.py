@@ -359,16 +359,18 @@ def pw_moe_forward_layers(shp: PwMoeShape, T: int, x, router_ws, blocks, qs, y, 
 # contiguous last dimension, sizes) and refused as the library would refuse it.
 _torch = None
 _current_stream = None   # GPU index -> raw handle of torch's current stream there
+_current_device = None   # -> index of the current GPU
 _DTYPES: dict = {}
 
 
 def _load_ops() -> ctypes.CDLL:
-    global _torch, _current_stream
+    global _torch, _current_stream, _current_device
     if _torch is None:
         import torch
         # the handle alone, without a Stream object around it (1.0 us less a call), where torch offers that
         _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _DTYPES.update({torch.float32: PW_F32, torch.float16: PW_F16, torch.bfloat16: PW_BF16,
                         torch.float8_e4m3fn: PW_E4M3})
         _torch = torch
@@ -421,21 +423,25 @@ def _scratch(t, dev):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _run(name, check, dev, stream, fn, *args) -> int:
-    """fn(*args, stream) with the tensors' GPU as the current one."""
-    cuda = _torch.cuda
+def _handle(stream, dev) -> int:
+    """Raw handle of a stream of the tensors' GPU; None: torch's current one there."""
     if stream is None:
-        stream = _current_stream(dev)
-    elif not isinstance(stream, int):
-        if stream.device.index != dev:
-            raise _Refused("stream must be one of the tensors' GPU")
-        stream = stream.cuda_stream
-    if cuda.current_device() == dev:
-        st = fn(*args, stream)
+        return _current_stream(dev)
+    if isinstance(stream, int):
+        return stream
+    if stream.device.index != dev:
+        raise _Refused("stream must be one of the tensors' GPU")
+    return stream.cuda_stream
+
+
+def _call(name, check, dev, fn, args) -> int:
+    """fn(*args) with the tensors' GPU as the current one."""
+    if _current_device() == dev:
+        st = fn(*args)
     else:
-        with cuda.device(dev):
-            st = fn(*args, stream)
-    if st != PW_OK and check:
+        with _torch.cuda.device(dev):
+            st = fn(*args)
+    if st and check:
         raise PwError(st, name)
     return st
 
@@ -458,8 +464,9 @@ def pw_rmsnorm(T: int, H: int, x, weight, eps: float, y, residual=None, residual
         py, sy = _rows(y, "y", T, H, dev, y.dtype)
         pc = None if scale is None else _array(scale, "scale", T * ((H + 127) // 128 if group else 1), dev,
                                                _torch.float32)
-        return _run("pw_rmsnorm", check, dev, stream, lib.pw_rmsnorm, T, H, _DTYPES.get(dt, -1), px, sx, pr, sr, po,
-                    so, _array(weight, "weight", H, dev, dt), eps, _DTYPES.get(y.dtype, -1), py, sy, pc, group)
+        return _call("pw_rmsnorm", check, dev, lib.pw_rmsnorm, (
+            T, H, _DTYPES.get(dt, -1), px, sx, pr, sr, po, so, _array(weight, "weight", H, dev, dt), eps,
+            _DTYPES.get(y.dtype, -1), py, sy, pc, group, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_rmsnorm", check, e)
 
@@ -478,9 +485,9 @@ def pw_rmsnorm_backward(T: int, H: int, dy, r, weight, eps: float, dx, dweight=N
         pa, sa = _rows(dresidual, "dresidual", T, H, dev, dt)
         px, sx = _rows(dx, "dx", T, H, dev, dt)
         pw, nw = _scratch(workspace, dev)
-        return _run("pw_rmsnorm_backward", check, dev, stream, lib.pw_rmsnorm_backward, T, H, _DTYPES.get(dt, -1), pd,
-                    sd, pr, sr, _array(weight, "weight", H, dev, dt), eps, pa, sa, px, sx,
-                    _array(dweight, "dweight", H, dev, _torch.float32), pw, nw)
+        return _call("pw_rmsnorm_backward", check, dev, lib.pw_rmsnorm_backward, (
+            T, H, _DTYPES.get(dt, -1), pd, sd, pr, sr, _array(weight, "weight", H, dev, dt), eps, pa, sa, px, sx,
+            _array(dweight, "dweight", H, dev, _torch.float32), pw, nw, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_rmsnorm_backward", check, e)
 
@@ -504,11 +511,11 @@ def pw_moe_permute(shp: PwMoeShape, T: int, x, ids, xs, offsets, inv, perm, work
         px, sx = _rows(x, "x", T, H, dev, dt)
         ps, ss = _rows(xs, "xs", S, H, dev, dt)
         pw, nw = _scratch(workspace, dev)
-        return _run("pw_moe_permute", check, dev, stream, lib.pw_moe_permute, ctypes.byref(shp), T,
-                    _DTYPES.get(dt, -1), px, sx, _array(x_scale, "x_scale", T * groups, dev, f32), groups,
-                    _array(ids, "ids", S, dev, i32), ps, ss, _array(xs_scale, "xs_scale", S * groups, dev, f32),
-                    _array(offsets, "offsets", shp.num_experts + 1, dev, i32), _array(inv, "inv", S, dev, i32),
-                    _array(perm, "perm", S, dev, i32), _array(status, "status", 1, dev, i32), pw, nw)
+        return _call("pw_moe_permute", check, dev, lib.pw_moe_permute, (
+            ctypes.byref(shp), T, _DTYPES.get(dt, -1), px, sx, _array(x_scale, "x_scale", T * groups, dev, f32),
+            groups, _array(ids, "ids", S, dev, i32), ps, ss, _array(xs_scale, "xs_scale", S * groups, dev, f32),
+            _array(offsets, "offsets", shp.num_experts + 1, dev, i32), _array(inv, "inv", S, dev, i32),
+            _array(perm, "perm", S, dev, i32), _array(status, "status", 1, dev, i32), pw, nw, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_moe_permute", check, e)
 
@@ -519,8 +526,9 @@ def pw_moe_permute_backward(shp: PwMoeShape, T: int, dxs, inv, dx, stream=None, 
         dev, dt, H, S = _gpu(dxs), dxs.dtype, shp.hidden, T * shp.top_k
         ps, ss = _rows(dxs, "dxs", S, H, dev, dt)
         px, sx = _rows(dx, "dx", T, H, dev, dt)
-        return _run("pw_moe_permute_backward", check, dev, stream, lib.pw_moe_permute_backward, ctypes.byref(shp), T,
-                    _DTYPES.get(dt, -1), ps, ss, _array(inv, "inv", S, dev, _torch.int32), px, sx)
+        return _call("pw_moe_permute_backward", check, dev, lib.pw_moe_permute_backward, (
+            ctypes.byref(shp), T, _DTYPES.get(dt, -1), ps, ss, _array(inv, "inv", S, dev, _torch.int32), px, sx,
+            _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_moe_permute_backward", check, e)
 
@@ -532,9 +540,9 @@ def pw_moe_unpermute(shp: PwMoeShape, T: int, rows, inv, w, y, stream=None, chec
         dev, dt, H, S = _gpu(rows), rows.dtype, shp.hidden, T * shp.top_k
         pr, sr = _rows(rows, "rows", S, H, dev, dt)
         py, sy = _rows(y, "y", T, H, dev, dt)
-        return _run("pw_moe_unpermute", check, dev, stream, lib.pw_moe_unpermute, ctypes.byref(shp), T,
-                    _DTYPES.get(dt, -1), pr, sr, _array(inv, "inv", S, dev, _torch.int32),
-                    _array(w, "w", S, dev, _torch.float32), py, sy)
+        return _call("pw_moe_unpermute", check, dev, lib.pw_moe_unpermute, (
+            ctypes.byref(shp), T, _DTYPES.get(dt, -1), pr, sr, _array(inv, "inv", S, dev, _torch.int32),
+            _array(w, "w", S, dev, _torch.float32), py, sy, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_moe_unpermute", check, e)
 
@@ -548,9 +556,10 @@ def pw_moe_unpermute_backward(shp: PwMoeShape, T: int, dy, rows, inv, w, drows, 
         pd, sd = _rows(dy, "dy", T, H, dev, dt)
         pr, sr = _rows(rows, "rows", S, H, dev, dt)
         po, so = _rows(drows, "drows", S, H, dev, dt)
-        return _run("pw_moe_unpermute_backward", check, dev, stream, lib.pw_moe_unpermute_backward, ctypes.byref(shp),
-                    T, _DTYPES.get(dt, -1), pd, sd, pr, sr, _array(inv, "inv", S, dev, _torch.int32),
-                    _array(w, "w", S, dev, _torch.float32), po, so, _array(dw, "dw", S, dev, _torch.float32))
+        return _call("pw_moe_unpermute_backward", check, dev, lib.pw_moe_unpermute_backward, (
+            ctypes.byref(shp), T, _DTYPES.get(dt, -1), pd, sd, pr, sr, _array(inv, "inv", S, dev, _torch.int32),
+            _array(w, "w", S, dev, _torch.float32), po, so, _array(dw, "dw", S, dev, _torch.float32),
+            _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_moe_unpermute_backward", check, e)
 
@@ -566,11 +575,11 @@ def pw_router_backward(shp: PwMoeShape, T: int, x, router_w, ids, w, dw, dx, dro
         dev, n, S, E = _gpu(x), T * shp.hidden, T * shp.top_k, shp.num_experts * shp.hidden
         f16, f32 = _torch.float16, _torch.float32
         pw, nw = _scratch(workspace, dev)
-        return _run("pw_router_backward", check, dev, stream, lib.pw_router_backward, ctypes.byref(shp), T,
-                    _array(x, "x", n, dev, f16), _array(router_w, "router_w", E, dev, f16),
-                    _array(ids, "ids", S, dev, _torch.int32), _array(w, "w", S, dev, f32),
-                    _array(dw, "dw", S, dev, f32), _array(dx_add, "dx_add", n, dev, f16),
-                    _array(dx, "dx", n, dev, f16), _array(drouter_w, "drouter_w", E, dev, f32), pw, nw)
+        return _call("pw_router_backward", check, dev, lib.pw_router_backward, (
+            ctypes.byref(shp), T, _array(x, "x", n, dev, f16), _array(router_w, "router_w", E, dev, f16),
+            _array(ids, "ids", S, dev, _torch.int32), _array(w, "w", S, dev, f32), _array(dw, "dw", S, dev, f32),
+            _array(dx_add, "dx_add", n, dev, f16), _array(dx, "dx", n, dev, f16),
+            _array(drouter_w, "drouter_w", E, dev, f32), pw, nw, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_router_backward", check, e)
 

@@ -426,6 +426,101 @@ def test_rows_past_32_bits(torch):
     near(f64(dw[-3:]), square, (H // 64 + 8) * U * square, "last dw")
 
 
+def test_more_rows_than_a_grid_has_blocks(torch):
+    """Launches end at 2^20 blocks; the blocks then walk the remaining rows."""
+    T, H = 34_000_001, 8
+    say(f"norm and its gradient: {T} rows of {H}")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((T, H), generator=g, device=DEV, dtype=torch.float16)
+    w, y = torch.ones(H, dtype=torch.float16, device=DEV), torch.empty_like(x)
+    B.pw_rmsnorm(T, H, x, w, EPS, y)
+    ref = x.float() * torch.rsqrt(x.float().square().mean(dim=1, keepdim=True) + EPS)
+    # two fp32 computations, each within ROW half steps, and one rounding to fp16 on this side
+    assert bool(((y.float() - ref).abs() <= ref.abs() * (2.0 ** -11 + 2 * ROW * U) + 2.0 ** -25).all())
+    del x, y, ref
+    T, H, E = 67_200_003, 32, 8
+    say(f"permute and back: {T} rows of {H}")
+    shp = B.shape(H, 32, E, 1)
+    x = torch.randint(0, 255, (T, H), generator=g, device=DEV, dtype=torch.uint8).half()
+    ids = torch.randint(-1, E, (T, 1), generator=g, device=DEV, dtype=torch.int32)
+    off, inv = torch.empty(E + 1, dtype=torch.int32, device=DEV), torch.empty(T, dtype=torch.int32, device=DEV)
+    ws = torch.empty(B.pw_moe_permute_workspace_bytes(shp, T), dtype=torch.uint8, device=DEV)
+    xs = torch.zeros_like(x)
+    B.pw_moe_permute(shp, T, x, ids, xs, off, inv, None, ws)
+    order = torch.argsort(torch.where(ids.reshape(-1) < 0, E, ids.reshape(-1)).to(torch.uint8), stable=True)
+    n = int(off[E])
+    assert n == int((ids >= 0).sum())
+    assert torch.equal(inv[order[:n]], torch.arange(n, dtype=torch.int32, device=DEV)) and bool((inv[order[n:]] == -1).all())
+    for s in range(0, n, 1 << 23):
+        e = min(n, s + (1 << 23))
+        assert torch.equal(xs[s:e], x[order[s:e]])
+    y = torch.empty_like(x)
+    B.pw_moe_unpermute(shp, T, xs, inv, None, y)
+    kept = ids >= 0
+    assert torch.equal(y, torch.where(kept, x, torch.zeros_like(x)))
+    dw = torch.empty((T, 1), device=DEV)
+    B.pw_moe_unpermute_backward(shp, T, x, xs, inv, None, xs, dw)      # whole numbers up to 32 * 254^2: exact in fp32
+    torch.cuda.synchronize()
+    assert torch.equal(dw, torch.where(kept, x.float().square().sum(dim=1, keepdim=True), 0.0))
+
+
+def test_nan_in_masked_places(torch):
+    """Padding holds anything: what a dropped slot or a padded token carries is never read into a result."""
+    nan = float("nan")
+    for T in (40, 900):
+        H, E, k = 160, 12, 3
+        say(f"NaN in the weights, gradients and rows of dropped slots and padded tokens, T={T}")
+        shp = B.shape(H, 32, E, k)
+        ids = draw_ids(3, T, E, k, 0.3)
+        ids[T // 2:] = -1                                # the second half of the batch is padding
+        idd = torch.from_numpy(ids).to(DEV)
+        lost = idd < 0
+        lost |= idd >= E
+        w, dw = torch.softmax(rand(torch, 4, (T, k), "f32"), dim=1).contiguous(), rand(torch, 5, (T, k), "f32")
+        x, add, wr = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (T, H), "f16"), rand(torch, 3, (E, H), "f16")
+        inv = torch.from_numpy(plan(ids, E)[1].astype(np.int32)).to(DEV)
+        rows = rand(torch, 6, (T * k, H), "f16")
+        ws = torch.empty(B.pw_router_backward_workspace_bytes(shp, T), dtype=torch.uint8, device=DEV)
+        got = []
+        for value in (0.0, nan):
+            w2, dw2, x2 = w.masked_fill(lost, value), dw.masked_fill(lost, value), x.clone()
+            x2[T // 2:] = value
+            rows2 = rows.clone()
+            rows2[int((~lost).sum()):] = value
+            dx, dwr, y = torch.empty_like(x), torch.empty((E, H), device=DEV), torch.empty_like(x)
+            drows, dws = torch.zeros_like(rows), torch.empty((T, k), device=DEV)
+            B.pw_router_backward(shp, T, x2, wr, idd, w2, dw2, dx, dwr, ws, dx_add=add)
+            B.pw_moe_unpermute(shp, T, rows2, inv, w2, y)
+            B.pw_moe_unpermute_backward(shp, T, x2, rows2, inv, w2, drows, dws)
+            torch.cuda.synchronize()
+            got.append((dx, dwr, y, drows, dws))
+        assert all(torch.equal(a, b) and bool(a.isfinite().all()) for a, b in zip(*got))
+
+
+def test_broadcast_and_wide_inputs(torch):
+    say("rows that are one row repeated (stride 0), and rows of a much wider matrix")
+    T, H, E, k = 70, 64, 8, 2
+    shp = B.shape(H, 32, E, k)
+    one, wide = rand(torch, 1, (1, H), "f16"), rand(torch, 2, (T, 40 * H), "f16")[:, 8 * H:9 * H]
+    ids = draw_ids(4, T, E, k, 0.0)
+    g = rand(torch, 3, (1, H), "f16")[0]
+    for x in (one.expand(T, H), wide):
+        y, yc = torch.empty((T, H), dtype=torch.float16, device=DEV), torch.empty((T, H), dtype=torch.float16, device=DEV)
+        B.pw_rmsnorm(T, H, x, g, EPS, y, residual=x, residual_out=torch.empty_like(y))
+        B.pw_rmsnorm(T, H, x.contiguous(), g, EPS, yc, residual=x.contiguous(), residual_out=torch.empty_like(y))
+        assert torch.equal(y, yc)
+        xs, _, inv, perm, _, _, _ = run_permute(torch, x, ids, E)
+        assert torch.equal(xs, x.contiguous()[perm.long() // k])
+        big = torch.zeros((T * k, 3 * H), dtype=torch.float16, device=DEV)
+        w, dw, dw2 = rand(torch, 7, (T, k), "f32"), torch.empty((T, k), device=DEV), torch.empty((T, k), device=DEV)
+        B.pw_moe_unpermute_backward(shp, T, x, xs, inv, w, big[:, H:2 * H], dw)
+        plain = torch.empty_like(xs)
+        B.pw_moe_unpermute_backward(shp, T, x.contiguous(), xs, inv, w, plain, dw2)
+        torch.cuda.synchronize()
+        assert torch.equal(big[:, H:2 * H], plain) and torch.equal(dw, dw2)
+        assert bool((big[:, :H] == 0).all()) and bool((big[:, 2 * H:] == 0).all())
+
+
 # ----- the router's gradient --------------------------------------------------
 
 ROUTER_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd", 7, 96, 5, 3, 0.3),
@@ -473,7 +568,7 @@ def test_router_backward(torch, name, T, H, E, k, dropped):
     for got, plus, what in [(dx, A, "dx"), (alone, 0 * A, "dx with nothing to add to")]:
         ref = refx + plus
         near(f64(got), ref, np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + (2 * k + 8) * U * (magx + np.abs(plus)), what)
-    # a stretch adds at most 512 tokens here, at most 64 stretches follow; k + 8 roundings of dl
+    # at most 512 listed rows in turn, at most 64 sums of those; k + 8 roundings of dl
     near(f64(dwr), refw, (min(T, 512) + 64 + 2 * k + 8) * U * magw, "drouter_w")
 
 
