@@ -43,8 +43,8 @@ __device__ __forceinline__ void load_pieces(const PermuteArgs& a, int64_t t, int
 }
 
 // ... and their copies at the places pos[0..k), -1: none.  WAVE: all lanes of a
-// wave have the same places.
-template <int N, bool WAVE>
+// wave have the same places.  STREAM: past the caches.
+template <int N, bool WAVE, bool STREAM = false>
 __device__ __forceinline__ void store_pieces(const PermuteArgs& a, const int* pos, int64_t c0, int lanes,
                                              const piece_t (&v)[kUnroll]) {
   for (int j = 0; j < a.k; ++j) {
@@ -53,7 +53,11 @@ __device__ __forceinline__ void store_pieces(const PermuteArgs& a, const int* po
     uint8_t* dst = a.xs + p * a.xs_stride + c0;
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      if (c0 + u * 16 * lanes < a.row_bytes) *reinterpret_cast<piece_t*>(dst + u * 16 * lanes) = v[u];
+      if (c0 + u * 16 * lanes < a.row_bytes) {
+        piece_t* to = reinterpret_cast<piece_t*>(dst + u * 16 * lanes);
+        if (STREAM) __builtin_nontemporal_store(v[u], to);
+        else *to = v[u];
+      }
   }
 }
 
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(kWave) void permute_scan_kernel(PermuteArgs a) {
 // wave.  Each wave requests its first token's row before all that.
 //
 // NARROW (rows of up to 512 bytes): 1 << shift threads take a token.
-template <bool SCANNED, bool NARROW>
+template <bool SCANNED, bool NARROW, bool STREAM>
 __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a, int shift) {
   __shared__ int total[kMaxExperts];         // the expert's slots
   __shared__ int next[kMaxExperts];          // its slots before this block, then its next place
@@ -317,11 +321,11 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
     const int* mypos = pos + t * a.k;
     if constexpr (NARROW) {
       if (t != own) load_pieces<1>(a, t0 + t, 16 * (int64_t)in_row, lanes, v);
-      store_pieces<1, false>(a, mypos, 16 * (int64_t)in_row, lanes, v);
+      store_pieces<1, false, STREAM>(a, mypos, 16 * (int64_t)in_row, lanes, v);
     } else {
       for (int64_t c0 = 16 * (int64_t)lane; c0 - 16 * lane < a.row_bytes; c0 += kPiece) {
         if (t != own || c0 >= kPiece) load_pieces<kUnroll>(a, t0 + t, c0, kWave, v);
-        store_pieces<kUnroll, true>(a, mypos, c0, kWave, v);
+        store_pieces<kUnroll, true, STREAM>(a, mypos, c0, kWave, v);
       }
     }
     if (a.groups) scatter_scales(a, t0 + t, mypos, in_row, lanes);
@@ -446,6 +450,22 @@ hipError_t run_unpermute_grad(const UnpermuteGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Copies that no cache could keep for their reader go past the caches where
+// they are most of the traffic: four copies a row and 192 MB or more of them
+// (T = 16384, k = 8 137 -> 120 us, T = 32768, k = 4 144 -> 140, 200000 rows of
+// 256 bytes, k = 4 95 -> 72; with two copies 88.4 -> 90.6, and at T = 4096, k = 4,
+// which the 256 MB behind the L2s hold, 19.2 -> 20.3).
+constexpr int64_t kStreamBytes = 192 << 20;
+
+template <bool SCANNED, bool NARROW>
+hipError_t run_scatter(const PermuteArgs& a, unsigned grid, size_t lds, int shift, hipStream_t s) {
+  if (a.k >= 4 && (int64_t)a.T * a.k * a.row_bytes >= kStreamBytes)
+    hipLaunchKernelGGL((permute_scatter_kernel<SCANNED, NARROW, true>), dim3(grid), dim3(kThreads), lds, s, a, shift);
+  else
+    hipLaunchKernelGGL((permute_scatter_kernel<SCANNED, NARROW, false>), dim3(grid), dim3(kThreads), lds, s, a, shift);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_permute(PermuteArgs a, hipStream_t s) {
@@ -474,12 +494,10 @@ hipError_t launch_permute(PermuteArgs a, hipStream_t s) {
   }
   const bool narrow = a.row_bytes <= 512;
   const int shift = lanes_shift((int)(a.row_bytes / 16), kWave);
-  const dim3 grid((unsigned)blocks), block(kThreads);
-  if (p.scan && narrow) hipLaunchKernelGGL((permute_scatter_kernel<true, true>), grid, block, lds, s, a, shift);
-  else if (p.scan) hipLaunchKernelGGL((permute_scatter_kernel<true, false>), grid, block, lds, s, a, shift);
-  else if (narrow) hipLaunchKernelGGL((permute_scatter_kernel<false, true>), grid, block, lds, s, a, shift);
-  else hipLaunchKernelGGL((permute_scatter_kernel<false, false>), grid, block, lds, s, a, shift);
-  return hipGetLastError();
+  const unsigned grid = (unsigned)blocks;
+  if (p.scan)
+    return narrow ? run_scatter<true, true>(a, grid, lds, shift, s) : run_scatter<true, false>(a, grid, lds, shift, s);
+  return narrow ? run_scatter<false, true>(a, grid, lds, shift, s) : run_scatter<false, false>(a, grid, lds, shift, s);
 }
 
 hipError_t launch_unpermute(const UnpermuteArgs& a, int dtype, hipStream_t s) {

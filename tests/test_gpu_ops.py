@@ -300,6 +300,22 @@ def test_permute(torch, name, T, H, E, k, dropped):
         assert run_permute(torch, x, ids, E, scale, perm=False)[3].eq(-9).all()
 
 
+@pytest.mark.parametrize("T,H", [(30001, 1024), (140001, 512), (120001, 256), (230001, 128)])
+def test_permute_of_large_outputs(torch, T, H):
+    """Outputs that go past the caches: wide and narrow rows, with and without the scan launch."""
+    E, k = 60, 4
+    say(f"permute T={T} H={H} k={k}: {T * k * H * 2 >> 20} MiB of copies")
+    ids = draw_ids(5, T // 100, E, k, 0.1)
+    ids = np.tile(ids, (101, 1))[:T].copy()
+    offsets, inv, perm = plan(ids, E)
+    x = rand(torch, 5, (T, H), "f16")
+    xs, off, iv, pm, _, _, raw = run_permute(torch, x, ids, E)
+    n = len(perm)
+    assert np.array_equal(off.cpu().numpy(), offsets) and np.array_equal(iv.cpu().numpy(), inv)
+    assert np.array_equal(pm[:n].cpu().numpy(), perm)
+    assert torch.equal(xs[:n], x[torch.from_numpy(perm // k).to(DEV)]) and bool((raw[n:] == 3).all())
+
+
 def test_permute_same_expert_twice(torch):
     say("permute: tokens that list an expert more than once")
     for T in (50, 3000):
