@@ -241,6 +241,12 @@ hipError_t launch_router(const uint16_t* x, const uint16_t* wr, int T, int H, in
 hipError_t launch_combine_router(const float* o, const float* w_prev, const int32_t* inv, int kparts,
                                  uint16_t* x_out, const uint16_t* wr, int T, int H, int E, int k, int32_t* ids,
                                  float* w, uint32_t* count, float* mass, hipStream_t s);
+// residual += x, the norm of it to xn, then the router on xn (fp16).
+constexpr int kRouterAloneTokens = 256;   // a workgroup a token up to here
+inline bool norm_router_fits(int T, int H) { return T <= kRouterAloneTokens && H <= 8192; }
+hipError_t launch_norm_router(const uint16_t* x, uint16_t* residual, const uint16_t* norm_w, float eps, uint16_t* xn,
+                              const uint16_t* wr, int T, int H, int E, int k, int32_t* ids, float* w, uint32_t* count,
+                              float* mass, hipStream_t s);
 hipError_t launch_status_clear(uint32_t* status, hipStream_t s);
 
 // ----- operators around the layer (strides in elements unless said) --------

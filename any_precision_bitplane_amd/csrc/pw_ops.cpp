@@ -232,10 +232,18 @@ pw_status pw_moe_forward_block(const pw_moe_shape* shape, int32_t T, const uint1
   pw_path_info info;   // options the layer would refuse are refused before the norm runs
   PW_TRY(pw_moe_path_info(shape, T, opts, &info));
   if (opts && opts->event_mode != PW_EVENTS_STAGES && opts->event_mode != PW_EVENTS_KERNELS) return PW_ERR_INVALID_ARG;
-  uint16_t* xn = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + W.xl);
-  PW_TRY(pw_rmsnorm(T, H, PW_F16, x, H, residual, H, residual, H, norm_w, eps, PW_F16, xn, H, nullptr, 0, stream));
-  return pw_moe_forward_routed(shape, T, xn, router_w, blocks, q, y, stat_count, stat_mass, workspace,
-                               workspace_bytes, opts, stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* xn = reinterpret_cast<uint16_t*>(ws + W.xl);
+  if (!norm_router_fits(T, H)) {
+    PW_TRY(pw_rmsnorm(T, H, PW_F16, x, H, residual, H, residual, H, norm_w, eps, PW_F16, xn, H, nullptr, 0, stream));
+    return pw_moe_forward_routed(shape, T, xn, router_w, blocks, q, y, stat_count, stat_mass, workspace,
+                                 workspace_bytes, opts, stream);
+  }
+  int32_t* ids = reinterpret_cast<int32_t*>(ws + W.rids);
+  float* w = reinterpret_cast<float*>(ws + W.rw);
+  PW_TRY(hip_status(launch_norm_router(x, residual, norm_w, eps, xn, router_w, T, H, shape->num_experts, shape->top_k,
+                                       ids, w, stat_count, stat_mass, (hipStream_t)stream)));
+  return pw_moe_forward(shape, T, xn, ids, w, blocks, q, y, workspace, workspace_bytes, opts, stream);
 }
 
 }  // extern "C"

@@ -20,8 +20,7 @@
 // about as much as the work.
 #include <limits.h>
 
-#include "pw_device.h"
-#include "pw_internal.h"
+#include "pw_rows.h"
 
 namespace pw {
 
@@ -186,9 +185,55 @@ __global__ __launch_bounds__(kRouterWaves * kWave) void combine_router_kernel(
   if (threadIdx.x < kWave) select_topk(lg[0], E, k, t, ids, w, count, mass);
 }
 
+// The norm in front of a routed layer and its router in one launch, for the
+// batches that take one workgroup a token: thread c holds chunk c of the row
+// (H <= 8192), the norm's output goes to memory for the expert products and to
+// LDS for the logits.  Sums in the norm's own order (a wave's lanes, then the
+// waves in turn; waves past the row add zeros), so every output has the bits of
+// the two calls apart.  Saves a launch and one reading of the row.
+__global__ __launch_bounds__(kRouterWaves * kWave) void norm_router_kernel(
+    const uint16_t* x, uint16_t* residual, const uint16_t* __restrict__ norm_w, float eps,
+    uint16_t* __restrict__ xn, const uint16_t* __restrict__ wr, int H, int E, int k, int32_t* __restrict__ ids,
+    float* __restrict__ w, uint32_t* __restrict__ count, float* __restrict__ mass) {
+  using R = Row<PW_F16>;
+  __shared__ float lg[1][kMaxExperts];
+  __shared__ float part[kRouterWaves];
+  __shared__ __align__(16) _Float16 xs[8 * kRouterWaves * kWave];
+  const int t = blockIdx.x, c = threadIdx.x;
+  const bool in = 8 * c < H;
+  const size_t at = (size_t)t * H + 8 * c;
+  floatx8 v = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  R::chunk g = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (in) {
+    g = R::load(reinterpret_cast<const _Float16*>(norm_w) + 8 * c);
+    v = R::wide(R::load(reinterpret_cast<const _Float16*>(x) + at)) +
+        R::wide(R::load(reinterpret_cast<const _Float16*>(residual) + at));
+    R::store(reinterpret_cast<_Float16*>(residual) + at, R::narrow(v));
+  }
+  float sq = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[j], v[j], sq);
+  sq = wave_sum(sq);
+  if ((c & (kWave - 1)) == 0) part[c / kWave] = sq;
+  __syncthreads();
+  sq = part[0];
+#pragma unroll
+  for (int i = 1; i < kRouterWaves; ++i) sq += part[i];
+  const float rstd = rsqrtf(sq / (float)H + eps);
+  if (in) {
+    const R::chunk y = R::narrow(v * rstd * R::wide(g));
+    R::store(reinterpret_cast<_Float16*>(xn) + at, y);
+    R::store(xs + 8 * c, y);
+  }
+  __syncthreads();
+  router_logits<1>(reinterpret_cast<const uint16_t*>(xs), (size_t)H, wr, 1, H, E, lg);
+  __syncthreads();
+  if (threadIdx.x < kWave) select_topk(lg[0], E, k, t, ids, w, count, mass);
+}
+
 hipError_t launch_router(const uint16_t* x, const uint16_t* wr, int T, int H, int E, int k, int32_t* ids, float* w,
                          uint32_t* count, float* mass, hipStream_t s) {
-  if (T <= 256) {
+  if (T <= kRouterAloneTokens) {
     hipLaunchKernelGGL(router_kernel<1>, dim3(T), dim3(kRouterWaves * kWave), 0, s, x, wr, T, H, E, k, ids, w, count,
                        mass);
   } else {
@@ -196,6 +241,15 @@ hipError_t launch_router(const uint16_t* x, const uint16_t* wr, int T, int H, in
     hipLaunchKernelGGL(router_kernel<kRouterTokens>, dim3((T + kRouterTokens - 1) / kRouterTokens),
                        dim3(kRouterWaves * kWave), 0, s, x, wr, T, H, E, k, ids, w, count, mass);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_router(const uint16_t* x, uint16_t* residual, const uint16_t* norm_w, float eps, uint16_t* xn,
+                              const uint16_t* wr, int T, int H, int E, int k, int32_t* ids, float* w,
+                              uint32_t* count, float* mass, hipStream_t s) {
+  if (!norm_router_fits(T, H)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(norm_router_kernel, dim3(T), dim3(kRouterWaves * kWave), 0, s, x, residual, norm_w, eps, xn, wr,
+                     H, E, k, ids, w, count, mass);
   return hipGetLastError();
 }
 

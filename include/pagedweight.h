@@ -474,7 +474,8 @@ pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, co
 /* The routed half of a transformer block: norm, router and layer in one call,
  *     residual += x;   y = layer(pw_rmsnorm(residual))
  * The next norm's residual addition adds y.  Equal bit for bit to pw_rmsnorm
- * (fp16, in place on residual) followed by pw_moe_forward_routed on its output.
+ * (fp16, in place on residual) followed by pw_moe_forward_routed on its output;
+ * the norm and the router are one launch for up to 256 tokens of H <= 8192.
  *   x         fp16 [T][H];  residual  fp16 [T][H], updated;  norm_w  fp16 [H]
  *   y         fp16 [T][H], overwritten; may be x
  *   the rest  as for pw_rmsnorm and pw_moe_forward_routed */

@@ -601,10 +601,19 @@ def test_router_backward_of_no_tokens(torch):
 
 # ----- together -----------------------------------------------------------------
 
-@pytest.mark.parametrize("wl", ["tiny", "qwen_decode"])
-def test_forward_block(torch, wl):
-    say(f"forward_block {wl}: equal to norm, router and layer called apart")
-    L = synth.make_layer(synth.WORKLOADS[wl])
+@pytest.mark.parametrize("wl,T", [("tiny", 16), ("tiny", 256), ("tiny", 257), ("qwen_decode", 4), ("qwen_decode", 1)])
+def test_forward_block(torch, wl, T):
+    say(f"forward_block {wl} T={T}: equal to norm, router and layer called apart")
+    check_block(torch, synth.make_layer(synth.WORKLOADS[wl].with_T(T)))
+
+
+@pytest.mark.parametrize("H,T", [(32, 3), (64, 5), (96, 2), (288, 9), (1056, 4), (8192, 2), (8224, 2)])
+def test_forward_block_sizes(torch, H, T):
+    say(f"forward_block H={H} T={T}: narrow and long rows, one launch up to H = 8192 and two above")
+    check_block(torch, synth.make_layer(synth.Workload("block", H=H, I=64, E=5, k=2, T=T, seed=77)))
+
+
+def check_block(torch, L):
     dev = DeviceLayer(L, device=DEV)
     w = L.wl
     x, res0 = rand(torch, 1, (w.T, w.H), "f16"), rand(torch, 2, (w.T, w.H), "f16", 2.0)
@@ -622,6 +631,29 @@ def test_forward_block(torch, wl):
     assert torch.equal(res, res2) and torch.equal(y, y2) and torch.equal(stats[0][0], stats[1][0])
     assert torch.equal(x3, y) and torch.equal(res3, res) and dev.status() == 0
     assert float(y.float().abs().max()) > 0
+
+
+def test_forward_block_in_a_graph(torch):
+    say("forward_block captured and replayed: the residual stream goes on, as in eager calls")
+    L = synth.make_layer(synth.WORKLOADS["tiny"])
+    dev, w = DeviceLayer(L, device=DEV), L.wl
+    x, res0, g = rand(torch, 1, (w.T, w.H), "f16"), rand(torch, 2, (w.T, w.H), "f16"), rand(torch, 3, (1, w.H), "f16")[0]
+    wr = torch.from_numpy(synth.draw_router_weights(5, w.E, w.H)).to(DEV)
+    res, y = res0.clone(), torch.empty_like(x)
+    call = lambda r, o: B.pw_moe_forward_block(dev.shape, w.T, x, r, g, EPS, wr, dev.blocks[0], dev.q, o, None, None, dev.ws)
+    call(res, y)
+    torch.cuda.synchronize()
+    res.copy_(res0)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        call(res, y)
+    eager, ye = res0.clone(), torch.empty_like(x)
+    for n in range(4):
+        gr.replay()
+        torch.cuda.synchronize()
+        call(eager, ye)
+        torch.cuda.synchronize()
+        assert torch.equal(res, eager) and torch.equal(y, ye), n
 
 
 def experts(torch, L, e, rows):
