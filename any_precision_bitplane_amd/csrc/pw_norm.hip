@@ -334,13 +334,14 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
     }
   } else {
     // several rows at a time: their lanes' shares meet first
-    static_assert(kRows == 1 || (NV == 1 && WPR == 1), "one chunk a lane");
-    __shared__ floatx8 sums[kRows * LPR];
+    static_assert(kRows == 1 || NV == 1, "one chunk a lane");
+    constexpr int kLanes = LPR * WPR;   // of a row: thread own * kLanes + first
+    __shared__ floatx8 sums[kRows * kLanes];
     sums[threadIdx.x] = dg[0];
     __syncthreads();
-    if ((int)threadIdx.x < LPR && (int)threadIdx.x < C) {
+    if ((int)threadIdx.x < kLanes && (int)threadIdx.x < C) {
       floatx8 s = dg[0];
-      for (int i = 1; i < kRows; ++i) s += sums[i * LPR + threadIdx.x];
+      for (int i = 1; i < kRows; ++i) s += sums[i * kLanes + threadIdx.x];
       Row<PW_F32>::store(p + 8 * threadIdx.x, s);
     }
   }
@@ -388,6 +389,7 @@ hipError_t pick_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) 
   if (C <= 16) return run_norm_grad<DT, 16, 1, 1>(a, dweight, s);
   if (C <= 32) return run_norm_grad<DT, 32, 1, 1>(a, dweight, s);
   if (C <= 64) return run_norm_grad<DT, 64, 1, 1>(a, dweight, s);
+  if (C <= 128) return run_norm_grad<DT, 64, 2, 1>(a, dweight, s);
   if (C <= 256) return run_norm_grad<DT, 64, 4, 1>(a, dweight, s);
   if (C <= 512) return run_norm_grad<DT, 64, 4, 2>(a, dweight, s);
   if (C <= 1024) return run_norm_grad<DT, 64, 16, 1>(a, dweight, s);
