@@ -383,6 +383,8 @@ class _Refused(Exception):
 
 def _gpu(t) -> int:
     """The GPU of the call's first tensor."""
+    if t is None:
+        raise _Refused("a tensor is missing")
     dev = t.get_device()
     if dev < 0:
         raise _Refused("tensors must be on a GPU")
@@ -458,6 +460,8 @@ def pw_rmsnorm(T: int, H: int, x, weight, eps: float, y, residual=None, residual
     lib = _load_ops()
     try:
         dev, dt = _gpu(x), x.dtype
+        if y is None:
+            raise _Refused("a tensor is missing")
         px, sx = _rows(x, "x", T, H, dev, dt)
         pr, sr = _rows(residual, "residual", T, H, dev, dt)
         po, so = _rows(residual_out, "residual_out", T, H, dev, dt)

@@ -252,8 +252,7 @@ hipError_t launch_status_clear(uint32_t* status, hipStream_t s);
 // ----- operators around the layer (strides in elements unless said) --------
 constexpr int kMaxNormHidden = 32768;   // a block of sixteen waves holds a row, four chunks a lane
 constexpr int kNormGroup = 128;         // columns per scale of the 8-bit output
-constexpr int kNormFewRows = 1024;      // up to here a row is spread over all the waves it can use
-constexpr int kNormGradBlocks = 512;    // blocks (and shares of the weight's gradient) of the norm's backward pass
+constexpr int kNormGradBlocks = 512;    // most blocks (and shares of the weight's gradient) of the norm's backward pass
 
 struct NormArgs {
   int T, H;

@@ -93,12 +93,36 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
   const int own = wave / WPR * (kWave / LPR) + (LPR == kWave ? 0 : lane / LPR);   // the lane's row of the block
   const int first = (wave % WPR) * kWave + (lane & (LPR - 1));                    // its first chunk of that row
   const int C = a.H / 8;
-  int parity = 0;
-  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += (int64_t)gridDim.x * kRows, parity ^= 1) {
-    const int64_t row = base + own;
-    const bool live = row < a.T;
+  typedef typename R::chunk chunk;
+  // Past the row's end the first chunk is read again, which nothing uses.
+  int at[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = first + i * WPR * kWave;
+    at[i] = c < C ? 8 * c : 0;
+  }
+  chunk xc[NV], rc[NV], g[NV];
+  auto fetch = [&](int64_t row) {
+    if (row >= a.T) return;
     const elem* x = static_cast<const elem*>(a.x) + row * a.x_stride;
     const elem* res = static_cast<const elem*>(a.residual) + row * a.residual_stride;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xc[i] = R::load(x + at[i]);
+      if (a.residual) rc[i] = R::load(res + at[i]);
+    }
+  };
+  // The weight is requested with the row, not after its sum (fp16 [16384][4096]
+  // 97 -> 93 us, bf16 to e4m3 91 -> 81), and the row before the loop, ahead of
+  // what the compiler moves out of it (bf16 [65536][2048] alone 98 -> 87).
+#pragma unroll
+  for (int i = 0; i < NV; ++i) g[i] = R::load(static_cast<const elem*>(a.weight) + at[i]);
+  fetch((int64_t)blockIdx.x * kRows + own);
+  int parity = 0;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  for (int64_t base = (int64_t)blockIdx.x * kRows; base < a.T; base += step, parity ^= 1) {
+    const int64_t row = base + own;
+    const bool live = row < a.T;
     elem* out = static_cast<elem*>(a.residual_out) + row * a.residual_out_stride;
     floatx8 v[NV];
     float sq = 0.f;
@@ -107,24 +131,21 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
       const int c = first + i * WPR * kWave;
       v[i] = floatx8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (!live || c >= C) continue;
-      v[i] = R::wide(R::load(x + 8 * c));
+      v[i] = R::wide(xc[i]);
       if (a.residual) {
-        v[i] += R::wide(R::load(res + 8 * c));
+        v[i] += R::wide(rc[i]);
         if (a.residual_out) R::store(out + 8 * c, R::narrow(v[i]));
       }
     }
+    fetch(row + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) sq = __builtin_fmaf(v[i][j], v[i][j], sq);
     sq = row_sum<LPR, WPR>(sq, part[parity], wave);
     const float rstd = rsqrtf(sq / (float)a.H + a.eps);
-    const elem* g = static_cast<const elem*>(a.weight);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = first + i * WPR * kWave;
-      if (c < C) v[i] = v[i] * rstd * R::wide(R::load(g + 8 * c));
-    }
+    for (int i = 0; i < NV; ++i) v[i] = v[i] * rstd * R::wide(g[i]);
     if constexpr (!Q8) {
       elem* y = static_cast<elem*>(a.y) + row * a.y_stride;
 #pragma unroll
@@ -184,8 +205,13 @@ hipError_t run_norm(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Few rows: a row over as many waves as it has chunks for, so each lane waits
-// for one load.  Many rows: four chunks a lane, so a row takes few waves.
+// A row over as many lanes as it has chunks for, up to sixteen waves, so each
+// lane waits for one load.  Four chunks a lane and a quarter of the waves were
+// slower nearly everywhere (fp16 [64][2048] 4.8 us against 3.0, [16384][4096]
+// 103.8 against 97.1, fp32 205 against 185; faster by 5% for fp16 [4096][4096],
+// which stays in the caches).
+// Measured with the residual: fp16 [16384][4096] 93 us, 5.7 TB/s; bf16 to e4m3
+// 81 us, 5.8 TB/s; fp32 193 us, 5.6 TB/s (a large copy: 5.0).
 template <int DT, bool Q8>
 hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
   const int C = a.H / 8;
@@ -193,19 +219,11 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
   if (C <= 16) return run_norm<DT, 16, 1, 1, Q8>(a, s);
   if (C <= 32) return run_norm<DT, 32, 1, 1, Q8>(a, s);
   if (C <= 64) return run_norm<DT, 64, 1, 1, Q8>(a, s);
-  if (a.T <= kNormFewRows) {
-    if (C <= 128) return run_norm<DT, 64, 2, 1, Q8>(a, s);
-    if (C <= 256) return run_norm<DT, 64, 4, 1, Q8>(a, s);
-    if (C <= 512) return run_norm<DT, 64, 8, 1, Q8>(a, s);
-    if (C <= 1024) return run_norm<DT, 64, 16, 1, Q8>(a, s);
-    if (C <= 2048) return run_norm<DT, 64, 16, 2, Q8>(a, s);
-    return run_norm<DT, 64, 16, 4, Q8>(a, s);
-  }
-  if (C <= 128) return run_norm<DT, 64, 1, 2, Q8>(a, s);
-  if (C <= 256) return run_norm<DT, 64, 1, 4, Q8>(a, s);
-  if (C <= 512) return run_norm<DT, 64, 2, 4, Q8>(a, s);
-  if (C <= 1024) return run_norm<DT, 64, 4, 4, Q8>(a, s);
-  if (C <= 2048) return run_norm<DT, 64, 8, 4, Q8>(a, s);
+  if (C <= 128) return run_norm<DT, 64, 2, 1, Q8>(a, s);
+  if (C <= 256) return run_norm<DT, 64, 4, 1, Q8>(a, s);
+  if (C <= 512) return run_norm<DT, 64, 8, 1, Q8>(a, s);
+  if (C <= 1024) return run_norm<DT, 64, 16, 1, Q8>(a, s);
+  if (C <= 2048) return run_norm<DT, 64, 16, 2, Q8>(a, s);
   return run_norm<DT, 64, 16, 4, Q8>(a, s);
 }
 
@@ -216,7 +234,7 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 // r (both sums in the same pass), so the forward keeps nothing but its
 // residual output.  A block walks every gridDim-th group of rows and keeps its
 // share of dg in registers; the shares meet in a second kernel, in a fixed
-// order.
+// order.  Measured: bf16 [16384][4096] with dresidual 98 us, 5.5 TB/s.
 //
 // AHEAD: the next row is requested before the current one is used (dx may be
 // written over an input: the rows in flight are the block's own later ones).
@@ -370,7 +388,12 @@ template <int DT, int LPR, int WPR, int NV>
 hipError_t run_norm_grad(const NormGradArgs& a, float* dweight, hipStream_t s) {
   constexpr int kRows = block_rows(LPR, WPR);
   const unsigned want = ((unsigned)a.T + kRows - 1) / kRows;
-  const unsigned grid = want < (unsigned)kNormGradBlocks ? want : (unsigned)kNormGradBlocks;
+  // Each block's share of dweight is written and read, so no more blocks than
+  // keep the memory busy: one a CU, two where a row is 4 KB or less (bf16
+  // [16384][4096] 98 us against 105 with two, [1024][8192] 19 against 26;
+  // [16384][2048] 61 against 55).
+  const unsigned most = (int64_t)a.H * (DT == PW_F32 ? 4 : 2) <= 4096 ? kNormGradBlocks : kNormGradBlocks / 2;
+  const unsigned grid = want < most ? want : most;
   // registers of a lane's chunks: 4 (16-bit) or 8 (fp32) for each of three matrices, again for the row ahead
   constexpr int kChunkRegs = NV * (DT == PW_F32 ? 8 : 4);
   constexpr bool kLean = WPR == 16 && kChunkRegs >= 16, kAhead = !kLean && kChunkRegs <= 16;

@@ -183,8 +183,8 @@ def test_rmsnorm_backward(torch, T, H, name):
     for got, add, what in [(dx, a, "dx"), (alone, np.zeros_like(a), "dx without the stream's gradient")]:
         ref, dgr = oo.rmsnorm_backward(d, rr, gg, EPS, add)
         near(f64(got), ref, np.abs(ref) * rel + ab + 2 * ROW * U * (mag + np.abs(add)), what)
-    # a lane adds at most ceil(T / 512) rows, a block at most 32 lanes' shares, then 512 blocks: 8 a thread and six levels
-    chain = -(-T // 512) + 32 + 8 + 6 + ROW
+    # a lane adds at most ceil(T / 256) rows, a block at most 32 lanes' shares, then 512 blocks: 8 a thread and six levels
+    chain = -(-T // 256) + 32 + 8 + 6 + ROW
     near(f64(dg), dgr, chain * U * np.sum(np.abs(d * rr * s), axis=0), "dweight")
 
 
@@ -843,6 +843,10 @@ def test_binding_refusals(torch):
     ws = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
     x, g, xs = h(T, H), h(H), h(T * k, H)
     bad = [
+        lambda: B.pw_rmsnorm(T, H, None, g, EPS, x),
+        lambda: B.pw_rmsnorm(T, H, x, None, EPS, x),
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, None),
+        lambda: B.pw_moe_unpermute(shp, T, xs, None, None, x),
         lambda: B.pw_rmsnorm(T, H, x, f(H), EPS, x),                              # weight of another type
         lambda: B.pw_rmsnorm(T, H, x, g, EPS, f(T, H)),                           # output of another type
         lambda: B.pw_rmsnorm(T, H, h(H, T).t(), g, EPS, x),                       # columns apart
