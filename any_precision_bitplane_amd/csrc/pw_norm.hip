@@ -134,7 +134,7 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
       v[i] = R::wide(xc[i]);
       if (a.residual) {
         v[i] += R::wide(rc[i]);
-        if (a.residual_out) R::store(out + 8 * c, R::narrow(v[i]));
+        if (a.residual_out) R::store_once(out + 8 * c, R::narrow(v[i]));
       }
     }
     fetch(row + step);
@@ -151,7 +151,7 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = first + i * WPR * kWave;
-        if (live && c < C) R::store(y + 8 * c, R::narrow(v[i]));
+        if (live && c < C) R::store_once(y + 8 * c, R::narrow(v[i]));
       }
     } else {
       // A NaN or an infinity counts as infinity, so it shows in the group's maximum.
@@ -178,17 +178,18 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
         const bool finite = most < INFINITY;
         const float scale = finite ? fmaxf(most / kE4m3Max, kScaleMin) : __builtin_nanf("");
         const float inv = 1.f / scale;
-        uint32_t lo = 0x7F7F7F7Fu, hi = 0x7F7F7F7Fu;
+        typedef uint32_t codes_t __attribute__((ext_vector_type(2)));
+        codes_t codes = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
         if (finite) {
           floatx8 q;
 #pragma unroll
           for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(v[i][j] * inv, -kE4m3Max), kE4m3Max);
           int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-          lo = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], p, true);
+          codes[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], p, true);
           p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-          hi = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], p, true);
+          codes[1] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], p, true);
         }
-        *reinterpret_cast<uint2*>(y + 8 * c) = make_uint2(lo, hi);
+        __builtin_nontemporal_store(codes, reinterpret_cast<codes_t*>(y + 8 * c));   // as store_once
         if (a.group ? (c % (kNormGroup / 8) == 0) : c == 0)
           a.scale[row * groups + (a.group ? c / (kNormGroup / 8) : 0)] = scale;
       }
@@ -210,8 +211,8 @@ hipError_t run_norm(const NormArgs& a, hipStream_t s) {
 // slower nearly everywhere (fp16 [64][2048] 4.8 us against 3.0, [16384][4096]
 // 103.8 against 97.1, fp32 205 against 185; faster by 5% for fp16 [4096][4096],
 // which stays in the caches).
-// Measured with the residual: fp16 [16384][4096] 93 us, 5.7 TB/s; bf16 to e4m3
-// 81 us, 5.8 TB/s; fp32 193 us, 5.6 TB/s (a large copy: 5.0).
+// Measured with the residual: fp16 [16384][4096] 90 us, 5.9 TB/s; bf16 to e4m3
+// 78 us, 6.0 TB/s; fp32 185 us, 5.8 TB/s (a large copy: 5.0).
 template <int DT, bool Q8>
 hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
   const int C = a.H / 8;
@@ -234,7 +235,7 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 // r (both sums in the same pass), so the forward keeps nothing but its
 // residual output.  A block walks every gridDim-th group of rows and keeps its
 // share of dg in registers; the shares meet in a second kernel, in a fixed
-// order.  Measured: bf16 [16384][4096] with dresidual 98 us, 5.5 TB/s.
+// order.  Measured: bf16 [16384][4096] with dresidual 97 us, 5.6 TB/s.
 //
 // AHEAD: the next row is requested before the current one is used (dx may be
 // written over an input: the rows in flight are the block's own later ones).
@@ -338,7 +339,7 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(
       const floatx8 r = R::wide(rc[i]), d = R::wide(dc[i]);
       floatx8 v = rstd * (R::wide(LEAN ? R::load(gain + 8 * c) : gc[LEAN ? 0 : i]) * d - r * f);
       if (adds) v += R::wide(LEAN ? R::load(dres + 8 * c) : ac[i]);
-      R::store(dx + 8 * c, R::narrow(v));
+      R::store_once(dx + 8 * c, R::narrow(v));
       dg[i] += d * r * rstd;
     }
   }

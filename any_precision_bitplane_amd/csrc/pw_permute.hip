@@ -45,8 +45,10 @@ __device__ __forceinline__ void load_pieces(const PermuteArgs& a, int64_t t, int
 }
 
 // ... and their copies at the places pos[0..k), -1: none.  WAVE: all lanes of a
-// wave have the same places.  STREAM: past the caches.
-template <int N, bool WAVE, bool STREAM = false>
+// wave have the same places.  Stored past the L2s, which hold none of it until
+// its reader starts (k = 4, H = 2048, fp16: T = 1024 9.9 -> 8.7 us, 16384 78 ->
+// 61; at worst 20.1 -> 20.8, at 4096).
+template <int N, bool WAVE>
 __device__ __forceinline__ void store_pieces(const PermuteArgs& a, const int* pos, int64_t c0, int lanes,
                                              const piece_t (&v)[kUnroll]) {
   for (int j = 0; j < a.k; ++j) {
@@ -55,11 +57,8 @@ __device__ __forceinline__ void store_pieces(const PermuteArgs& a, const int* po
     uint8_t* dst = a.xs + p * a.xs_stride + c0;
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      if (c0 + u * 16 * lanes < a.row_bytes) {
-        piece_t* to = reinterpret_cast<piece_t*>(dst + u * 16 * lanes);
-        if (STREAM) __builtin_nontemporal_store(v[u], to);
-        else *to = v[u];
-      }
+      if (c0 + u * 16 * lanes < a.row_bytes)
+        __builtin_nontemporal_store(v[u], reinterpret_cast<piece_t*>(dst + u * 16 * lanes));
   }
 }
 
@@ -233,7 +232,7 @@ __global__ __launch_bounds__(kWave) void permute_scan_kernel(PermuteArgs a) {
 // wave.  Each wave requests its first token's row before all that.
 //
 // NARROW (rows of up to 512 bytes): 1 << shift threads take a token.
-template <bool SCANNED, bool NARROW, bool STREAM>
+template <bool SCANNED, bool NARROW>
 __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a, int shift) {
   __shared__ int total[kMaxExperts];         // the expert's slots
   __shared__ int next[kMaxExperts];          // its slots before this block, then its next place
@@ -324,11 +323,11 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
     const int* mypos = pos + t * a.k;
     if constexpr (NARROW) {
       if (t != own) load_pieces<1>(a, t0 + t, 16 * (int64_t)in_row, lanes, v);
-      store_pieces<1, false, STREAM>(a, mypos, 16 * (int64_t)in_row, lanes, v);
+      store_pieces<1, false>(a, mypos, 16 * (int64_t)in_row, lanes, v);
     } else {
       for (int64_t c0 = 16 * (int64_t)lane; c0 - 16 * lane < a.row_bytes; c0 += kPiece) {
         if (t != own || c0 >= kPiece) load_pieces<kUnroll>(a, t0 + t, c0, kWave, v);
-        store_pieces<kUnroll, true, STREAM>(a, mypos, c0, kWave, v);
+        store_pieces<kUnroll, true>(a, mypos, c0, kWave, v);
       }
     }
     if (a.groups) scatter_scales(a, t0 + t, mypos, in_row, lanes);
@@ -338,8 +337,9 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
 // y[t] = sum_j w[t][j] rows[inv[t k + j]]; w null: ones.  `lanes` threads (a
 // power of two) share a token, or one of the pieces of a longer row, each
 // taking one chunk of eight columns; the rows of four slots are requested
-// together.  Bound by memory: bf16, T = 16383, H = 4096, k = 2 70.8 us, 5.7 TB/s.
-template <int DT>
+// together.  Bound by memory: bf16, T = 16383, H = 4096, k = 2 68 us, 5.9 TB/s.
+// STREAM: the rows are read past the L2s.
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a, int shift, int pieces) {
   using R = Row<DT>;
   using elem = typename R::elem;
@@ -364,24 +364,28 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteArgs a, in
         in[u] = p >= 0 && p < S;
         if (!in[u]) continue;
         w[u] = a.w ? a.w[s] : 1.f;
-        v[u] = R::load(static_cast<const elem*>(a.rows) + p * a.rows_stride + 8 * c);
+        const elem* row = static_cast<const elem*>(a.rows) + p * a.rows_stride + 8 * c;
+        v[u] = STREAM ? R::load_once(row) : R::load(row);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (in[u]) acc += w[u] * R::wide(v[u]);
     }
-    R::store(static_cast<elem*>(a.y) + t * a.y_stride + 8 * c, R::narrow(acc));
+    R::store_once(static_cast<elem*>(a.y) + t * a.y_stride + 8 * c, R::narrow(acc));
   }
 }
 
 // Gradient of unpermute, one slot at a time: `lanes` threads of a wave read the
 // token's dy (k times, all but the first from the caches) and the slot's row,
-// write drows and sum dw.  Bound by memory: fp16, T = 8191, H = 2048, k = 4
-// 60 us, 5.0 TB/s.
-template <int DT>
+// write drows and sum dw.  drows is stored past the L2s, which leaves them to dy
+// (bf16, T = 4096, H = 4096, k = 2 37.6 -> 31.4 us; never slower); STREAM: the
+// rows are read past them too.
+// Bound by memory: fp16, T = 8191, H = 2048, k = 4 53 us, 5.7 TB/s.
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(kThreads) void unpermute_grad_kernel(UnpermuteGradArgs a, int shift) {
   using R = Row<DT>;
   using elem = typename R::elem;
+  typedef typename R::chunk chunk;
   const int C = a.H / 8;
   const int lanes = 1 << shift;
   const int per_block = kThreads >> shift;
@@ -398,15 +402,17 @@ __global__ __launch_bounds__(kThreads) void unpermute_grad_kernel(UnpermuteGradA
       const elem* dy = static_cast<const elem*>(a.dy) + s / a.k * a.dy_stride;
       const elem* row = static_cast<const elem*>(a.rows) + p * a.rows_stride;
       elem* drow = static_cast<elem*>(a.drows) + p * a.drows_stride;
-      constexpr int U = DT == PW_F32 ? 2 : 4;   // chunks requested together (fp32: registers)
+      // chunks requested together (fp32, T = 8192, H = 2048, k = 8: two 241 us, four 258, eight 224; fp16,
+      // rows of 512 columns: four 66, eight 87)
+      constexpr int U = DT == PW_F32 ? 8 : 4;
       for (int c0 = lane; c0 < C; c0 += U * lanes) {
-        typename R::chunk d[U], r[U];
+        chunk d[U], r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int c = c0 + u * lanes;
           if (c >= C) continue;
           d[u] = R::load(dy + 8 * c);
-          if (a.dw) r[u] = R::load(row + 8 * c);
+          if (a.dw) r[u] = STREAM ? R::load_once(row + 8 * c) : R::load(row + 8 * c);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -418,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_grad_kernel(UnpermuteGradA
 #pragma unroll
             for (int i = 0; i < 8; ++i) dot = __builtin_fmaf(dv[i], rv[i], dot);
           }
-          R::store(drow + 8 * c, R::narrow(w * dv));
+          __builtin_nontemporal_store(R::narrow(w * dv), reinterpret_cast<chunk*>(drow + 8 * c));   // fp32 too
         }
       }
     }
@@ -437,37 +443,35 @@ int lanes_shift(int chunks, int most) {
 
 unsigned grid_for(int64_t blocks) { return (unsigned)(blocks < (int64_t)kMaxGrid ? blocks : (int64_t)kMaxGrid); }
 
+// Rows of 16 bits that fill half the 256 MB behind the L2s are read past the L2s
+// (T = 32768, H = 2048, k = 4 119 -> 110 us, T = 8192 31.7 -> 29.9; T = 4096
+// 14.2 -> 16.1; fp32, T = 16384, H = 4096, k = 2 144 -> 152).
+constexpr int64_t kBehindL2 = 256 << 20;
+
 template <int DT>
 hipError_t run_unpermute(const UnpermuteArgs& a, hipStream_t s) {
   const int shift = lanes_shift(a.H / 8, kThreads);
   const int per_block = kThreads >> shift, pieces = (a.H / 8 + (1 << shift) - 1) >> shift;
-  hipLaunchKernelGGL((unpermute_kernel<DT>), dim3(grid_for(((int64_t)a.T * pieces + per_block - 1) / per_block)),
-                     dim3(kThreads), 0, s, a, shift, pieces);
+  const dim3 grid(grid_for(((int64_t)a.T * pieces + per_block - 1) / per_block));
+  if (DT != PW_F32 && (int64_t)a.T * a.k * a.H * 2 >= kBehindL2 / 2)
+    hipLaunchKernelGGL((unpermute_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, shift, pieces);
+  else
+    hipLaunchKernelGGL((unpermute_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, shift, pieces);
   return hipGetLastError();
 }
 
+// Rows of 16 bits that the 256 MB behind the L2s cannot hold beside drows and
+// dy are read past the L2s (bf16, T = 8192, H = 4096, k = 2, 336 MB, 70.8 -> 59.3
+// us; T = 3000, 123 MB, 20.9 -> 22.8; fp32, T = 8192, k = 2 143 -> 152).
 template <int DT>
 hipError_t run_unpermute_grad(const UnpermuteGradArgs& a, hipStream_t s) {
   const int shift = lanes_shift(a.H / 8, kWave);
   const int per_block = kThreads >> shift;
-  hipLaunchKernelGGL((unpermute_grad_kernel<DT>), dim3(grid_for(((int64_t)a.T * a.k + per_block - 1) / per_block)),
-                     dim3(kThreads), 0, s, a, shift);
-  return hipGetLastError();
-}
-
-// Copies that no cache could keep for their reader go past the caches where
-// they are most of the traffic: four copies a row and 192 MB or more of them
-// (T = 16384, k = 8 137 -> 120 us, T = 32768, k = 4 144 -> 140, 200000 rows of
-// 256 bytes, k = 4 95 -> 72; with two copies 88.4 -> 90.6, and at T = 4096, k = 4,
-// which the 256 MB behind the L2s hold, 19.2 -> 20.3).
-constexpr int64_t kStreamBytes = 192 << 20;
-
-template <bool SCANNED, bool NARROW>
-hipError_t run_scatter(const PermuteArgs& a, unsigned grid, size_t lds, int shift, hipStream_t s) {
-  if (a.k >= 4 && (int64_t)a.T * a.k * a.row_bytes >= kStreamBytes)
-    hipLaunchKernelGGL((permute_scatter_kernel<SCANNED, NARROW, true>), dim3(grid), dim3(kThreads), lds, s, a, shift);
+  const dim3 grid(grid_for(((int64_t)a.T * a.k + per_block - 1) / per_block));
+  if (DT != PW_F32 && (int64_t)a.T * (2 * a.k + 1) * a.H * 2 > kBehindL2)
+    hipLaunchKernelGGL((unpermute_grad_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, shift);
   else
-    hipLaunchKernelGGL((permute_scatter_kernel<SCANNED, NARROW, false>), dim3(grid), dim3(kThreads), lds, s, a, shift);
+    hipLaunchKernelGGL((unpermute_grad_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, shift);
   return hipGetLastError();
 }
 
@@ -501,10 +505,12 @@ hipError_t launch_permute(PermuteArgs a, hipStream_t s) {
   }
   const bool narrow = a.row_bytes <= 512;
   const int shift = lanes_shift((int)(a.row_bytes / 16), kWave);
-  const unsigned grid = (unsigned)blocks;
-  if (p.scan)
-    return narrow ? run_scatter<true, true>(a, grid, lds, shift, s) : run_scatter<true, false>(a, grid, lds, shift, s);
-  return narrow ? run_scatter<false, true>(a, grid, lds, shift, s) : run_scatter<false, false>(a, grid, lds, shift, s);
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  if (p.scan && narrow) hipLaunchKernelGGL((permute_scatter_kernel<true, true>), grid, block, lds, s, a, shift);
+  else if (p.scan) hipLaunchKernelGGL((permute_scatter_kernel<true, false>), grid, block, lds, s, a, shift);
+  else if (narrow) hipLaunchKernelGGL((permute_scatter_kernel<false, true>), grid, block, lds, s, a, shift);
+  else hipLaunchKernelGGL((permute_scatter_kernel<false, false>), grid, block, lds, s, a, shift);
+  return hipGetLastError();
 }
 
 hipError_t launch_unpermute(const UnpermuteArgs& a, int dtype, hipStream_t s) {

@@ -302,7 +302,7 @@ def test_permute(torch, name, T, H, E, k, dropped):
 
 @pytest.mark.parametrize("T,H", [(30001, 1024), (140001, 512), (120001, 256), (230001, 128)])
 def test_permute_of_large_outputs(torch, T, H):
-    """Outputs that go past the caches: wide and narrow rows, with and without the scan launch."""
+    """Wide and narrow rows, with and without the scan launch, at hundreds of MiB."""
     E, k = 60, 4
     say(f"permute T={T} H={H} k={k}: {T * k * H * 2 >> 20} MiB of copies")
     ids = draw_ids(5, T // 100, E, k, 0.1)
