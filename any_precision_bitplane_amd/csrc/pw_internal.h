@@ -289,10 +289,14 @@ struct NormGradArgs {
 inline size_t norm_grad_parts(int T) { return T < kNormGradBlocks ? (size_t)T : (size_t)kNormGradBlocks; }
 hipError_t launch_rmsnorm_grad(const NormGradArgs& a, int dtype, float* dweight, hipStream_t s);
 
-// One launch up to here: its blocks read all ids (S = 5360: 10.3 us against 17.4 of two launches; 7584: 16.4 against 14.5).
+// One launch up to here, whose blocks all read every id (5360 slots: 10.3 us
+// against 17.4 of two launches; 7584: 16.4 against 14.5).
 constexpr int kPermuteSmallSlots = 6144;
-constexpr int kPermutePieces = 64;         // most pieces of a larger call whose slots are counted apart, unless a scan follows
-constexpr int64_t kPermutePieceSlots = 8192;   // a piece has no more; with more than 64 pieces a launch sums their counts
+// Larger calls count the slots of pieces apart: at most 64 pieces, unless those
+// would have more slots than the second number; then a launch of its own sums
+// the counts of as many pieces as it takes.
+constexpr int kPermutePieces = 64;
+constexpr int64_t kPermutePieceSlots = 8192;
 
 struct PermuteArgs {
   int T, k, E;

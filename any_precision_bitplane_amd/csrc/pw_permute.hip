@@ -224,12 +224,13 @@ __global__ __launch_bounds__(kWave) void permute_scan_kernel(PermuteArgs a) {
   if (lane == 0) a.counts[(int64_t)a.pieces * a.E + e] = carry;
 }
 
-// Last launch (of the time of a large call nearly all: T = 32768, H = 2048, k = 4
-// 136 of 140 us, 4.9 TB/s of rows read and written): a block takes block_tokens tokens of one piece.  An expert's
-// slots of this block start at its offset plus its slots in earlier pieces and
-// in earlier blocks of the piece (counted again here); inside the block a
-// slot's rank is its position among the equal ids, found by ballots of one
-// wave.  Each wave requests its first token's row before all that.
+// Last launch, nearly all of a large call's time (T = 32768, H = 2048, k = 4 136
+// of 141 us, 4.9 TB/s of rows read and written): a block takes block_tokens
+// tokens of one piece.  An expert's slots of this block start at its offset plus
+// its slots in earlier pieces and in earlier blocks of the piece (counted again
+// here); inside the block a slot's rank is its position among the equal ids,
+// found by ballots of one wave.  Each wave requests its first token's row before
+// all that.
 //
 // NARROW (rows of up to 512 bytes): 1 << shift threads take a token.
 template <bool SCANNED, bool NARROW>

@@ -8,9 +8,9 @@
 // in fp32.  A dropped slot (id outside [0, E)) takes no part, in the inner sum
 // either.
 //
-// One launch for both.  dWr: a block takes one expert, 2048 columns and a
+// One launch for both.  dWr: a block takes one expert, up to 2048 columns and a
 // stretch of the slots; its waves list the slots that the expert serves, with
-// their token and dl, in LDS, then each sums 512 columns of the listed rows in
+// their token and dl, in LDS, then sum 512 columns each of the listed rows in
 // registers (no atomics: the same inputs give the same bits).  A row is read by
 // each of its k experts, so the blocks of one stretch and its columns go to one
 // XCD, whose L2 serves all but the first.  dx: a wave takes a token; the
@@ -61,10 +61,11 @@ __device__ __forceinline__ Listed slot_dl(const RouterGradArgs& a, int64_t s) {
 template <bool WIDE>
 __device__ __forceinline__ void router_grad_w(const RouterGradArgs& a, int block) {
   using R = Row<PW_F16>;
-  __shared__ Listed list[kWaves][kSegment];
+  __shared__ __align__(32) Listed list[kListed];   // a segment a wave
   __shared__ int listed[kWaves];
   static_assert(sizeof(list) >= kThreads * sizeof(floatx8), "the waves' sums take the list's place at the end");
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
+  Listed* mine = list + wave * kSegment;
   const int cw = 1 << a.cshift, lanes = WIDE ? kWave : 1 << a.shift;
   const int groups = WIDE ? 1 : kWave >> a.shift;
   const int columns = (a.H + 512 * cw - 1) / (512 * cw);
@@ -94,12 +95,12 @@ __device__ __forceinline__ void router_grad_w(const RouterGradArgs& a, int block
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const unsigned long long mask = __ballot(id[i] == e);
-      if (id[i] == e) list[wave][n + __popcll(mask & ((1ull << lane) - 1ull))].t = (wave + kWaves * i) * kWave + lane;
+      if (id[i] == e) mine[n + __popcll(mask & ((1ull << lane) - 1ull))].t = (wave + kWaves * i) * kWave + lane;
       n += __popcll(mask);
     }
     __builtin_amdgcn_wave_barrier();
     // ... then as tokens with their dl
-    for (int i = lane; i < n; i += kWave) list[wave][i] = slot_dl(a, c0 + list[wave][i].t);
+    for (int i = lane; i < n; i += kWave) mine[i] = slot_dl(a, c0 + mine[i].t);
     if (lane == 0) listed[wave] = n;
     __syncthreads();
     const int n1 = uniform(listed[0]), n2 = n1 + uniform(listed[1]), n3 = n2 + uniform(listed[2]);
@@ -113,7 +114,8 @@ __device__ __forceinline__ void router_grad_w(const RouterGradArgs& a, int block
       for (int u = 0; u < U; ++u) {
         const int at = i0 + u * parts + part;
         const int i = at < rows ? at : rows - 1;
-        const Listed l = list[0][i < n1 ? i : i < n2 ? kSegment + i - n1 : i < n3 ? 2 * kSegment + i - n2 : 3 * kSegment + i - n3];
+        const int from = i < n1 ? 0 : i < n2 ? kSegment - n1 : i < n3 ? 2 * kSegment - n2 : 3 * kSegment - n3;
+        const Listed l = list[from + i];
         dl[u] = l.dl;
         v[u] = R::load(x + (int64_t)(WIDE ? uniform(l.t) : l.t) * a.H);
       }
@@ -213,8 +215,9 @@ __device__ __forceinline__ void router_grad_x_narrow(const RouterGradArgs& a, in
     const int32_t e = ids[j];
     const bool kept = (uint32_t)e < (uint32_t)a.E;
     const float wj = w[j], dl = wj * dw[j] - wj * mean;
-    const floatx8 row = R::wide(R::load(reinterpret_cast<const _Float16*>(a.router_w) + (int64_t)(kept ? e : 0) * a.H + 8 * lane));
-    if (kept) acc += dl * row;
+    const _Float16* row = reinterpret_cast<const _Float16*>(a.router_w) + (int64_t)(kept ? e : 0) * a.H + 8 * lane;
+    const floatx8 v = R::wide(R::load(row));
+    if (kept) acc += dl * v;
   }
   R::store_once(reinterpret_cast<_Float16*>(a.dx) + t * a.H + 8 * lane, R::narrow(acc));
 }

@@ -73,7 +73,8 @@ def near(got, ref, allowed, what):
 
 # ----- norm -----------------------------------------------------------------
 
-NORM_SIZES = [(1, 8), (37, 40), (2050, 128), (19, 136), (1500, 256), (3, 64), (5, 520), (1, 2048), (2, 4104), (7, 8192), (2, 16384), (1, 32768),
+NORM_SIZES = [(1, 8), (37, 40), (2050, 128), (19, 136), (1500, 256), (3, 64), (5, 520), (1, 2048),
+              (2, 4104), (7, 8192), (2, 16384), (1, 32768),
               (1025, 64), (1030, 520), (1027, 1000), (1026, 2080), (1025, 4096), (1025, 8200), (1025, 16392),
               (1025, 24576)]
 
@@ -98,7 +99,8 @@ def test_rmsnorm(torch, T, H, name):
 
 
 @pytest.mark.parametrize("name", DTYPES)
-@pytest.mark.parametrize("T,H,group", [(1, 64, 0), (1, 64, 128), (70, 40, 128), (70, 40, 0), (2049, 128, 128), (9, 128, 0), (1026, 256, 128),
+@pytest.mark.parametrize("T,H,group", [(1, 64, 0), (1, 64, 128), (70, 40, 128), (70, 40, 0), (2049, 128, 128),
+                                       (9, 128, 0), (1026, 256, 128),
                                        (33, 232, 0), (3, 136, 128), (5, 2048, 128), (4, 2080, 0),
                                        (2, 32768, 0), (1, 32768, 128), (1030, 520, 128), (1025, 4096, 0),
                                        (1025, 8200, 128), (1025, 16384, 0)])
@@ -120,8 +122,8 @@ def test_rmsnorm_e4m3(torch, T, H, group, name):
     near(f64(scale), rs, rs * (ROW + 2) * U, "scale")
     wide = np.repeat(f64(scale), group if group else H, axis=1)[:, :H]
     # half a step of e4m3 (2^-4 of the value, 2^-10 of the scale below its normal numbers), and the fp32 work before it
-    near(f64(y) * wide, ref, np.maximum(np.abs(ref) * 2.0 ** -4, wide * 2.0 ** -10) + (np.abs(ref) + wide) * 2 * ROW * U,
-         "code * scale")
+    code = np.maximum(np.abs(ref) * 2.0 ** -4, wide * 2.0 ** -10)
+    near(f64(y) * wide, ref, code + (np.abs(ref) + wide) * 2 * ROW * U, "code * scale")
     assert np.max(np.abs(f64(y))) == (448.0 if ref.any() else 0.0)
 
 
@@ -155,7 +157,8 @@ def test_rmsnorm_in_place_and_special_rows(torch):
         near(f64(y[t:t + 1]), ref, np.abs(ref) * (2.0 ** -11 + ROW * U) + 2.0 ** -25, f"row {t}")
 
 
-GRAD_SIZES = [(1, 8), (6007, 40), (9000, 128), (4500, 200), (2050, 256), (3, 64), (2, 32768), (5, 8200), (700, 4096), (2500, 520), (1025, 2080), (513, 8192), (514, 16384),
+GRAD_SIZES = [(1, 8), (6007, 40), (9000, 128), (4500, 200), (2050, 256), (3, 64), (2, 32768),
+              (5, 8200), (700, 4096), (2500, 520), (1025, 2080), (513, 8192), (514, 16384),
               (515, 24576), (3000, 512)]
 
 
@@ -183,7 +186,7 @@ def test_rmsnorm_backward(torch, T, H, name):
     for got, add, what in [(dx, a, "dx"), (alone, np.zeros_like(a), "dx without the stream's gradient")]:
         ref, dgr = oo.rmsnorm_backward(d, rr, gg, EPS, add)
         near(f64(got), ref, np.abs(ref) * rel + ab + 2 * ROW * U * (mag + np.abs(add)), what)
-    # a lane adds at most ceil(T / 256) rows, a block at most 32 lanes' shares, then 512 blocks: 8 a thread and six levels
+    # a lane adds at most ceil(T / 256) rows, a block 32 lanes' shares, then 512 blocks: 8 a thread and six levels
     chain = -(-T // 256) + 32 + 8 + 6 + ROW
     near(f64(dg), dgr, chain * U * np.sum(np.abs(d * rr * s), axis=0), "dweight")
 
@@ -228,8 +231,10 @@ def test_rmsnorm_backward_of_no_rows(torch):
 # name, T, H, E, k, share of dropped slots; up to 6144 slots one launch, above two, from about half a million three
 SORT_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd", 7, 96, 5, 3, 0.3),
               ("all_dropped", 9, 64, 8, 2, 1.0), ("E256_k64", 5, 64, 256, 64, 0.1), ("E256_k256", 2, 32, 256, 256, 0.0),
-              ("more_experts_than_tokens", 3, 64, 200, 2, 0.0), ("edge_4096", 1024, 96, 60, 4, 0.1), ("edge_6144", 1536, 96, 60, 4, 0.1), ("above_6144", 1537, 320, 60, 4, 0.1),
-              ("above_4096", 1025, 96, 60, 4, 0.1), ("one_expert", 5000, 64, 1, 1, 0.0), ("large", 4099, 160, 8, 2, 0.05),
+              ("more_experts_than_tokens", 3, 64, 200, 2, 0.0), ("edge_4096", 1024, 96, 60, 4, 0.1),
+              ("edge_6144", 1536, 96, 60, 4, 0.1), ("above_6144", 1537, 320, 60, 4, 0.1),
+              ("above_4096", 1025, 96, 60, 4, 0.1), ("one_expert", 5000, 64, 1, 1, 0.0),
+              ("large", 4099, 160, 8, 2, 0.05),
               ("E256_k8", 1500, 64, 256, 8, 0.2), ("E256_k256_large", 40, 32, 256, 256, 0.1),
               ("all_dropped_large", 5001, 32, 9, 1, 1.0), ("k7", 3001, 64, 33, 7, 0.5),
               ("scanned", 140003, 32, 60, 4, 0.1), ("scanned_k64", 9001, 32, 256, 64, 0.1)]
@@ -466,7 +471,8 @@ def test_more_rows_than_a_grid_has_blocks(torch):
     order = torch.argsort(torch.where(ids.reshape(-1) < 0, E, ids.reshape(-1)).to(torch.uint8), stable=True)
     n = int(off[E])
     assert n == int((ids >= 0).sum())
-    assert torch.equal(inv[order[:n]], torch.arange(n, dtype=torch.int32, device=DEV)) and bool((inv[order[n:]] == -1).all())
+    assert torch.equal(inv[order[:n]], torch.arange(n, dtype=torch.int32, device=DEV))
+    assert bool((inv[order[n:]] == -1).all())
     for s in range(0, n, 1 << 23):
         e = min(n, s + (1 << 23))
         assert torch.equal(xs[s:e], x[order[s:e]])
@@ -521,7 +527,7 @@ def test_broadcast_and_wide_inputs(torch):
     ids = draw_ids(4, T, E, k, 0.0)
     g = rand(torch, 3, (1, H), "f16")[0]
     for x in (one.expand(T, H), wide):
-        y, yc = torch.empty((T, H), dtype=torch.float16, device=DEV), torch.empty((T, H), dtype=torch.float16, device=DEV)
+        y, yc = (torch.empty((T, H), dtype=torch.float16, device=DEV) for _ in range(2))
         B.pw_rmsnorm(T, H, x, g, EPS, y, residual=x, residual_out=torch.empty_like(y))
         B.pw_rmsnorm(T, H, x.contiguous(), g, EPS, yc, residual=x.contiguous(), residual_out=torch.empty_like(y))
         assert torch.equal(y, yc)
@@ -540,8 +546,9 @@ def test_broadcast_and_wide_inputs(torch):
 # ----- the router's gradient --------------------------------------------------
 
 ROUTER_CASES = [("one", 1, 32, 1, 1, 0.0), ("decode", 4, 2048, 60, 4, 0.0), ("odd", 7, 96, 5, 3, 0.3),
-                ("E256_k64", 6, 160, 256, 64, 0.1), ("qwen", 257, 2048, 60, 4, 0.05), ("mixtral", 1100, 4096, 8, 2, 0.0),
-                ("E256_k8", 1500, 288, 256, 8, 0.2), ("all_dropped", 33, 64, 8, 2, 1.0), ("large", 5001, 544, 33, 6, 0.1)]
+                ("E256_k64", 6, 160, 256, 64, 0.1), ("qwen", 257, 2048, 60, 4, 0.05), 
+                ("mixtral", 1100, 4096, 8, 2, 0.0), ("E256_k8", 1500, 288, 256, 8, 0.2),
+                ("all_dropped", 33, 64, 8, 2, 1.0), ("large", 5001, 544, 33, 6, 0.1)]
 
 
 @pytest.mark.parametrize("name,T,H,E,k,dropped", ROUTER_CASES, ids=[c[0] for c in ROUTER_CASES])
@@ -551,7 +558,8 @@ def test_router_backward(torch, name, T, H, E, k, dropped):
     if name == "large":
         ids[::3, 1] = ids[::3, 0]                       # the same expert twice in a token
     shp = B.shape(H, 32, E, k)
-    x, wr, add = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (E, H), "f16", H ** -0.5), rand(torch, 3, (T, H), "f16", 0.1)
+    x, wr = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (E, H), "f16", H ** -0.5)
+    add = rand(torch, 3, (T, H), "f16", 0.1)
     w = torch.softmax(rand(torch, 4, (T, k), "f32"), dim=1).contiguous()
     dw = rand(torch, 5, (T, k), "f32")
     idd = torch.from_numpy(ids).to(DEV)
@@ -637,10 +645,12 @@ def test_forward_block_in_a_graph(torch):
     say("forward_block captured and replayed: the residual stream goes on, as in eager calls")
     L = synth.make_layer(synth.WORKLOADS["tiny"])
     dev, w = DeviceLayer(L, device=DEV), L.wl
-    x, res0, g = rand(torch, 1, (w.T, w.H), "f16"), rand(torch, 2, (w.T, w.H), "f16"), rand(torch, 3, (1, w.H), "f16")[0]
+    x, res0 = rand(torch, 1, (w.T, w.H), "f16"), rand(torch, 2, (w.T, w.H), "f16")
+    g = rand(torch, 3, (1, w.H), "f16")[0]
     wr = torch.from_numpy(synth.draw_router_weights(5, w.E, w.H)).to(DEV)
     res, y = res0.clone(), torch.empty_like(x)
-    call = lambda r, o: B.pw_moe_forward_block(dev.shape, w.T, x, r, g, EPS, wr, dev.blocks[0], dev.q, o, None, None, dev.ws)
+    call = lambda r, o: B.pw_moe_forward_block(dev.shape, w.T, x, r, g, EPS, wr, dev.blocks[0], dev.q, o, None, None,
+                                               dev.ws)
     call(res, y)
     torch.cuda.synchronize()
     res.copy_(res0)
@@ -737,7 +747,8 @@ def test_gradients_through_the_chain(torch):
     out = sum(p[:, j:j + 1] * torch.stack([N[t] @ M[sel[t, j]].double().cpu() for t in range(T)]) for j in range(k))
     ((out * dy.double().cpu()).sum() + (R * dout.double().cpu()).sum()).backward()
     # five fp16 roundings (2^-11) lie between a leaf and its gradient, each at most once per addend
-    for got, ref, what in [(y, out.detach(), "y"), (dr, X.grad, "dx"), (dg, G.grad, "dweight"), (dwr, W.grad, "drouter_w")]:
+    for got, ref, what in [(y, out.detach(), "y"), (dr, X.grad, "dx"), (dg, G.grad, "dweight"),
+                           (dwr, W.grad, "drouter_w")]:
         rel = float((got.double().cpu() - ref).norm() / ref.norm())
         say(f"  {what}: rel_l2 {rel:.2e}")
         assert rel <= 5 * 2.0 ** -11, what
@@ -753,8 +764,9 @@ def all_ops(torch, seed, T=1500, H=256, E=8, k=4):
     b = {"x": rand(torch, seed, (T, H), "f16"), "res": rand(torch, seed + 1, (T, H), "f16"),
          "g": rand(torch, seed + 2, (1, H), "f16")[0], "wr": rand(torch, seed + 3, (E, H), "f16", H ** -0.5),
          "ids": torch.from_numpy(draw_ids(seed, T, E, k, 0.1)).to(DEV), "w": rand(torch, seed + 4, (T, k), "f32"),
-         "r": new(T, H), "y": new(T, H), "codes": torch.zeros((T, H), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn),
-         "scale": new(T, 2, d=torch.float32), "xs": new(S, H), "xs8": torch.zeros((S, H), dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn),
+         "r": new(T, H), "y": new(T, H), "codes": new(T, H, d=torch.uint8).view(torch.float8_e4m3fn),
+         "scale": new(T, 2, d=torch.float32), "xs": new(S, H),
+         "xs8": new(S, H, d=torch.uint8).view(torch.float8_e4m3fn),
          "sc": new(S, 2, d=torch.float32), "off": new(E + 1, d=torch.int32), "inv": new(S, d=torch.int32),
          "back": new(T, H), "drows": new(S, H), "dw": new(T, k, d=torch.float32), "dx": new(T, H), "dx2": new(T, H),
          "dwr": new(E, H, d=torch.float32), "dr": new(T, H), "dg": new(H, d=torch.float32)}
@@ -764,7 +776,8 @@ def all_ops(torch, seed, T=1500, H=256, E=8, k=4):
 
     def calls(stream=None):
         B.pw_rmsnorm(T, H, b["x"], b["g"], EPS, b["y"], residual=b["res"], residual_out=b["r"], stream=stream)
-        B.pw_rmsnorm(T, H, b["x"], b["g"], EPS, b["codes"], residual=b["res"], scale=b["scale"], group=128, stream=stream)
+        B.pw_rmsnorm(T, H, b["x"], b["g"], EPS, b["codes"], residual=b["res"], scale=b["scale"], group=128,
+                     stream=stream)
         B.pw_moe_permute(shp, T, b["codes"], b["ids"], b["xs8"], b["off"], b["inv"], None, ws["p"], x_scale=b["scale"],
                          xs_scale=b["sc"], stream=stream)
         B.pw_moe_permute(shp, T, b["y"], b["ids"], b["xs"], b["off"], b["inv"], None, ws["p"], stream=stream)
@@ -776,7 +789,8 @@ def all_ops(torch, seed, T=1500, H=256, E=8, k=4):
         B.pw_rmsnorm_backward(T, H, b["dx2"], b["r"], b["g"], EPS, b["dr"], b["dg"], ws["n"], dresidual=b["dx"],
                               stream=stream)
 
-    outs = ["r", "y", "codes", "scale", "xs8", "sc", "xs", "off", "inv", "back", "drows", "dw", "dx", "dx2", "dwr", "dr", "dg"]
+    outs = ["r", "y", "codes", "scale", "xs8", "sc", "xs", "off", "inv", "back", "drows", "dw", "dx", "dx2",
+            "dwr", "dr", "dg"]
     return b, calls, outs
 
 
@@ -853,7 +867,7 @@ def test_binding_refusals(torch):
         lambda: B.pw_rmsnorm(T + 1, H, x, g, EPS, x),                             # too few rows
         lambda: B.pw_rmsnorm(T, H, x[:, :32], g, EPS, x),                         # too few columns
         lambda: B.pw_rmsnorm(T, H, x, g, EPS, x, residual=f(T, H)),
-        lambda: B.pw_rmsnorm(T, H, x, g, EPS, torch.zeros((T, H), dtype=torch.float8_e4m3fn, device=DEV), scale=f(T - 1, 1)),
+        lambda: B.pw_rmsnorm(T, H, x, g, EPS, ws[:T * H].view(torch.float8_e4m3fn).view(T, H), scale=f(T - 1, 1)),
         lambda: B.pw_rmsnorm(T, H, x, g, EPS, x.double()),
         lambda: B.pw_rmsnorm(T, H, x, g, EPS, h(1, H).expand(T, H)),              # rows that overlap
         lambda: B.pw_rmsnorm(T, H, x, g.cpu(), EPS, x),
