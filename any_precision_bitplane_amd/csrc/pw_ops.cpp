@@ -1,8 +1,6 @@
 // C-ABI host layer of the operators around the routed layer: the norm in front
 // of it, tokens sorted by expert and back, and the gradients.  Argument checks
 // and launches only.
-#include <limits.h>
-
 #include "pw_internal.h"
 
 using namespace pw;
@@ -38,9 +36,8 @@ pw_status check_norm_shape(int32_t T, int32_t H, int32_t dtype, float eps) {
     if (st_ != PW_OK) return st_;        \
   } while (0)
 
-pw_status unpermute(const pw_moe_shape* shape, int32_t T, int32_t dtype, const void* rows,
-                     int64_t rows_stride, const int32_t* inv, const float* w, void* y, int64_t y_stride,
-                     void* stream) {
+pw_status unpermute(const pw_moe_shape* shape, int32_t T, int32_t dtype, const void* rows, int64_t rows_stride,
+                    const int32_t* inv, const float* w, void* y, int64_t y_stride, void* stream) {
   PW_TRY(pw_check_shape(shape, T));
   const int64_t bytes = row_type_bytes(dtype);
   if (!bytes) return PW_ERR_INVALID_ARG;

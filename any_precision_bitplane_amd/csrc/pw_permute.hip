@@ -454,10 +454,12 @@ hipError_t run_unpermute(const UnpermuteArgs& a, hipStream_t s) {
   const int shift = lanes_shift(a.H / 8, kThreads);
   const int per_block = kThreads >> shift, pieces = (a.H / 8 + (1 << shift) - 1) >> shift;
   const dim3 grid(grid_for(((int64_t)a.T * pieces + per_block - 1) / per_block));
-  if (DT != PW_F32 && (int64_t)a.T * a.k * a.H * 2 >= kBehindL2 / 2)
-    hipLaunchKernelGGL((unpermute_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, shift, pieces);
-  else
-    hipLaunchKernelGGL((unpermute_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, shift, pieces);
+  if constexpr (DT != PW_F32)
+    if ((int64_t)a.T * a.k * a.H * 2 >= kBehindL2 / 2) {
+      hipLaunchKernelGGL((unpermute_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, shift, pieces);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((unpermute_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, shift, pieces);
   return hipGetLastError();
 }
 
@@ -469,10 +471,12 @@ hipError_t run_unpermute_grad(const UnpermuteGradArgs& a, hipStream_t s) {
   const int shift = lanes_shift(a.H / 8, kWave);
   const int per_block = kThreads >> shift;
   const dim3 grid(grid_for(((int64_t)a.T * a.k + per_block - 1) / per_block));
-  if (DT != PW_F32 && (int64_t)a.T * (2 * a.k + 1) * a.H * 2 > kBehindL2)
-    hipLaunchKernelGGL((unpermute_grad_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, shift);
-  else
-    hipLaunchKernelGGL((unpermute_grad_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, shift);
+  if constexpr (DT != PW_F32)
+    if ((int64_t)a.T * (2 * a.k + 1) * a.H * 2 > kBehindL2) {
+      hipLaunchKernelGGL((unpermute_grad_kernel<DT, true>), grid, dim3(kThreads), 0, s, a, shift);
+      return hipGetLastError();
+    }
+  hipLaunchKernelGGL((unpermute_grad_kernel<DT, false>), grid, dim3(kThreads), 0, s, a, shift);
   return hipGetLastError();
 }
 
