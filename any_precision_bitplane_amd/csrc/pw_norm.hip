@@ -154,7 +154,8 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
         if (live && c < C) R::store_once(y + 8 * c, R::narrow(v[i]));
       }
     } else {
-      // A NaN or an infinity counts as infinity, so it shows in the group's maximum.
+      // A NaN or an infinity counts as infinity, so it shows in the group's maximum.  Lanes past the row's end
+      // hold zeros times the first chunk's weight, which may be NaN: they count as zero.
       float m[NV], top = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
@@ -164,6 +165,7 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
           const float t = __builtin_fabsf(v[i][j]);
           m[i] = t < INFINITY ? fmaxf(m[i], t) : INFINITY;
         }
+        if (first + i * WPR * kWave >= C) m[i] = 0.f;
         if (a.group) m[i] = lanes_max<LPR < 16 ? LPR : 16>(m[i]);   // 16 chunks of 8: one group of 128
         top = fmaxf(top, m[i]);
       }

@@ -157,6 +157,23 @@ def test_rmsnorm_in_place_and_special_rows(torch):
         near(f64(y[t:t + 1]), ref, np.abs(ref) * (2.0 ** -11 + ROW * U) + 2.0 ** -25, f"row {t}")
 
 
+@pytest.mark.parametrize("H", [40, 136, 520, 1160, 4104, 8200, 16392])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_rmsnorm_e4m3_weight_that_is_not_finite(torch, H, value):
+    say(f"rmsnorm e4m3 H={H}: weight[3] = {value} shows in its own group only")
+    T, groups = 5, -(-H // 128)
+    x, g = rand(torch, 1, (T, H), "bf16"), rand(torch, 2, (1, H), "bf16")[0]
+    good = [torch.zeros((T, H), dtype=torch.float8_e4m3fn, device=DEV), torch.zeros((T, groups), device=DEV)]
+    bad = [torch.zeros_like(good[0]), torch.zeros_like(good[1])]
+    B.pw_rmsnorm(T, H, x, g, EPS, good[0], scale=good[1], group=128)
+    g[3] = value
+    B.pw_rmsnorm(T, H, x, g, EPS, bad[0], scale=bad[1], group=128)
+    torch.cuda.synchronize()
+    assert bool(bad[1][:, 0].isnan().all()) and bool(bad[0][:, :128].float().isnan().all())
+    assert torch.equal(bad[1][:, 1:], good[1][:, 1:])
+    assert torch.equal(bad[0][:, 128:].view(torch.uint8), good[0][:, 128:].view(torch.uint8))
+
+
 GRAD_SIZES = [(1, 8), (6007, 40), (9000, 128), (4500, 200), (2050, 256), (3, 64), (2, 32768),
               (5, 8200), (700, 4096), (2500, 520), (1025, 2080), (513, 8192), (514, 16384),
               (515, 24576), (3000, 512)]
