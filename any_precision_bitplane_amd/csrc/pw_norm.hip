@@ -185,7 +185,13 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
         if (finite) {
           floatx8 q;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) q[j] = fminf(fmaxf(v[i][j] * inv, -kE4m3Max), kE4m3Max);
+          for (int j = 0; j < 8; ++j) {
+            // y / scale to nearest: the product with the reciprocal may be a step or two off, which moves codes whose
+            // quotient lies at a midpoint of e4m3; its remainder, exact in an fma, corrects it (bf16 [16384][4096]
+            // 78.3 us with and without)
+            const float t = v[i][j] * inv;
+            q[j] = fminf(fmaxf(__builtin_fmaf(__builtin_fmaf(-t, scale, v[i][j]), inv, t), -kE4m3Max), kE4m3Max);
+          }
           int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
           codes[0] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], p, true);
           p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);

@@ -910,3 +910,29 @@ def test_binding_refusals(torch):
     with pytest.raises(B.PwError) as e:
         B.pw_rmsnorm_backward(T, H, x, x, g, EPS, h(T, H), f(H), ws[:256])
     assert e.value.status == B.PW_ERR_WORKSPACE
+
+
+# ----- the 8-bit codes ----------------------------------------------------------
+
+@pytest.mark.parametrize("name", DTYPES)
+@pytest.mark.parametrize("T,H,group", [(2000, 40, 0), (3000, 520, 128), (1000, 4096, 128), (500, 4096, 0),
+                                       (100, 8200, 128), (60, 16392, 0)])
+def test_rmsnorm_e4m3_codes_are_nearest(torch, T, H, group, name):
+    """A code is the e4m3 number nearest to the fp32 quotient y / scale, to the bit: fp32 rows store the y that is
+    divided as it is, and 16-bit rows are widened without a change."""
+    say(f"rmsnorm e4m3 codes {name} T={T} H={H} group={group}")
+    x, res, g = rand(torch, 1, (T, H), name), rand(torch, 2, (T, H), name, 4.0), rand(torch, 3, (1, H), name)[0]
+    wide = torch.empty((T, H), device=DEV)
+    B.pw_rmsnorm(T, H, x.float(), g.float(), EPS, wide, residual=res.float(), residual_out=torch.empty_like(wide))
+    y = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.empty((T, -(-H // 128) if group else 1), device=DEV)
+    B.pw_rmsnorm(T, H, x, g, EPS, y, residual=res, scale=scale, group=group)
+    torch.cuda.synchronize()
+    pieces = wide.cpu().split(group or H, dim=1)
+    want = torch.stack([p.abs().amax(dim=1) / 448.0 for p in pieces], dim=1)
+    assert torch.equal(scale.cpu(), want)
+    codes = torch.cat([(p / want[:, i:i + 1]).clamp(-448, 448).to(torch.float8_e4m3fn)
+                       for i, p in enumerate(pieces)], dim=1)
+    off = int((y.cpu().float() != codes.float()).sum())
+    say(f"  {off} of {T * H} codes differ")
+    assert off == 0
