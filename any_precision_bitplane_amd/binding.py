@@ -425,6 +425,17 @@ def _scratch(t, dev):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _table(t, name, nbytes, dev):
+    """Pointer of a contiguous tensor of at least nbytes bytes of any type; an address stays as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev:
+        raise _Refused(f"{name} must be on the GPU of the other tensors")
+    if t.numel() * t.element_size() < nbytes or not t.is_contiguous():
+        raise _Refused(f"{name} must be {nbytes} contiguous bytes")
+    return t.data_ptr()
+
+
 def _handle(stream, dev) -> int:
     """Raw handle of a stream of the tensors' GPU; None: torch's current one there."""
     if stream is None:
@@ -591,14 +602,22 @@ def pw_router_backward(shp: PwMoeShape, T: int, x, router_w, ids, w, dw, dx, dro
 def pw_moe_forward_block(shp: PwMoeShape, T: int, x, residual, norm_w, eps: float, router_w, blocks, q, y, stat_count,
                          stat_mass, workspace, opts: Optional[PwMoeOptions] = None, stream=None,
                          check: bool = True) -> int:
-    ws_bytes = workspace.numel() * workspace.element_size()
-    st = load().pw_moe_forward_block(ctypes.byref(shp), T, _ptr(x), _ptr(residual), _ptr(norm_w), eps, _ptr(router_w),
-                                     _ptr(blocks), _ptr(q), _ptr(y), _ptr(stat_count), _ptr(stat_mass),
-                                     _ptr(workspace), ws_bytes, ctypes.byref(opts) if opts is not None else None,
-                                     _stream(stream))
-    if check:
-        _check(st, "pw_moe_forward_block")
-    return st
+    """blocks and q: tensors, or raw addresses of tables that live elsewhere."""
+    lib = _load_ops()
+    try:
+        dev, H, E, f16 = _gpu(x), shp.hidden, shp.num_experts, _torch.float16
+        # the library's counts are unsigned; torch code mostly keeps them in int32
+        counts = _torch.uint32 if stat_count is not None and stat_count.dtype is _torch.uint32 else _torch.int32
+        pw, nw = _scratch(workspace, dev)
+        return _call("pw_moe_forward_block", check, dev, lib.pw_moe_forward_block, (
+            ctypes.byref(shp), T, _array(x, "x", T * H, dev, f16), _array(residual, "residual", T * H, dev, f16),
+            _array(norm_w, "norm_w", H, dev, f16), eps, _array(router_w, "router_w", E * H, dev, f16),
+            _table(blocks, "blocks", 2 * E * ctypes.sizeof(PwBlockDesc), dev), _table(q, "q", 2 * E, dev),
+            _array(y, "y", T * H, dev, f16), _array(stat_count, "stat_count", E, dev, counts),
+            _array(stat_mass, "stat_mass", E, dev, _torch.float32), pw, nw,
+            ctypes.byref(opts) if opts is not None else None, _handle(stream, dev)))
+    except _Refused as e:
+        return _refuse("pw_moe_forward_block", check, e)
 
 
 # --- planner ----------------------------------------------------------------

@@ -173,3 +173,85 @@ def test_binding_refuses_host_tensors(lib, shp):
         with pytest.raises(B.PwError, match="GPU") as e:
             call(True)
         assert e.value.status == B.PW_ERR_INVALID_ARG
+
+
+def block_args(torch, shp, T=4, where=lambda t: t):
+    """Arguments of pw_moe_forward_block by name, as zeros on the host; `where` puts each somewhere."""
+    h = lambda *n: where(torch.zeros(n, dtype=torch.float16))
+    H, E = shp.hidden, shp.num_experts
+    return {"x": h(T, H), "residual": h(T, H), "norm_w": h(H), "eps": 1e-5, "router_w": h(E, H),
+            "blocks": where(torch.zeros((E, 2, 2), dtype=torch.int64)),
+            "q": where(torch.zeros((E, 2), dtype=torch.uint8)), "y": h(T, H), "stat_count": where(torch.zeros(E, dtype=torch.int32)), "stat_mass": where(torch.zeros(E)),
+            "workspace": where(torch.zeros(B.pw_workspace_bytes(shp, T), dtype=torch.uint8))}
+
+
+class Elsewhere:
+    """A host tensor that says it is on GPU `index`: enough for the binding's checks, never launched on."""
+
+    def __init__(self, t, index):
+        self.t, self.index = t, index
+
+    def get_device(self):
+        return self.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_forward_block_binding_refuses_host_tensors(lib, shp):
+    import torch
+    args = block_args(torch, shp)
+    assert B.pw_moe_forward_block(shp, 4, **args, check=False) == B.PW_ERR_INVALID_ARG
+    with pytest.raises(B.PwError, match="GPU"):
+        B.pw_moe_forward_block(shp, 4, **args)
+
+
+def test_forward_block_binding_checks_and_device(lib, shp, monkeypatch):
+    """Every tensor's device, type and size are checked before the call, which goes to the tensors' GPU and a stream
+    of it, whichever GPU is current."""
+    import contextlib
+
+    import torch
+    B._load_ops()
+    calls, entered = [], []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(d)
+        yield
+
+    class Lib:
+        @staticmethod
+        def pw_moe_forward_block(*a):
+            calls.append(a)
+            return B.PW_OK
+
+    monkeypatch.setattr(B, "_lib", Lib)
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_current_stream", lambda dev: 1000 + dev)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    with monkeypatch.context() as m:
+        m.setattr(B, "_lib", lib)
+        good = block_args(torch, shp, where=lambda t: Elsewhere(t, 1))
+    call = lambda **kw: B.pw_moe_forward_block(shp, 4, **{**good, **kw}, check=False)
+    assert call() == B.PW_OK and entered == [1] and calls[-1][-1] == 1001
+    assert call(blocks=1 << 20, q=1 << 21, stat_count=None, stat_mass=None) == B.PW_OK     # raw tables, no statistics
+    assert calls[-1][7] == 1 << 20 and calls[-1][8] == 1 << 21
+    assert call(stat_count=Elsewhere(good["stat_count"].t.view(torch.uint32), 1)) == B.PW_OK
+    n = len(calls)
+    for name, arg in good.items():
+        if name == "eps":
+            continue
+        t = arg.t
+        assert call(**{name: Elsewhere(t, 0)}) == B.PW_ERR_INVALID_ARG, name                # another GPU
+        assert call(**{name: t}) == B.PW_ERR_INVALID_ARG, name                              # the host
+        wide = torch.zeros((*t.shape, 2), dtype=t.dtype)[..., 0]
+        assert call(**{name: Elsewhere(wide, 1)}) == B.PW_ERR_INVALID_ARG, name             # elements apart
+        if name == "workspace":
+            continue                                                                        # the library's own check
+        assert call(**{name: Elsewhere(t.reshape(-1)[:-1], 1)}) == B.PW_ERR_INVALID_ARG, name
+        if name not in ("blocks", "q"):
+            assert call(**{name: Elsewhere(t.double(), 1)}) == B.PW_ERR_INVALID_ARG, name
+    for name in ("x", "residual", "norm_w", "router_w", "y"):
+        assert call(**{name: Elsewhere(good[name].t.bfloat16(), 1)}) == B.PW_ERR_INVALID_ARG, name
+    assert call(x=None) == B.PW_ERR_INVALID_ARG and len(calls) == n
