@@ -420,9 +420,9 @@ inline RouterGradPlan router_grad_plan(int H, int E, int k, int64_t T) {
   p.split_slots = (S + fill - 1) / fill;
   p.split_slots = p.split_slots < least ? least : (p.split_slots + 255) / 256 * 256;
   p.splits = (int)((S + p.split_slots - 1) / p.split_slots);
-  // no T' <= T has more stretches than this, so a workspace for T serves them all
-  const int64_t most = (S + least - 1) / least < 4096 ? (S + least - 1) / least : 4096;
-  p.bytes = align_up(sizeof(float) * (size_t)most * E * H + 1, kAlign);
+  // no T' <= T has more stretches than this (its tiles are no wider), so a workspace for T serves them all
+  const int64_t by_slots = (S + least - 1) / least;
+  p.bytes = align_up(sizeof(float) * (size_t)(by_slots < fill ? by_slots : fill) * E * H + 1, kAlign);
   return p;
 }
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);

@@ -3,6 +3,7 @@ launch: C entry points by made-up pointers, the binding by tensors that are not
 on a GPU.  No GPU needed."""
 import ctypes
 import os
+import subprocess
 
 import pytest
 
@@ -255,3 +256,20 @@ def test_forward_block_binding_checks_and_device(lib, shp, monkeypatch):
     for name in ("x", "residual", "norm_w", "router_w", "y"):
         assert call(**{name: Elsewhere(good[name].t.bfloat16(), 1)}) == B.PW_ERR_INVALID_ARG, name
     assert call(x=None) == B.PW_ERR_INVALID_ARG and len(calls) == n
+
+
+def test_router_gradient_workspace_is_what_its_plan_uses(tmp_path):
+    """For up to 2^20 tokens: enough for every smaller call, and at most about twice what the largest uses."""
+    from any_precision_bitplane_amd import build
+    exe = str(tmp_path / "plan_test")
+    subprocess.run([build.hipcc(), "-x", "hip", "--offload-host-only", "-O1", "-std=c++17", "-I", build.CSRC,
+                    os.path.join(build.ROOT, "tests", "cpp", "router_grad_plan_test.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+def test_router_gradient_workspace_of_large_calls(lib):
+    """What 4096 blocks' shares take, whatever the number of tokens."""
+    size = lambda H, E, k, T: B.pw_router_backward_workspace_bytes(B.shape(H, 32, E, k), T) >> 20
+    assert size(8192, 256, 8, 1 << 20) <= 34 and size(7168, 256, 8, 1 << 18) <= 34
+    assert size(4096, 8, 2, 1 << 20) <= 34 and size(2048, 60, 4, 32768) <= 34
