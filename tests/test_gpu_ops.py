@@ -936,3 +936,165 @@ def test_rmsnorm_e4m3_codes_are_nearest(torch, T, H, group, name):
     off = int((y.cpu().float() != codes.float()).sum())
     say(f"  {off} of {T * H} codes differ")
     assert off == 0
+
+
+# ----- the router's gradient by the form of its tiles ----------------------------
+
+def router_chain(T, H, E, k):
+    """Most fp32 additions in turn behind one element of drouter_w: a wave's part of a list of up to 2048 slots (its
+    block's four waves share the rows of 512 columns up to 8192 slots; above, 2 or 4 of them take other columns where H
+    is over 512 or 1024), the lists of a stretch, the parts, the stretches.  Stretches: at least 1024 slots and 4 E
+    tokens, as many as make 4096 blocks; a list's length is bounded by the slots too."""
+    waves = 1 if T * k <= 8192 or H <= 512 else 2 if H <= 1024 else 4
+    tiles = E * -(-H // (512 * waves))
+    least = max(1024, 4 * E * k)
+    stretch = max(least, -(-T * k // (-(-4096 // tiles))) + 255)
+    parts = 4 // waves * (1 if H >= 512 else 64)
+    return min(T * k, 512 * waves) + -(-stretch // 2048) + parts + -(-T * k // least) + 2 * k + 8
+
+
+def draw_skewed(seed, T, E, k, hot, share):
+    """Distinct experts a token, with expert `hot` in the first slot of `share` of the tokens."""
+    ids = draw_ids(seed, T, E, k, 0.0)
+    rng = np.random.default_rng(seed)
+    at = (rng.random(T) < share) & ~(ids == hot).any(axis=1)
+    ids[at, 0] = hot
+    return ids
+
+
+# below and above 8192 slots; H over 1024 with whole tiles of 2048 columns, with a last tile of 32, and with waves past
+# H; full lists (every slot the same expert, twice a token); nearly all tokens at one expert; several stretches
+ROUTER_TILES = [("below", 4096, 1056, 8, 2), ("above", 4097, 4096, 8, 2), ("waves_past_H", 2100, 1056, 60, 4),
+                ("last_tile_32", 2100, 2080, 60, 4), ("full_lists", 5000, 2080, 2, 2), ("skewed", 4099, 2048, 60, 4),
+                ("E256", 3000, 1056, 256, 8), ("two_columns", 4200, 1024, 9, 2), ("E1", 8200, 1056, 1, 1)]
+
+
+@pytest.mark.parametrize("name,T,H,E,k", ROUTER_TILES, ids=[c[0] for c in ROUTER_TILES])
+def test_router_backward_tiles(torch, name, T, H, E, k):
+    chain = router_chain(T, H, E, k)
+    say(f"router_backward tiles {name} T={T} H={H} E={E} k={k}, chain {chain}")
+    ids = draw_skewed(13, T, E, k, 7, 0.95) if name == "skewed" else draw_ids(13, T, E, k, 0.05)
+    if name == "full_lists":
+        ids[:] = 0
+    shp = B.shape(H, 32, E, k)
+    x, wr = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (E, H), "f16", H ** -0.5)
+    add = rand(torch, 3, (T, H), "f16", 0.1)
+    # one expert for all of a token's slots: weights that do not sum to one, or the gradients would cancel
+    part = 0.5 if E == 1 or name == "full_lists" else 1.0
+    w = (torch.softmax(rand(torch, 4, (T, k), "f32"), dim=1) * part).contiguous()
+    dw = rand(torch, 5, (T, k), "f32")
+    idd = torch.from_numpy(ids).to(DEV)
+    ws = torch.full((B.pw_router_backward_workspace_bytes(shp, T),), 255, dtype=torch.uint8, device=DEV)
+    dx, dwr, again = torch.full_like(x, 7.0), torch.full((E, H), 7.0, device=DEV), torch.empty((E, H), device=DEV)
+    B.pw_router_backward(shp, T, x, wr, idd, w, dw, dx, dwr, ws, dx_add=add)
+    B.pw_router_backward(shp, T, x, wr, idd, w, dw, torch.empty_like(x), again, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(dwr, again)
+    X, Wr, A, W, D = f64(x), f64(wr), f64(add), f64(w), f64(dw)
+    kept = (ids >= 0) & (ids < E)
+    dl = np.where(kept, W * (D - np.sum(W * D * kept, axis=1, keepdims=True)), 0.0)
+    dm = np.where(kept, W * (np.abs(D) + np.sum(np.abs(W * D) * kept, axis=1, keepdims=True)), 0.0)
+    dense, mag = np.zeros((T, E + 1)), np.zeros((T, E + 1))
+    for j in range(k):
+        np.add.at(dense, (np.arange(T), np.where(kept[:, j], ids[:, j], E)), dl[:, j])
+        np.add.at(mag, (np.arange(T), np.where(kept[:, j], ids[:, j], E)), dm[:, j])
+    dense, mag = dense[:, :E], mag[:, :E]
+    ref = dense @ Wr + A
+    near(f64(dx), ref, np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + (2 * k + 8) * U * (mag @ np.abs(Wr) + np.abs(A)), "dx")
+    near(f64(dwr), dense.T @ X, chain * U * (mag.T @ np.abs(X)), "drouter_w")
+
+    # whole numbers: dl = w (dw - sum w dw) with w = part / k and dw a multiple of (k / part)^2 is one too, at most
+    # 4 k / part, and every partial sum stays below 2^24, so fp32 adds without a rounding and no row may be missing
+    whole = lambda seed, shape, most: torch.randint(-most, most + 1, shape,
+                                                    generator=torch.Generator().manual_seed(seed))
+    x, w = whole(1, (T, H), 3).half().to(DEV), torch.full((T, k), part / k, device=DEV)
+    dw = (whole(2, (T, k), 2) * int(k / part) ** 2).float().to(DEV)
+    B.pw_router_backward(shp, T, x, wr, idd, w, dw, dx, dwr, ws)
+    torch.cuda.synchronize()
+    D = f64(dw) * kept
+    dl = np.where(kept, (D - np.sum(D, axis=1, keepdims=True) * part / k) * part / k, 0.0)
+    dense = np.zeros((T, E + 1))
+    for j in range(k):
+        np.add.at(dense, (np.arange(T), np.where(kept[:, j], ids[:, j], E)), dl[:, j])
+    assert np.max(np.sum(np.abs(dl), axis=1)) * T * 3 < 2 ** 24 and dl.any()
+    assert np.array_equal(f64(dwr), dense[:, :E].T @ f64(x))
+
+
+@pytest.mark.parametrize("T,H", [(4_200_003, 512), (67_200_003, 32)])
+def test_router_backward_of_more_tokens_than_a_grid_takes(torch, T, H):
+    """The launch's dx blocks end at 2^20, each four tokens (H = 512) or 64 (H = 32); they then walk the rest.  Whole
+    numbers: w = 1/2 and dw a multiple of 4 give a whole dl of at most 2, and the partial sums, walks of at most 2^27
+    steps of up to 6 in both directions, stay far below 2^24 (the last line checks), so every sum is exact."""
+    E, k = 4, 2
+    say(f"router_backward T={T} H={H}: {T * H * 2 / 2 ** 30:.1f} GiB a matrix")
+    shp = B.shape(H, 32, E, k)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty((T, H), dtype=torch.float16, device=DEV)
+    step = (1 << 27) // H
+    for s in range(0, T, step):
+        x[s:s + step] = torch.randint(-3, 4, x[s:s + step].shape, generator=g, device=DEV, dtype=torch.int8).half()
+    wr = torch.randint(-8, 9, (E, H), generator=g, device=DEV).half()
+    first = torch.randint(0, E, (T, 1), generator=g, device=DEV, dtype=torch.int32)
+    ids = torch.cat([first, (first + 1) % E], dim=1).contiguous()
+    w = torch.full((T, k), 0.5, device=DEV)
+    dw = 4.0 * torch.randint(-1, 2, (T, k), generator=g, device=DEV).float()
+    dx, dwr = torch.full_like(x, 7.0), torch.empty((E, H), device=DEV)
+    ws = torch.empty(B.pw_router_backward_workspace_bytes(shp, T), dtype=torch.uint8, device=DEV)
+    B.pw_router_backward(shp, T, x, wr, ids, w, dw, dx, dwr, ws)
+    torch.cuda.synchronize()
+    ref, reach = torch.zeros((E, H), dtype=torch.float64, device=DEV), 0.0
+    for s in range(0, T, step):
+        D = dw[s:s + step].double()
+        dl = 0.5 * (D - 0.5 * D.sum(1, keepdim=True))
+        dense = torch.zeros((D.shape[0], E), dtype=torch.float64, device=DEV)
+        dense.scatter_add_(1, ids[s:s + step].long(), dl)
+        assert torch.equal(dx[s:s + step].double(), dense @ wr.double()), s
+        ref += dense.t() @ x[s:s + step].double()
+        reach = max(reach, float(ref.abs().max()))
+    assert torch.equal(dwr.double(), ref)
+    say(f"  largest partial sum seen {reach:.0f}")
+    assert reach < 2 ** 22
+
+
+# ----- loops that only the largest calls turn twice --------------------------------
+
+@pytest.mark.parametrize("T,H,out", [(2_097_160, 520, "same"), (2_097_160, 520, "e4m3"), (1_048_581, 1032, "same"),
+                                     (1_048_581, 1032, "e4m3")])
+def test_rmsnorm_walks_long_rows(torch, T, H, out):
+    """More than 2^20 blocks of rows that take several waves, two (H = 520, two rows a block) or four."""
+    say(f"rmsnorm {out} T={T} H={H}")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.empty((T, H), dtype=torch.float16, device=DEV).normal_(generator=g)
+    x *= torch.rand((T, 1), generator=g, device=DEV).half() + 0.25       # rows of different size
+    w = torch.randn(H, generator=g, device=DEV).half()
+    y = torch.empty((T, H), dtype=torch.float8_e4m3fn if out == "e4m3" else torch.float16, device=DEV)
+    scale = torch.empty((T, 1), device=DEV) if out == "e4m3" else None
+    B.pw_rmsnorm(T, H, x, w, EPS, y, scale=scale)
+    torch.cuda.synchronize()
+    for s in range(0, T, 1 << 17):
+        X = x[s:s + (1 << 17)].double()
+        ref = X / (X.square().mean(1, keepdim=True) + EPS).sqrt() * w.double()
+        got = y[s:s + (1 << 17)].float().double()
+        if out == "same":
+            ok = (got - ref).abs() <= ref.abs() * (2.0 ** -11 + ROW * U) + 2.0 ** -25
+        else:
+            sc = scale[s:s + (1 << 17)].double()
+            want = ref.abs().amax(1, keepdim=True) / 448
+            assert bool(((sc - want).abs() <= want * (ROW + 2) * U).all()), s
+            ok = (got * sc - ref).abs() <= torch.maximum(ref.abs() * 2.0 ** -4, sc * 2.0 ** -10) + \
+                (ref.abs() + sc) * 2 * ROW * U
+        assert bool(ok.all()), s
+
+
+@pytest.mark.parametrize("T,H,k,dt", [(5, 8192, 3, "f32"), (300, 4128, 4, "f16"), (1100, 2080, 5, "f16")])
+def test_permute_of_few_long_rows(torch, T, H, k, dt):
+    """One launch, rows longer than its threads take at a time: 16 KB (up to 256 tokens), 8 KB (1024), 4 KB."""
+    say(f"permute {dt} T={T} H={H} k={k}: {H * (4 if dt == 'f32' else 2)} bytes a row")
+    E = 9
+    ids = draw_ids(6, T, E, k, 0.1)
+    offsets, inv, perm = plan(ids, E)
+    x = rand(torch, 5, (T, H), dt)
+    xs, off, iv, _, _, _, raw = run_permute(torch, x, ids, E)
+    n = len(perm)
+    assert np.array_equal(off.cpu().numpy(), offsets) and np.array_equal(iv.cpu().numpy(), inv)
+    assert torch.equal(xs[:n], x[torch.from_numpy(perm // k).to(DEV)]) and bool((raw[n:] == 3).all())
