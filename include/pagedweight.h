@@ -372,6 +372,12 @@ pw_status pw_moe_forward_layers(const pw_moe_shape* shape /* host */, int32_t L,
  *                 NaN or an infinity gets the scale NaN and NaN codes.
  *                 Otherwise scale is NULL and group 0.  y may be x itself if
  *                 they have the same type and stride.
+ * Range (here and in the gradient): the squares are summed in fp32, so finite
+ * values follow the formula up to |r| = 2^56 (7.2e16) at any H, and where
+ * mean_h r_h^2 + eps is at least 2^-100 (7.9e-31; every r then, where eps is).
+ * Above, a row whose sum of squares is past fp32 gives y = 0; below, the
+ * squares lose digits.  fp16 rows are always inside, with eps 0 if one value is
+ * not zero.
  * One launch.  T == 0 returns PW_OK and enqueues nothing. */
 pw_status pw_rmsnorm(int32_t T, int32_t H, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                      int64_t residual_stride, void* residual_out, int64_t residual_out_stride, const void* weight,

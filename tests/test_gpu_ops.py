@@ -1098,3 +1098,65 @@ def test_permute_of_few_long_rows(torch, T, H, k, dt):
     n = len(perm)
     assert np.array_equal(off.cpu().numpy(), offsets) and np.array_equal(iv.cpu().numpy(), inv)
     assert torch.equal(xs[:n], x[torch.from_numpy(perm // k).to(DEV)]) and bool((raw[n:] == 3).all())
+
+
+# ----- the norm's range -----------------------------------------------------------
+
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -99, 1e-5, 1e30])
+@pytest.mark.parametrize("name", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [40, 128, 520, 4096, 16392, 32768])
+def test_rmsnorm_range(torch, H, name, eps):
+    """Rows at both ends of the stated range: every value +-2^56, and a mean square of 2^-100 (any, down to subnormal
+    values, where eps is at least that); a lone 2^56 among zeros and among values 2^-100 of it."""
+    say(f"rmsnorm and its gradient {name} H={H} eps={eps}: the ends of the range")
+    g64 = torch.Generator().manual_seed(1)
+    signs = (torch.randint(0, 2, (8, H), generator=g64) * 2 - 1).double()
+    part = 0.25 + 0.75 * torch.rand((8, H), generator=g64, dtype=torch.float64)
+    power = torch.tensor([56, 56, 56, 30, 0, -49, -50, -50 if eps == 0 else -126], dtype=torch.float64)
+    a = signs * part * torch.exp2(power)[:, None]
+    a[0] = signs[0] * 2.0 ** 56
+    a[1, 1:], a[1, 0] = 0.0, 2.0 ** 56
+    a[2, 1:] *= 2.0 ** -100
+    a[6] = signs[6] * 2.0 ** -50                                  # a mean square of 2^-100 exactly
+    if eps == 0:
+        a[7] = signs[7] * 2.0 ** -49
+    x = a.to(dtype_of(torch, name)).to(DEV)
+    g = rand(torch, 3, (1, H), name)[0]
+    rel, ab = half_step(torch, name)
+    y, codes = torch.empty_like(x), torch.empty((8, H), dtype=torch.float8_e4m3fn, device=DEV)
+    scale = torch.empty((8, 1), device=DEV)
+    B.pw_rmsnorm(8, H, x, g, eps, y)
+    B.pw_rmsnorm(8, H, x, g, eps, codes, scale=scale)
+    dy = rand(torch, 5, (8, H), name)
+    dx, dg = torch.empty_like(x), torch.empty(H, device=DEV)
+    ws = torch.empty(B.pw_rmsnorm_backward_workspace_bytes(8, H), dtype=torch.uint8, device=DEV)
+    B.pw_rmsnorm_backward(8, H, dy, x, g, eps, dx, dg, ws)
+    torch.cuda.synchronize()
+    X, G, D = f64(x), f64(g), f64(dy)
+    ref = oo.rmsnorm(X, G, eps)[1]
+    # r / rms below fp32's normal numbers has half a subnormal step of its own, which the weight multiplies
+    near(f64(y), ref, np.abs(ref) * (rel + ROW * U) + ab + 2.0 ** -149 * (1 + np.abs(G)), "y")
+    rs = oo.e4m3_scales(ref, 0)
+    near(f64(scale), rs, rs * (ROW + 2) * U, "scale")
+    wide = np.repeat(f64(scale), H, axis=1)
+    code = np.maximum(np.abs(ref) * 2.0 ** -4, wide * 2.0 ** -10)
+    near(f64(codes) * wide, ref, code + (np.abs(ref) + wide) * 2 * ROW * U, "code * scale")
+    s = 1 / np.sqrt(np.mean(X * X, axis=1, keepdims=True) + eps)
+    mag = np.abs(s * G * D) + np.abs(X * s) * s * s * np.sum(np.abs(G * D * X), axis=1, keepdims=True) / H
+    ref, dgr = oo.rmsnorm_backward(D, X, G, eps)
+    near(f64(dx), ref, np.abs(ref) * rel + ab + 2 * ROW * U * mag + 2.0 ** -148, "dx")
+    near(f64(dg), dgr, (1 + 32 + 8 + 6 + ROW) * U * np.sum(np.abs(D * X * s), axis=0) + 2.0 ** -145, "dweight")
+
+
+def test_rmsnorm_past_its_range(torch):
+    """Finite values whose squares' sum is past fp32 give zeros, as stated, and no other row is touched."""
+    say("rmsnorm: rows past the range give zeros")
+    for H in (40, 520, 4096):
+        x = rand(torch, 1, (3, H), "bf16")
+        one = x[0:1].clone()
+        x[1, 0] = 2.0 ** 70
+        y, alone, g = torch.empty_like(x), torch.empty_like(one), rand(torch, 3, (1, H), "bf16")[0]
+        B.pw_rmsnorm(3, H, x, g, EPS, y)
+        B.pw_rmsnorm(1, H, one, g, EPS, alone)
+        torch.cuda.synchronize()
+        assert bool((y[1] == 0).all()) and torch.equal(y[0:1], alone) and bool((y[2] != 0).any())
