@@ -343,7 +343,8 @@ pw_status pw_moe_forward_layers(const pw_moe_shape* shape /* host */, int32_t L,
  * same, what a call writes must overlap nothing else that it reads or writes.
  *
  * Sums, means and gradients of weights are fp32; an output is rounded once, to
- * nearest even.  Every call is deterministic, allocates nothing, can be
+ * nearest even.  Every call is deterministic (but for the order of stat_mass's
+ * sums in pw_moe_forward_block, see pw_router_topk), allocates nothing, can be
  * captured into a graph, and leaves what it does not write as it was.  Inputs
  * that hold NaN or infinities give what the formula gives.  A workspace is
  * 256-byte aligned and needs no initialisation; calls that may overlap in time

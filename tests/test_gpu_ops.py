@@ -1160,3 +1160,29 @@ def test_rmsnorm_past_its_range(torch):
         B.pw_rmsnorm(1, H, one, g, EPS, alone)
         torch.cuda.synchronize()
         assert bool((y[1] == 0).all()) and torch.equal(y[0:1], alone) and bool((y[2] != 0).any())
+
+
+# ----- the fused call's routing statistics ------------------------------------------
+
+@pytest.mark.parametrize("wl,T", [("tiny", 16), ("tiny", 256), ("tiny", 257), ("qwen_decode", 4)])
+def test_forward_block_statistics(torch, wl, T):
+    say(f"forward_block {wl} T={T}: counts and masses of two calls in a row, against the router's own ids and weights")
+    L = synth.make_layer(synth.WORKLOADS[wl].with_T(T))
+    dev, w = DeviceLayer(L, device=DEV), L.wl
+    x, res = rand(torch, 1, (T, w.H), "f16"), rand(torch, 2, (T, w.H), "f16", 2.0)
+    g = rand(torch, 3, (1, w.H), "f16")[0]
+    wr = torch.from_numpy(synth.draw_router_weights(5, w.E, w.H)).to(DEV)
+    count, mass = torch.zeros(w.E, dtype=torch.int32, device=DEV), torch.zeros(w.E, device=DEV)
+    counted, weighed = np.zeros(w.E, np.int64), np.zeros(w.E)
+    y, xn, ref = torch.empty_like(x), torch.empty_like(x), res.clone()
+    ids, wt = torch.empty((T, w.k), dtype=torch.int32, device=DEV), torch.empty((T, w.k), device=DEV)
+    for _ in range(2):
+        B.pw_rmsnorm(T, w.H, x, g, EPS, xn, residual=ref, residual_out=ref)
+        B.pw_router_topk(dev.shape, T, xn, wr, ids, wt, None, None, dev.ws)
+        torch.cuda.synchronize()
+        np.add.at(counted, ids.cpu().numpy().reshape(-1), 1)
+        np.add.at(weighed, ids.cpu().numpy().reshape(-1), f64(wt).reshape(-1))
+        B.pw_moe_forward_block(dev.shape, T, x, res, g, EPS, wr, dev.blocks[0], dev.q, y, count, mass, dev.ws)
+        torch.cuda.synchronize()
+    assert torch.equal(res, ref) and np.array_equal(count.cpu().numpy(), counted)
+    near(f64(mass), weighed, counted * U * weighed, "mass")       # an fp32 sum of that many weights, in any order
