@@ -465,14 +465,20 @@ size_t pw_router_backward_workspace_bytes(const pw_moe_shape* shape /* host */, 
  *     dl[t][j]      = w[t][j] (dw[t][j] - sum_i w[t][i] dw[t][i])
  *     dx[t]         = dx_add[t] + sum_j dl[t][j] router_w[ids[t][j]]
  *     drouter_w[e]  = sum over the slots of expert e of dl[t][j] x[t]
- *   x, router_w, ids, w  as pw_router_topk took and wrote them (k <= 64); a
- *              slot whose id is outside [0, E) takes no part
+ *   x, router_w, ids, w  as pw_router_topk took and wrote them (k <= 64).  A
+ *              slot whose id is outside [0, E) takes no part, in the inner sum
+ *              either: the gradient for weights that are a softmax over the
+ *              kept slots, or of a token without any.  Where slots were masked
+ *              after the router (an expert's capacity, another rank's experts)
+ *              and the others kept their weights, pass the router's own ids
+ *              here, with dw 0 (which pw_moe_unpermute_backward writes for a
+ *              dropped slot) or the other rank's dw
  *   dw         fp32 [T][k]: gradient of w (as pw_moe_unpermute_backward writes)
  *   dx_add     fp16 [T][H] or NULL: gradient that reaches x by other ways (as
  *              pw_moe_permute_backward writes)
  *   dx         fp16 [T][H], overwritten; may be dx_add itself
  *   drouter_w  fp32 [E][H], 16-byte aligned, overwritten (zero for T == 0)
- * Two launches (one for up to 1024 slots). */
+ * Two launches (one for up to max(1024, 4 E k) slots). */
 pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, const uint16_t* x,
                              const uint16_t* router_w, const int32_t* ids, const float* w, const float* dw,
                              const uint16_t* dx_add, uint16_t* dx, float* drouter_w, void* workspace,

@@ -1186,3 +1186,39 @@ def test_forward_block_statistics(torch, wl, T):
         torch.cuda.synchronize()
     assert torch.equal(res, ref) and np.array_equal(count.cpu().numpy(), counted)
     near(f64(mass), weighed, counted * U * weighed, "mass")       # an fp32 sum of that many weights, in any order
+
+
+def test_router_gradient_of_slots_masked_after_the_router(torch):
+    """An expert's capacity: slots lose their expert after the router, the others keep their weights.  The sort and the
+    way back take the masked ids, the router's gradient the router's own, with the dw that the way back writes."""
+    T, H, E, k = 50, 96, 6, 3
+    say(f"router_backward after masking, T={T} H={H} E={E} k={k}")
+    shp = B.shape(H, 32, E, k)
+    x, wr = rand(torch, 1, (T, H), "f16"), rand(torch, 2, (E, H), "f16", H ** -0.5)
+    dy, rows = rand(torch, 3, (T, H), "f32"), rand(torch, 4, (T * k, H), "f32")
+    ids, w = torch.empty((T, k), dtype=torch.int32, device=DEV), torch.empty((T, k), device=DEV)
+    ws = torch.empty(max(B.pw_workspace_bytes(shp, T), B.pw_router_backward_workspace_bytes(shp, T)),
+                     dtype=torch.uint8, device=DEV)
+    B.pw_router_topk(shp, T, x, wr, ids, w, workspace=ws)
+    kept = np.random.default_rng(1).random((T, k)) < 0.7
+    masked = np.where(kept, ids.cpu().numpy(), -1).astype(np.int32)
+    _, inv, perm = plan(masked, E)
+    iv = torch.from_numpy(inv.astype(np.int32)).to(DEV)
+    drows, dw = torch.zeros_like(rows), torch.empty((T, k), device=DEV)
+    B.pw_moe_unpermute_backward(shp, T, dy, rows, iv, w, drows, dw)
+    dx, dwr = torch.empty_like(x), torch.empty((E, H), device=DEV)
+    B.pw_router_backward(shp, T, x, wr, ids, w, dw, dx, dwr, ws)
+    torch.cuda.synchronize()
+    leaf = lambda t: t.detach().double().cpu().requires_grad_()
+    X, W = leaf(x), leaf(wr)
+    p = torch.softmax(torch.gather(X @ W.t(), 1, ids.long().cpu()), dim=1)
+    mine = torch.from_numpy(f64(rows)[np.where(inv >= 0, inv, 0)] * (inv >= 0)[:, None]).reshape(T, k, H)
+    ((p[:, :, None] * mine).sum(1) * dy.double().cpu()).sum().backward()
+    # w carries the router's fp32 logits (H + 8 roundings of sums of |x wr|, times the softmax's slope of at most one)
+    D = np.abs(f64(dy))[:, None, :] * np.abs(mine.numpy())
+    big = np.max(np.sum(D, axis=2))
+    logits = np.max(np.abs(f64(x)) @ np.abs(f64(wr)).T)
+    slack = 4 * k * big * ((H + 8) * logits + 16) * U
+    ref = X.grad.numpy()
+    near(f64(dx), ref, np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + slack * np.max(np.abs(f64(wr))), "dx")
+    near(f64(dwr), W.grad.numpy(), slack * np.sum(np.abs(f64(x)), axis=0), "drouter_w")

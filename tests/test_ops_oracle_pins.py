@@ -82,3 +82,37 @@ def test_router_gradient_against_differences():
     again = oo.router_backward(x, wr, ids2, w2, dw2, add)
     np.testing.assert_array_equal(again[0], dx)
     np.testing.assert_array_equal(again[1], dwr)
+
+
+def test_router_gradient_of_slots_masked_after_the_router():
+    """Slots that lose their expert after the softmax, the others keeping their weights: the gradient is that of the
+    router's own ids with dw 0 in the masked slots, and not that of the masked ids, which forgets the masked slots'
+    logits in the softmax (it is right where the kept weights are a softmax of their own)."""
+    rng = np.random.default_rng(5)
+    T, E, k, H = 6, 7, 3, 5
+    x, wr, dw = rng.normal(size=(T, H)), rng.normal(size=(E, H)), rng.normal(size=(T, k))
+    ids = np.argsort(-(x @ wr.T), axis=1)[:, :k]
+    kept = rng.random((T, k)) < 0.6
+    kept[0], kept[1] = False, True
+
+    def weights(x, wr, among):
+        l = np.where(among, np.take_along_axis(x @ wr.T, ids, axis=1), -np.inf)
+        z = np.exp(l - np.take_along_axis(x @ wr.T, ids, axis=1).max(axis=1, keepdims=True))
+        return z / np.maximum(z.sum(axis=1, keepdims=True), 1e-300)
+
+    every = np.ones((T, k), bool)
+    loss = lambda a, b: np.sum(np.where(kept, weights(a, b, every) * dw, 0.0))
+    want = differences(lambda a: loss(a, wr), x), differences(lambda b: loss(x, b), wr)
+    got = oo.router_backward(x, wr, ids, weights(x, wr, every), np.where(kept, dw, 0.0))
+    for a, b in zip(got, want):
+        np.testing.assert_allclose(a, b, atol=1e-8)
+    masked = np.where(kept, ids, -1)
+    short = oo.router_backward(x, wr, masked, weights(x, wr, every), dw)
+    assert np.max(np.abs(short[0] - want[0])) > 1e-2
+
+    # a softmax over the kept slots alone: the masked ids are the right ones
+    loss = lambda a, b: np.sum(np.where(kept, weights(a, b, kept) * dw, 0.0))
+    want = differences(lambda a: loss(a, wr), x), differences(lambda b: loss(x, b), wr)
+    got = oo.router_backward(x, wr, masked, weights(x, wr, kept), dw)
+    for a, b in zip(got, want):
+        np.testing.assert_allclose(a, b, atol=1e-8)
