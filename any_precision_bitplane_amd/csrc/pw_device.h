@@ -406,6 +406,15 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(row_lane(v, 0), row_lane(v, 16)), fmaxf(row_lane(v, 32), row_lane(v, 48)));
 }
 
+// What some lanes of a wave wrote to LDS before, the others read after: the wave
+// executes its LDS accesses in order, so this only keeps the compiler from moving
+// them (no instruction).
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Workspace status word: set bits, never cleared by kernels of the forward.
 __device__ __forceinline__ void raise_status(uint32_t* status, uint32_t bits) {
   atomicOr(status, bits);

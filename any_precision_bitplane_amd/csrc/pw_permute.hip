@@ -296,7 +296,7 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
       off += c[i];
     }
     if (lane == kWave - 1 && blockIdx.x == 0) a.offsets[a.E] = inclusive;
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     for (int r0 = 0; r0 < slots; r0 += kWave) {
       const int s = r0 + lane;
       const uint32_t e = s < slots ? expert_of(a.ids[t0 * a.k + s], a.E) : kDropped;
@@ -307,9 +307,9 @@ __global__ __launch_bounds__(kThreads) void permute_scatter_kernel(PermuteArgs a
       }
       const int rank = __popcll(same & ((1ull << lane) - 1ull));
       const int start = e != kDropped ? next[e] : 0;
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
       if (e != kDropped && rank == 0) next[e] = start + __popcll(same);
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
       if (s < slots) {
         const int p = e == kDropped ? -1 : start + rank;
         pos[s] = p;

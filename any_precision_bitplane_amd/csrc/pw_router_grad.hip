@@ -98,7 +98,7 @@ __device__ __forceinline__ void router_grad_w(const RouterGradArgs& a, int block
       if (id[i] == e) mine[n + __popcll(mask & ((1ull << lane) - 1ull))].t = (wave + kWaves * i) * kWave + lane;
       n += __popcll(mask);
     }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     // ... then as tokens with their dl
     for (int i = lane; i < n; i += kWave) mine[i] = slot_dl(a, c0 + mine[i].t);
     if (lane == 0) listed[wave] = n;
