@@ -417,6 +417,12 @@ def _array(t, name, n, dev, dtype):
     return t.data_ptr()
 
 
+def _words(t, name, n, dev):
+    """Pointer of n contiguous 32-bit words: the library's are unsigned, torch code mostly keeps them in int32."""
+    unsigned = t is not None and t.dtype is _torch.uint32
+    return _array(t, name, n, dev, _torch.uint32 if unsigned else _torch.int32)
+
+
 def _scratch(t, dev):
     if t is None:
         return None, 0
@@ -530,7 +536,7 @@ def pw_moe_permute(shp: PwMoeShape, T: int, x, ids, xs, offsets, inv, perm, work
             ctypes.byref(shp), T, _DTYPES.get(dt, -1), px, sx, _array(x_scale, "x_scale", T * groups, dev, f32),
             groups, _array(ids, "ids", S, dev, i32), ps, ss, _array(xs_scale, "xs_scale", S * groups, dev, f32),
             _array(offsets, "offsets", shp.num_experts + 1, dev, i32), _array(inv, "inv", S, dev, i32),
-            _array(perm, "perm", S, dev, i32), _array(status, "status", 1, dev, i32), pw, nw, _handle(stream, dev)))
+            _array(perm, "perm", S, dev, i32), _words(status, "status", 1, dev), pw, nw, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_moe_permute", check, e)
 
@@ -606,14 +612,12 @@ def pw_moe_forward_block(shp: PwMoeShape, T: int, x, residual, norm_w, eps: floa
     lib = _load_ops()
     try:
         dev, H, E, f16 = _gpu(x), shp.hidden, shp.num_experts, _torch.float16
-        # the library's counts are unsigned; torch code mostly keeps them in int32
-        counts = _torch.uint32 if stat_count is not None and stat_count.dtype is _torch.uint32 else _torch.int32
         pw, nw = _scratch(workspace, dev)
         return _call("pw_moe_forward_block", check, dev, lib.pw_moe_forward_block, (
             ctypes.byref(shp), T, _array(x, "x", T * H, dev, f16), _array(residual, "residual", T * H, dev, f16),
             _array(norm_w, "norm_w", H, dev, f16), eps, _array(router_w, "router_w", E * H, dev, f16),
             _table(blocks, "blocks", 2 * E * ctypes.sizeof(PwBlockDesc), dev), _table(q, "q", 2 * E, dev),
-            _array(y, "y", T * H, dev, f16), _array(stat_count, "stat_count", E, dev, counts),
+            _array(y, "y", T * H, dev, f16), _words(stat_count, "stat_count", E, dev),
             _array(stat_mass, "stat_mass", E, dev, _torch.float32), pw, nw,
             ctypes.byref(opts) if opts is not None else None, _handle(stream, dev)))
     except _Refused as e:

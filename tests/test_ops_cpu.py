@@ -273,3 +273,28 @@ def test_router_gradient_workspace_of_large_calls(lib):
     size = lambda H, E, k, T: B.pw_router_backward_workspace_bytes(B.shape(H, 32, E, k), T) >> 20
     assert size(8192, 256, 8, 1 << 20) <= 34 and size(7168, 256, 8, 1 << 18) <= 34
     assert size(4096, 8, 2, 1 << 20) <= 34 and size(2048, 60, 4, 32768) <= 34
+
+
+def test_permute_binding_takes_unsigned_status(lib, shp, monkeypatch):
+    """The status word is a device uint32: torch.uint32 and int32 are both passed on, other types refused."""
+    import torch
+    B._load_ops()
+    calls = []
+
+    class Lib:
+        @staticmethod
+        def pw_moe_permute(*a):
+            calls.append(a)
+            return B.PW_OK
+
+    monkeypatch.setattr(B, "_lib", Lib)
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_current_stream", lambda dev: 0)
+    on = lambda *n, d=torch.int32: Elsewhere(torch.zeros(n, dtype=d), 0)
+    x, xs = on(4, 256, d=torch.float16), on(8, 256, d=torch.float16)
+    call = lambda st: B.pw_moe_permute(shp, 4, x, on(4, 2), xs, on(9), on(8), None, on(64), status=st, check=False)
+    for dtype in (torch.int32, torch.uint32):
+        status = on(1, d=dtype)
+        assert call(status) == B.PW_OK and calls[-1][14] == status.t.data_ptr()
+    assert call(None) == B.PW_OK and calls[-1][14] is None
+    assert call(on(1, d=torch.int64)) == B.PW_ERR_INVALID_ARG and len(calls) == 3
