@@ -348,7 +348,10 @@ pw_status pw_moe_forward_layers(const pw_moe_shape* shape /* host */, int32_t L,
  * captured into a graph, and leaves what it does not write as it was.  Inputs
  * that hold NaN or infinities give what the formula gives.  A workspace is
  * 256-byte aligned and needs no initialisation; calls that may overlap in time
- * (two streams, two captured graphs) need workspaces of their own.
+ * (two streams, two captured graphs) need workspaces of their own.  A call with
+ * a size function of its own here writes over the status word of a workspace
+ * that a forward uses too: give it another.  A shape is one that
+ * pw_check_shape accepts.
  * ---------------------------------------------------------------------- */
 #define PW_F32  0
 #define PW_F16  1
