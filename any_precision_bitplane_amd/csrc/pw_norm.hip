@@ -9,7 +9,10 @@
 // fp32 sum, before the residual's own rounding.
 //
 // The work is one pass over memory: a row's chunks of eight elements stay in
-// registers between the sum of squares and the output.
+// registers between the sum of squares and the output.  Above 16384 columns the
+// four chunks a lane no longer all fit beside the next row's: fp32 spills 30
+// registers a lane (87 to e4m3, 16-bit rows 12 to e4m3), fp32 [2048][32768]
+// with the residual 274 us, 3.9 TB/s, bf16 103 us, 5.2 TB/s.
 #include "pw_rows.h"
 
 namespace pw {
@@ -113,8 +116,8 @@ __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_kernel(NormA
     }
   };
   // The weight is requested with the row, not after its sum (fp16 [16384][4096]
-  // 97 -> 93 us, bf16 to e4m3 91 -> 81), and the row before the loop, ahead of
-  // what the compiler moves out of it (bf16 [65536][2048] alone 98 -> 87).
+  // 4% faster, bf16 to e4m3 11%), and the row before the loop, ahead of what the
+  // compiler moves out of it (bf16 [65536][2048] without a residual 11%).
 #pragma unroll
   for (int i = 0; i < NV; ++i) g[i] = R::load(static_cast<const elem*>(a.weight) + at[i]);
   fetch((int64_t)blockIdx.x * kRows + own);
@@ -217,10 +220,10 @@ hipError_t run_norm(const NormArgs& a, hipStream_t s) {
 // A row over as many lanes as it has chunks for, up to sixteen waves, so each
 // lane waits for one load.  Four chunks a lane and a quarter of the waves were
 // slower nearly everywhere (fp16 [64][2048] 4.8 us against 3.0, [16384][4096]
-// 103.8 against 97.1, fp32 205 against 185; faster by 5% for fp16 [4096][4096],
-// which stays in the caches).
-// Measured with the residual: fp16 [16384][4096] 90 us, 5.9 TB/s; bf16 to e4m3
-// 78 us, 6.0 TB/s; fp32 185 us, 5.8 TB/s (a large copy: 5.0).
+// by 7%, fp32 by 11%; faster by 5% for fp16 [4096][4096], which stays in the
+// caches).
+// Measured with the residual: fp16 [16384][4096] 89 us, 6.0 TB/s; bf16 to e4m3
+// 78 us, 6.0 TB/s; fp32 184 us, 5.8 TB/s (a large copy: 5.0).
 template <int DT, bool Q8>
 hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
   const int C = a.H / 8;
@@ -243,12 +246,13 @@ hipError_t pick_norm(const NormArgs& a, hipStream_t s) {
 // r (both sums in the same pass), so the forward keeps nothing but its
 // residual output.  A block walks every gridDim-th group of rows and keeps its
 // share of dg in registers; the shares meet in a second kernel, in a fixed
-// order.  Measured: bf16 [16384][4096] with dresidual 97 us, 5.6 TB/s.
+// order.  Measured: bf16 [16384][4096] with dresidual 95 us, 5.6 TB/s.
 //
 // AHEAD: the next row is requested before the current one is used (dx may be
 // written over an input: the rows in flight are the block's own later ones).
-// LEAN: the weight and dresidual are loaded where they are used, so that the
-// longest rows' chunks stay in registers.
+// LEAN: the weight and dresidual are loaded where they are used, so that more of
+// the longest rows' chunks stay in registers (above 16384 columns 17 to 21 of
+// them still spill: bf16 [2048][32768] 158 us, 3.4 TB/s, fp32 254 us, 4.2 TB/s).
 template <int DT, int LPR, int WPR, int NV, bool AHEAD, bool LEAN>
 __global__ __launch_bounds__(block_waves(WPR) * kWave) void rmsnorm_grad_kernel(NormGradArgs a) {
   using R = Row<DT>;

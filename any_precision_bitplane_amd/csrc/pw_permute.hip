@@ -224,9 +224,9 @@ __global__ __launch_bounds__(kWave) void permute_scan_kernel(PermuteArgs a) {
   if (lane == 0) a.counts[(int64_t)a.pieces * a.E + e] = carry;
 }
 
-// Last launch, nearly all of a large call's time (T = 32768, H = 2048, k = 4 136
-// of 141 us, 4.9 TB/s of rows read and written): a block takes block_tokens
-// tokens of one piece.  An expert's slots of this block start at its offset plus
+// Last launch, nearly all of a large call's time (T = 32768, H = 2048, k = 4, bf16
+// 141 us, 4.8 TB/s of rows read and written, after 4.7 for the counts): a block
+// takes block_tokens tokens of one piece.  An expert's slots of this block start at its offset plus
 // its slots in earlier pieces and in earlier blocks of the piece (counted again
 // here); inside the block a slot's rank is its position among the equal ids,
 // found by ballots of one wave.  Each wave requests its first token's row before

@@ -16,10 +16,12 @@
 // XCD, whose L2 serves all but the first.  dx: a wave takes a token; the
 // router's rows come from L2, and dx is stored past it.  With several stretches
 // a second launch sums their shares in order.
-// Bound by memory: T = 16384, H = 4096, E = 8, k = 2 81 us, 5.0 TB/s of x, dx_add
+// Bound by memory: T = 16384, H = 4096, E = 8, k = 2 80 us, 5.0 TB/s of x, dx_add
 // and dx; from E = 60 on also by the L2s, which serve each row of x and of the
 // router k times (T = 32768, H = 2048, E = 60, k = 4 111 us, 3.6 TB/s; E = 256,
-// k = 8 102 us for half the tokens).
+// k = 8 103 us for half the tokens).  With skewed routing by the hot expert's
+// blocks, each of which sums all rows that its expert has in a stretch (136 us
+// and 169 us for the same two).
 #include "pw_rows.h"
 
 namespace pw {
