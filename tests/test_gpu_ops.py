@@ -1222,3 +1222,32 @@ def test_router_gradient_of_slots_masked_after_the_router(torch):
     ref = X.grad.numpy()
     near(f64(dx), ref, np.abs(ref) * 2.0 ** -11 + 2.0 ** -25 + slack * np.max(np.abs(f64(wr))), "dx")
     near(f64(dwr), W.grad.numpy(), slack * np.sum(np.abs(f64(x)), axis=0), "drouter_w")
+
+
+def test_forward_block_on_another_stream(torch):
+    say("forward_block on two streams at once, each with its own workspace, equal to calls alone")
+    L = synth.make_layer(synth.WORKLOADS["tiny"])
+    dev, w = DeviceLayer(L, device=DEV), L.wl
+    g, wr = rand(torch, 3, (1, w.H), "f16")[0], torch.from_numpy(synth.draw_router_weights(5, w.E, w.H)).to(DEV)
+    sets, want = [], []
+    for n in range(2):
+        ws = torch.empty_like(dev.ws)
+        B.pw_workspace_init(ws)
+        sets.append((rand(torch, 10 + n, (w.T, w.H), "f16"), rand(torch, 20 + n, (w.T, w.H), "f16"), ws))
+    call = lambda x, res, y, ws, st: B.pw_moe_forward_block(dev.shape, w.T, x, res, g, EPS, wr, dev.blocks[0], dev.q, y,
+                                                            None, None, ws, stream=st)
+    for x, res, ws in sets:
+        r, y = res.clone(), torch.empty_like(x)
+        for _ in range(3):
+            call(x, r, y, ws, None)
+        want.append((r, y))
+    torch.cuda.synchronize()
+    out = [(res.clone(), torch.empty_like(x)) for x, res, _ in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (x, _, ws), (r, y), st in zip(sets, out, streams):
+            call(x, r, y, ws, st)
+    torch.cuda.synchronize()
+    for (r, y), (rw, yw) in zip(out, want):
+        assert torch.equal(r, rw) and torch.equal(y, yw)
