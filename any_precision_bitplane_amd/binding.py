@@ -54,6 +54,10 @@ PW_F16 = 1
 PW_BF16 = 2
 PW_E4M3 = 3
 
+PW_ACT_NONE = 0
+PW_ACT_SILU = 1
+PW_ACT_GELU = 2
+
 
 class PwMoeShape(ctypes.Structure):
     _fields_ = [("hidden", c_int32), ("inter", c_int32), ("num_experts", c_int32), ("top_k", c_int32)]
@@ -164,6 +168,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "pw_moe_forward_block": (c_int32, [POINTER(PwMoeShape), c_int32, c_void_p, c_void_p, c_void_p, c_float,
                                            c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
                                            c_size_t, POINTER(PwMoeOptions), c_void_p]),
+        "pw_moe_product_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_int32]),
+        "pw_moe_product_backward_workspace_bytes": (c_size_t, [c_int32, c_int32, c_int32, c_int32]),
+        "pw_moe_product": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p,
+                                     c_void_p, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                     c_void_p, c_size_t, c_void_p]),
+        "pw_moe_product_backward": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_int64, c_void_p,
+                                              c_int64, c_void_p, c_void_p, c_int32, c_void_p, c_int64, c_void_p,
+                                              c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "pw_moe_ffn_workspace_bytes": (c_size_t, [POINTER(PwMoeShape), c_int32]),
+        "pw_moe_ffn_backward_workspace_bytes": (c_size_t, [POINTER(PwMoeShape), c_int32]),
+        "pw_moe_ffn": (c_int32, [POINTER(PwMoeShape), c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                 c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_size_t,
+                                 c_void_p]),
+        "pw_moe_ffn_backward": (c_int32, [POINTER(PwMoeShape), c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64,
+                                          c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_int64, c_void_p,
+                                          c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -183,7 +203,9 @@ def exported_symbols() -> Sequence[str]:
             "pw_plan_bitwidths", "pw_rmsnorm", "pw_rmsnorm_backward_workspace_bytes", "pw_rmsnorm_backward",
             "pw_moe_permute_workspace_bytes", "pw_moe_permute", "pw_moe_permute_backward", "pw_moe_unpermute",
             "pw_moe_unpermute_backward", "pw_router_backward_workspace_bytes", "pw_router_backward",
-            "pw_moe_forward_block"]
+            "pw_moe_forward_block", "pw_moe_product_workspace_bytes", "pw_moe_product_backward_workspace_bytes",
+            "pw_moe_product", "pw_moe_product_backward", "pw_moe_ffn_workspace_bytes",
+            "pw_moe_ffn_backward_workspace_bytes", "pw_moe_ffn", "pw_moe_ffn_backward"]
 
 
 # ---------------------------------------------------------------------------
@@ -622,6 +644,109 @@ def pw_moe_forward_block(shp: PwMoeShape, T: int, x, residual, norm_w, eps: floa
             ctypes.byref(opts) if opts is not None else None, _handle(stream, dev)))
     except _Refused as e:
         return _refuse("pw_moe_forward_block", check, e)
+
+
+# --- expert products in 16 bits ---------------------------------------------
+def pw_moe_product_workspace_bytes(E: int, S_max: int, N: int, K: int) -> int:
+    return load().pw_moe_product_workspace_bytes(E, S_max, N, K)
+
+
+def pw_moe_product_backward_workspace_bytes(E: int, S_max: int, N: int, K: int) -> int:
+    return load().pw_moe_product_backward_workspace_bytes(E, S_max, N, K)
+
+
+def pw_moe_product(E: int, S: int, N: int, K: int, x, w, y, workspace, offsets=None, bias=None, act: int = PW_ACT_NONE,
+                   residual=None, pre=None, stream=None, check: bool = True) -> int:
+    """offsets: int32 [E+1], or None for one expert with all rows."""
+    lib = _load_ops()
+    try:
+        dev, dt = _gpu(x), x.dtype
+        px, sx = _rows(x, "x", S, K, dev, dt)
+        pr, sr = _rows(residual, "residual", S, N, dev, dt)
+        pp, sp = _rows(pre, "pre", S, N, dev, dt)
+        py, sy = _rows(y, "y", S, N, dev, dt)
+        pw, nw = _scratch(workspace, dev)
+        return _call("pw_moe_product", check, dev, lib.pw_moe_product, (
+            E, S, N, K, _DTYPES.get(dt, -1), px, sx, _array(offsets, "offsets", E + 1, dev, _torch.int32),
+            _array(w, "w", E * N * K, dev, dt), _array(bias, "bias", E * N, dev, dt), act, pr, sr, pp, sp, py, sy, pw,
+            nw, _handle(stream, dev)))
+    except _Refused as e:
+        return _refuse("pw_moe_product", check, e)
+
+
+def pw_moe_product_backward(E: int, S: int, N: int, K: int, dy, x, w, workspace, offsets=None, act: int = PW_ACT_NONE,
+                            pre=None, dx=None, dw=None, dbias=None, stream=None, check: bool = True) -> int:
+    """dx, dw, dbias None: not wanted (without dx, w may be None; without dw, x may be)."""
+    lib = _load_ops()
+    try:
+        dev, dt = _gpu(dy), dy.dtype
+        pd, sd = _rows(dy, "dy", S, N, dev, dt)
+        px, sx = _rows(x, "x", S, K, dev, dt)
+        pp, sp = _rows(pre, "pre", S, N, dev, dt)
+        po, so = _rows(dx, "dx", S, K, dev, dt)
+        pw, nw = _scratch(workspace, dev)
+        return _call("pw_moe_product_backward", check, dev, lib.pw_moe_product_backward, (
+            E, S, N, K, _DTYPES.get(dt, -1), pd, sd, px, sx, _array(offsets, "offsets", E + 1, dev, _torch.int32),
+            _array(w, "w", E * N * K, dev, dt), act, pp, sp, po, so, _array(dw, "dw", E * N * K, dev, dt),
+            _array(dbias, "dbias", E * N, dev, dt), pw, nw, _handle(stream, dev)))
+    except _Refused as e:
+        return _refuse("pw_moe_product_backward", check, e)
+
+
+def pw_moe_ffn_workspace_bytes(shp: PwMoeShape, S_max: int) -> int:
+    return load().pw_moe_ffn_workspace_bytes(ctypes.byref(shp), S_max)
+
+
+def pw_moe_ffn_backward_workspace_bytes(shp: PwMoeShape, S_max: int) -> int:
+    return load().pw_moe_ffn_backward_workspace_bytes(ctypes.byref(shp), S_max)
+
+
+def _kept(z, z_scale, S, I, dev, dt):
+    """(type, pointer, row stride, pointer of the scales) of the checkpoint of gate and up."""
+    if z is None:
+        return _DTYPES.get(dt, -1), None, 0, _array(z_scale, "z_scale", 0, dev, _torch.float32)
+    pz, sz = _rows(z, "z", S, 2 * I, dev, z.dtype)
+    return _DTYPES.get(z.dtype, -1), pz, sz, _array(z_scale, "z_scale", S * 2 * ((I + 127) // 128), dev, _torch.float32)
+
+
+def pw_moe_ffn(shp: PwMoeShape, S: int, x, w_gate_up, w_down, y, workspace, offsets=None, act: int = PW_ACT_SILU,
+               z=None, z_scale=None, stream=None, check: bool = True) -> int:
+    """z: checkpoint [S][2I] in x's type, or torch.float8_e4m3fn with z_scale fp32 [S][2 ceil(I / 128)]."""
+    lib = _load_ops()
+    try:
+        dev, dt, E, H, I = _gpu(x), x.dtype, shp.num_experts, shp.hidden, shp.inter
+        px, sx = _rows(x, "x", S, H, dev, dt)
+        py, sy = _rows(y, "y", S, H, dev, dt)
+        zt, pz, sz, pc = _kept(z, z_scale, S, I, dev, dt)
+        pw, nw = _scratch(workspace, dev)
+        return _call("pw_moe_ffn", check, dev, lib.pw_moe_ffn, (
+            ctypes.byref(shp), S, _DTYPES.get(dt, -1), px, sx, _array(offsets, "offsets", E + 1, dev, _torch.int32),
+            _array(w_gate_up, "w_gate_up", E * 2 * I * H, dev, dt), _array(w_down, "w_down", E * H * I, dev, dt), act,
+            zt, pz, sz, pc, py, sy, pw, nw, _handle(stream, dev)))
+    except _Refused as e:
+        return _refuse("pw_moe_ffn", check, e)
+
+
+def pw_moe_ffn_backward(shp: PwMoeShape, S: int, dy, x, w_gate_up, w_down, z, workspace, offsets=None,
+                        act: int = PW_ACT_SILU, z_scale=None, dx=None, dw_gate_up=None, dw_down=None, stream=None,
+                        check: bool = True) -> int:
+    """dx, dw_gate_up, dw_down None: not wanted (without dx, w_gate_up may be None; without dw_gate_up, x may be)."""
+    lib = _load_ops()
+    try:
+        dev, dt, E, H, I = _gpu(dy), dy.dtype, shp.num_experts, shp.hidden, shp.inter
+        pd, sd = _rows(dy, "dy", S, H, dev, dt)
+        px, sx = _rows(x, "x", S, H, dev, dt)
+        po, so = _rows(dx, "dx", S, H, dev, dt)
+        zt, pz, sz, pc = _kept(z, z_scale, S, I, dev, dt)
+        pw, nw = _scratch(workspace, dev)
+        return _call("pw_moe_ffn_backward", check, dev, lib.pw_moe_ffn_backward, (
+            ctypes.byref(shp), S, _DTYPES.get(dt, -1), pd, sd, px, sx,
+            _array(offsets, "offsets", E + 1, dev, _torch.int32),
+            _array(w_gate_up, "w_gate_up", E * 2 * I * H, dev, dt), _array(w_down, "w_down", E * H * I, dev, dt), act,
+            zt, pz, sz, pc, po, so, _array(dw_gate_up, "dw_gate_up", E * 2 * I * H, dev, dt),
+            _array(dw_down, "dw_down", E * H * I, dev, dt), pw, nw, _handle(stream, dev)))
+    except _Refused as e:
+        return _refuse("pw_moe_ffn_backward", check, e)
 
 
 # --- planner ----------------------------------------------------------------

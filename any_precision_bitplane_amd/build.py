@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpagedweight.so")
 SOURCES = ["pw_api.cpp", "pw_ops.cpp", "pw_pager.cpp", "pw_route.hip", "pw_gemv.hip", "pw_mfma.hip", "pw_misc.hip",
            "pw_router.hip", "pw_planner.cpp", "pw_mgemv.hip", "pw_noalloc.hip", "pw_norm.hip", "pw_permute.hip",
-           "pw_router_grad.hip"]
+           "pw_router_grad.hip", "pw_products.cpp", "pw_product.hip", "pw_product_grad.hip", "pw_product_few.hip"]
 ARCH = "gfx950"
 
 

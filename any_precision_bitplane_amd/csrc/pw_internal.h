@@ -427,6 +427,62 @@ inline RouterGradPlan router_grad_plan(int H, int E, int k, int64_t T) {
 }
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
 
+// Products of the experts' rows (pw_product.hip, pw_product_few.hip): what each kind reads and writes.
+enum { kProductAct, kProductGate, kProductBack, kProductGateGrad };
+struct ProductArgs {
+  int E, S, N, K;             // columns of the result (gated: of one half), length of the reduction
+  const int32_t* offsets;     // null: one expert with all rows
+  const void* x;              // [S][K]
+  int64_t x_stride;
+  const void* w;              // [E][N][K]; gated [E][2N][K]; back [E][K][N]
+  int64_t w_expert;           // elements between two experts' matrices
+  const void* bias;           // [E][N] or null
+  const void* residual;       // [S][N] or null
+  int64_t residual_stride;
+  void* pre;                  // [S][N] or null; gated, back: dz [S][2N]
+  int64_t pre_stride;
+  void* y;                    // [S][N]; gated, back: h, or null
+  int64_t y_stride;
+  int act;
+  void* z;                    // gate and up [S][2N]: written by the gated product (or null), read by its way back
+  int64_t z_stride;
+  float* z_scale;             // [S][2 groups], of 8-bit z
+  int groups;
+  bool z8;
+  int NT;                     // set by the launch: column tiles
+};
+hipError_t launch_product(const ProductArgs& a, int dtype, int kind, hipStream_t s);
+bool few_rows(const ProductArgs& a, int kind);
+hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s);
+
+// out[e] = p^T q over the rows of expert e
+struct OuterArgs {
+  int E, S, M, N;
+  const int32_t* offsets;
+  const void* p;              // [S][M]
+  int64_t p_stride;
+  const void* q;              // [S][N]
+  int64_t q_stride;
+  void* out;                  // [E][M][N]
+  int MT, NT;                 // set by the launch
+  unsigned tiles;
+};
+hipError_t launch_outer(const OuterArgs& a, int dtype, hipStream_t s);
+
+struct DzArgs {
+  int E, S, N, act;
+  const int32_t* offsets;
+  const void* dy;             // [S][N]
+  int64_t dy_stride;
+  const void* pre;
+  int64_t pre_stride;
+  void* dz;                   // [S][N] without gaps, or null
+  float* part;                // column sums of stretches of rows, or null
+  void* dbias;                // [E][N] or null
+};
+size_t dz_part_floats(int E, int64_t S, int N);
+hipError_t launch_dz(const DzArgs& a, int dtype, hipStream_t s);
+
 // The fused layer on a caller-provided scratch area (the workspace, or the
 // allocation-free entry point's static array).  `status`, if non-null,
 // replaces the status word of the scratch header as the place device errors

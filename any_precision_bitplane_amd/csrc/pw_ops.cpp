@@ -1,27 +1,11 @@
 // C-ABI host layer of the operators around the routed layer: the norm in front
 // of it, tokens sorted by expert and back, and the gradients.  Argument checks
 // and launches only.
-#include "pw_internal.h"
+#include "pw_checks.h"
 
 using namespace pw;
 
 namespace {
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-pw_status hip_status(hipError_t e) { return e == hipSuccess ? PW_OK : PW_ERR_HIP; }
-
-// Bytes of an element of a row type, 0 if it is none.
-int64_t row_type_bytes(int32_t dtype) { return dtype == PW_F32 ? 4 : (dtype == PW_F16 || dtype == PW_BF16) ? 2 : 0; }
-
-// A matrix of T rows of H elements: 16-byte aligned rows `stride` elements
-// apart.  Rows that are written must not overlap.
-pw_status check_rows(const void* p, int64_t stride, int64_t T, int64_t H, int64_t bytes, bool written) {
-  if (!p) return PW_ERR_INVALID_ARG;
-  if (stride < 0 || (written && T > 1 && stride < H)) return PW_ERR_INVALID_ARG;
-  if (!aligned(p, 16) || (stride * bytes) % 16) return PW_ERR_ALIGNMENT;
-  return PW_OK;
-}
 
 pw_status check_norm_shape(int32_t T, int32_t H, int32_t dtype, float eps) {
   if (T < 0 || H <= 0 || !row_type_bytes(dtype)) return PW_ERR_INVALID_ARG;
@@ -29,12 +13,6 @@ pw_status check_norm_shape(int32_t T, int32_t H, int32_t dtype, float eps) {
   if (H % 8 || H > kMaxNormHidden) return PW_ERR_UNSUPPORTED_SHAPE;
   return PW_OK;
 }
-
-#define PW_TRY(expr)                     \
-  do {                                   \
-    const pw_status st_ = (expr);        \
-    if (st_ != PW_OK) return st_;        \
-  } while (0)
 
 pw_status unpermute(const pw_moe_shape* shape, int32_t T, int32_t dtype, const void* rows, int64_t rows_stride,
                     const int32_t* inv, const float* w, void* y, int64_t y_stride, void* stream) {

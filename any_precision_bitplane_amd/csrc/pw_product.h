@@ -1,0 +1,278 @@
+// 16-bit products of the rows of every expert with its matrix, on the matrix
+// cores with fp32 sums: what the kernels of pw_product.hip, pw_product_grad.hip
+// and pw_product_few.hip share.
+//
+// Tiles.  A block takes a tile of BM rows by 256 columns of one expert and walks
+// the reduction in steps of 64.  A step's operands are copied from memory to LDS
+// without passing registers, one step ahead of the products, in two buffers.
+// An operand whose reduction index is contiguous in memory lies in LDS as rows
+// of 64 (eight 16-byte pieces, piece c of row r at place c ^ (r & 7), so that
+// the eight rows of a read fall on different banks); one whose other index is
+// contiguous lies as it is and is transposed by the reads.
+#pragma once
+
+#include "pw_device.h"
+#include "pw_internal.h"
+#include "pw_rows.h"
+
+namespace pw {
+
+constexpr int kProdN = 256;       // columns of a tile: two halves of 128
+constexpr int kProdK = 64;        // reduction steps
+constexpr int kProdGroup = 8;     // row tiles that go through all columns together
+constexpr uint32_t kRsrcBytes = 0x80000000u;
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_void;
+
+template <int DT>
+struct Mma;
+template <>
+struct Mma<PW_F16> {
+  typedef _Float16 frag __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ f32x16 wide(s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 slim(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<PW_BF16> {
+  typedef __bf16 frag __attribute__((ext_vector_type(8)));
+  static __device__ __forceinline__ f32x16 wide(s16x8 a, s16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 slim(s16x8 a, s16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
+  }
+};
+
+// Rows [first, first + count) of expert e, inside [0, S) whatever offsets holds.
+__device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int S, int& first, int& count) {
+  if (!offsets) {
+    first = 0;
+    count = S;
+    return;
+  }
+  const int a = min(max(offsets[e], 0), S), b = min(max(offsets[e + 1], 0), S);
+  first = a;
+  count = max(b - a, 0);
+}
+
+// Tile of a block.  Tiles are numbered expert by expert, inside one in groups of
+// kProdGroup row tiles that go through the column tiles together, and dealt to
+// the eight XCDs in contiguous stretches, so that what runs together on an XCD
+// shares rows of x and of w in its L2.
+struct Tile {
+  int e, row0, rows, nt;   // rows: the expert's from row0 on; 0: no tile for this block
+};
+
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int E, int S, int NT) {
+  const int lane = (int)threadIdx.x & (kWave - 1);
+  int first[4] = {0, 0, 0, 0}, count[4] = {0, 0, 0, 0}, mine = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = 4 * lane + j;
+    if (e < E) expert_rows(offsets, e, S, first[j], count[j]);
+    mine += (count[j] + BM - 1) / BM;
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d *= 2) {
+    const int v = __shfl_up(upto, d, kWave);
+    if (lane >= d) upto += v;
+  }
+  const unsigned total = (unsigned)__builtin_amdgcn_readlane(upto, kWave - 1) * (unsigned)NT;
+  const unsigned each = (total + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each + i;
+  if (i >= each || id >= total) return {0, 0, 0, 0};
+  const int m = (int)(id / (unsigned)NT);
+  int before = upto - mine;
+  const int owner = __builtin_ctzll(__ballot(before <= m && m < upto));
+  int e = 4 * lane, from = first[0], n = count[0];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    const int t = (count[j] + BM - 1) / BM;
+    if (e == 4 * lane + j && before + t <= m) {
+      before += t;
+      e = 4 * lane + j + 1;
+      from = first[j + 1];
+      n = count[j + 1];
+    }
+  }
+  e = __builtin_amdgcn_readlane(e, owner);
+  from = __builtin_amdgcn_readlane(from, owner);
+  n = __builtin_amdgcn_readlane(n, owner);
+  before = __builtin_amdgcn_readlane(before, owner);
+  const int tiles = (n + BM - 1) / BM;
+  const int local = (int)(id - (unsigned)before * (unsigned)NT);
+  const int group = local / (kProdGroup * NT), rem = local - group * kProdGroup * NT;
+  const int here = min(kProdGroup, tiles - group * kProdGroup);
+  const int nt = rem / here, mt = group * kProdGroup + rem - nt * here;
+  return {e, from + mt * BM, n - mt * BM, nt};
+}
+
+// Blocks that cover every tile whatever the offsets: a row tile more per expert
+// with rows than the rows fill.
+inline int64_t product_row_tiles(const int32_t* offsets, int E, int64_t S, int BM) {
+  if (!offsets) return (S + BM - 1) / BM;
+  const int64_t with_rows = S < E ? S : E;
+  return S / BM + with_rows < S ? S / BM + with_rows : S;
+}
+inline int64_t product_grid(int64_t row_tiles, int64_t NT) { return (row_tiles * NT + 7) / 8 * 8; }
+
+// ----- a tile's operands ------------------------------------------------------
+
+// Where the lanes of a wave fetch their 16-byte pieces of a tile of R rows of 64
+// (reduction contiguous).  at[i]: byte offset of the lane's piece of copy i.
+template <int R, int WAVES>
+struct RowsOperand {
+  static constexpr int kCopies = R / 8 / WAVES;
+  uint32_t at[kCopies];
+  // A copy of a wave covers eight rows: lane l fetches row l / 8, piece (l ^ row) & 7.
+  template <class RowOffset>
+  __device__ __forceinline__ void init(int wave, int lane, RowOffset offset_of) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      at[i] = offset_of((i * WAVES + wave) * 8 + lane / 8) + (uint32_t)(((lane ^ (lane >> 3)) & 7) * 16);
+  }
+  __device__ __forceinline__ void copy(const char* base, char* lds, int wave, int lane, int k, int K) const {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, kRsrcBytes);
+    const bool whole = k + kProdK <= K;
+    const bool in = whole || k + ((lane ^ (lane >> 3)) & 7) * 8 < K;   // past the end reads zero
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void)(lds + (i * WAVES + wave) * 1024), 16,
+                                               (int)(in ? at[i] : kOutOfRange), k * 2, 0, 0);
+  }
+};
+
+// The same of a tile of 64 reduction rows of 256 contiguous columns.
+__device__ __forceinline__ int cols_place(int k) { return 4 * (k & 3); }   // piece c of row k lies at place c ^ this
+template <int WAVES>
+struct ColsOperand {
+  static constexpr int kCopies = 32 / WAVES;
+  uint32_t at[kCopies];
+  int row[kCopies];
+  // A copy of a wave covers two rows: lane l fetches row l / 32.  Columns past the matrix are read from its last piece.
+  __device__ __forceinline__ void init(int wave, int lane, int64_t row_bytes, int pieces) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+      row[i] = (i * WAVES + wave) * 2 + lane / 32;
+      at[i] = (uint32_t)(row[i] * row_bytes) + (uint32_t)(min((lane & 31) ^ cols_place(row[i]), pieces - 1) * 16);
+    }
+  }
+  // base: the first of the step's rows; left: reduction rows from there on
+  __device__ __forceinline__ void copy(const char* base, char* lds, int wave, int left) const {
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, kRsrcBytes);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void)(lds + (i * WAVES + wave) * 1024), 16,
+                                               (int)(row[i] < left ? at[i] : kOutOfRange), 0, 0, 0);
+  }
+};
+
+// Operand of 32 rows (or columns) from `r0` on for the sixteen reduction steps
+// from 16 kk on: lane l holds row l % 32, steps 8 (l / 32) .. + 7.
+__device__ __forceinline__ s16x8 read_rows(const char* lds, int r0, int kk, int lane) {
+  const int r = lane & 31, piece = (2 * kk + lane / 32) ^ (r & 7);
+  return *reinterpret_cast<const s16x8*>(lds + (r0 + r) * 128 + piece * 16);
+}
+// The transposing read gives lane i of sixteen column i of four rows of sixteen
+// columns, lanes 4 j .. 4 j + 3 of which hold the address of row j's.
+__device__ __forceinline__ s16x8 read_cols(const char* lds, int c0, int kk, int lane) {
+  const int k = 16 * kk + 8 * (lane / 32) + (lane & 15) / 4;
+  const int c = c0 + (lane & 16) + 4 * (lane & 3);
+  typedef __attribute__((address_space(3))) s16x4* p4;
+  const char* p = lds + k * 512 + (((c / 8) ^ cols_place(k)) * 16) + (c & 4) * 2;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * 512));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Every wave's copies have landed and every wave is done with the other buffer.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// ----- activations ------------------------------------------------------------
+
+__device__ __forceinline__ float act_of(float z, int act) {
+  if (act == PW_ACT_SILU) return silu_f32(z);
+  if (act == PW_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  return z;
+}
+__device__ __forceinline__ float act_slope(float z, int act) {
+  if (act == PW_ACT_SILU) {
+    const float q = __builtin_amdgcn_rcpf(1.f + __expf(-z));
+    return q * (1.f + z * (1.f - q));
+  }
+  if (act == PW_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+  return 1.f;
+}
+
+// ----- eight bits ---------------------------------------------------------------
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 7.888609052210118e-31f;   // 2^-100: scales stay divisible
+constexpr int kKeepGroup = 128;                       // columns of gate or up that share a scale
+
+// The largest of |v|, infinity where one is no finite number.
+__device__ __forceinline__ float most_of(floatx8 v, float most) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = __builtin_fabsf(v[j]);
+    most = t < INFINITY ? fmaxf(most, t) : INFINITY;
+  }
+  return most;
+}
+__device__ __forceinline__ float scale_of(float most) {
+  return most < INFINITY ? fmaxf(most / kE4m3Max, kScaleMin) : __builtin_nanf("");
+}
+// Codes nearest to v / scale: the product with the reciprocal, corrected by its remainder.
+__device__ __forceinline__ uint2 codes_of(floatx8 v, float scale) {
+  if (!(scale < INFINITY)) return {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+  const float inv = 1.f / scale;
+  floatx8 q;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = v[j] * inv;
+    q[j] = fminf(fmaxf(__builtin_fmaf(__builtin_fmaf(-t, scale, v[j]), inv, t), -kE4m3Max), kE4m3Max);
+  }
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false), hi;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
+  return {(uint32_t)lo, (uint32_t)hi};
+}
+__device__ __forceinline__ floatx8 values_of(uint2 codes, float scale) {
+  floatx8 v;
+#define PW_CODE(i, word, at) v[i] = __builtin_amdgcn_cvt_f32_fp8((int)(word), at) * scale
+  PW_CODE(0, codes.x, 0); PW_CODE(1, codes.x, 1); PW_CODE(2, codes.x, 2); PW_CODE(3, codes.x, 3);
+  PW_CODE(4, codes.y, 0); PW_CODE(5, codes.y, 1); PW_CODE(6, codes.y, 2); PW_CODE(7, codes.y, 3);
+#undef PW_CODE
+  return v;
+}
+
+// Sums of 32 rows by 32 columns come with lane l holding row l % 32 and columns
+// 8 q + 4 (l / 32) .. + 3 in registers 4 q .. 4 q + 3.  Half of them exchanged
+// with lane l ^ 32, a lane holds eight neighbouring columns: 8 (2 p + l / 32) ..
+// + 7 for p = 0, 1.  Both lanes of a pair have to be active.
+__device__ __forceinline__ floatx8 eight_columns(const f32x16& acc, int p) {
+  floatx8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[8 * p + i]), __float_as_uint(acc[8 * p + 4 + i]),
+                                                    false, false);
+    v[i] = __uint_as_float(r[0]);
+    v[4 + i] = __uint_as_float(r[1]);
+  }
+  return v;
+}
+
+}  // namespace pw

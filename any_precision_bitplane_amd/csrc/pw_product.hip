@@ -1,0 +1,261 @@
+// Products of every expert's rows with its matrix, with what follows them:
+//
+//   product        z = x W^T + bias,  y = act(z) + residual          W [N][K]
+//   gated          [g | u] = x W^T,   h = act(g) u                   W [2N][K]
+//   back           dx = dz W                                         W [K][N]
+//   gated, back    dh = dy W,  dg = dh u act'(g),  du = dh act(g),  h = act(g) u
+//
+// in tiles of 32 to 256 rows by 256 columns (gated: 128 of g and the same 128 of
+// u, so that a lane holds both for its columns).
+#include "pw_product.h"
+
+namespace pw {
+
+namespace {
+
+template <int MI, int WM>
+struct Shape {
+  static constexpr int kRows = MI * WM * 32;
+  static constexpr int kWaves = WM * 4;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int kABytes = kRows * 128;
+  static constexpr int kStage = kABytes + kProdN * 128;
+};
+
+template <int DT, int EPI, int MI, int WM>
+__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x16 (&acc)[MI][2], char* lds, int wm, int wn,
+                                       int lane) {
+  using R = Row<DT>;
+  using elem = typename R::elem;
+  const int hi = lane / 32;
+  constexpr bool kGate = EPI == kProductGate;
+  const int n0 = t.nt * (kGate ? kKeepGroup : kProdN) + wn * 32;
+  float scale[MI][2];
+  if (kGate && a.z8) {
+    // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the four waves'
+    float* part = reinterpret_cast<float*>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float most = 0.f;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const bool in = n0 + 8 * (2 * p + hi) < a.N;
+          const floatx8 v = eight_columns(acc[mi][half], p);
+          if (in) most = most_of(v, most);
+        }
+        most = fmaxf(most, __shfl_xor(most, 32, kWave));
+        if (hi == 0) part[(half * Shape<MI, WM>::kRows + (wm * MI + mi) * 32 + lane) * 4 + wn] = most;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float* p = part + (half * Shape<MI, WM>::kRows + (wm * MI + mi) * 32 + (lane & 31)) * 4;
+        scale[mi][half] = scale_of(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])));
+      }
+  }
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const int r = (wm * MI + mi) * 32 + (lane & 31);
+    if (r >= t.rows) continue;
+    const int64_t row = t.row0 + r;
+    if constexpr (kGate) {
+      if (a.z8 && wn == 0 && hi == 0) {
+        float* s = a.z_scale + row * 2 * a.groups + t.nt;
+        s[0] = scale[mi][0];
+        s[a.groups] = scale[mi][1];
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int n = n0 + 8 * (2 * p + hi);
+        const floatx8 g = eight_columns(acc[mi][0], p), u = eight_columns(acc[mi][1], p);   // with all lanes
+        if (n >= a.N) continue;
+        floatx8 h;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = act_of(g[j], a.act) * u[j];
+        R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
+        if (a.z8) {
+          uint8_t* z = static_cast<uint8_t*>(a.z) + row * a.z_stride + n;
+          *reinterpret_cast<uint2*>(z) = codes_of(g, scale[mi][0]);
+          *reinterpret_cast<uint2*>(z + a.N) = codes_of(u, scale[mi][1]);
+        } else if (a.z) {
+          elem* z = static_cast<elem*>(a.z) + row * a.z_stride + n;
+          R::store_once(z, R::narrow(g));
+          R::store_once(z + a.N, R::narrow(u));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const int n = n0 + half * 128 + 8 * (2 * p + hi);
+          floatx8 v = eight_columns(acc[mi][half], p);   // with all lanes
+          if (n >= a.N) continue;
+          if constexpr (EPI == kProductAct) {
+            if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)t.e * a.N + n));
+            if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
+            if (a.act != PW_ACT_NONE)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = act_of(v[j], a.act);
+            if (a.residual)
+              v += R::wide(R::load(static_cast<const elem*>(a.residual) + row * a.residual_stride + n));
+          }
+          if constexpr (EPI == kProductGateGrad) {
+            floatx8 g, u, dg, du, h;
+            if (a.z8) {
+              const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
+              const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
+              g = values_of(*reinterpret_cast<const uint2*>(z), s[0]);
+              u = values_of(*reinterpret_cast<const uint2*>(z + a.N), s[a.groups]);
+            } else {
+              const elem* z = static_cast<const elem*>(a.z) + row * a.z_stride + n;
+              g = R::wide(R::load(z));
+              u = R::wide(R::load(z + a.N));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float s = act_of(g[j], a.act);
+              dg[j] = v[j] * u[j] * act_slope(g[j], a.act);
+              du[j] = v[j] * s;
+              h[j] = s * u[j];
+            }
+            elem* dz = static_cast<elem*>(a.pre) + row * a.pre_stride + n;
+            R::store(dz, R::narrow(dg));
+            R::store(dz + a.N, R::narrow(du));
+            if (a.y) R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
+          } else {
+            R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(v));
+          }
+        }
+    }
+  }
+}
+
+template <int DT, int EPI, int MI, int WM>
+__global__ __launch_bounds__((Shape<MI, WM>::kThreads), 2) void product_kernel(ProductArgs a) {
+  using S = Shape<MI, WM>;
+  constexpr bool kBack = EPI == kProductBack || EPI == kProductGateGrad;
+  __shared__ __align__(1024) char lds[2 * S::kStage];
+  const Tile t = find_tile<S::kRows>(a.offsets, a.E, a.S, a.NT);
+  if (t.rows <= 0) return;
+  const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
+  const int wm = wave / 4, wn = wave % 4;
+  const char* x = static_cast<const char*>(a.x) + (int64_t)t.row0 * a.x_stride * 2;
+  const char* w = static_cast<const char*>(a.w) + (int64_t)t.e * a.w_expert * 2;
+
+  RowsOperand<S::kRows, S::kWaves> xo;
+  RowsOperand<kProdN, S::kWaves> wr;
+  ColsOperand<S::kWaves> wc;
+  xo.init(wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
+  if constexpr (EPI == kProductGate) {
+    const int n0 = t.nt * kKeepGroup, last = a.N - 1 - n0;
+    w += (int64_t)n0 * a.K * 2;
+    const uint32_t up = (uint32_t)a.N * (uint32_t)(a.K * 2);   // below 2^32: 2 N K is below 2^31
+    const uint32_t row_bytes = (uint32_t)a.K * 2u;
+    // u's rows lie N rows behind g's: past the 2^31 bytes that a copy reaches where N K is large, so they have a
+    // resource of their own
+    wr.init(wave, lane, [&](int r) { return (uint32_t)min(r & 127, last) * row_bytes; });
+    (void)up;
+  } else if constexpr (!kBack) {
+    const int n0 = t.nt * kProdN, last = a.N - 1 - n0;
+    w += (int64_t)n0 * a.K * 2;
+    wr.init(wave, lane, [&](int r) { return (uint32_t)min(r, last) * (uint32_t)(a.K * 2); });
+  } else {
+    w += (int64_t)t.nt * kProdN * 2;
+    wc.init(wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
+  }
+  auto stage = [&](int k, char* to) {
+    xo.copy(x, to, wave, lane, k, a.K);
+    if constexpr (EPI == kProductGate) {
+      constexpr int kHalf = RowsOperand<kProdN, S::kWaves>::kCopies / 2;   // the first half of a wave's copies are g's
+      const __amdgpu_buffer_rsrc_t gate = make_rsrc(w, kRsrcBytes), upr = make_rsrc(w + (int64_t)a.N * a.K * 2, kRsrcBytes);
+      const bool in = k + kProdK <= a.K || k + ((lane ^ (lane >> 3)) & 7) * 8 < a.K;
+#pragma unroll
+      for (int i = 0; i < 2 * kHalf; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(i < kHalf ? gate : upr,
+                                                 (lds_void)(to + S::kABytes + (i * S::kWaves + wave) * 1024), 16,
+                                                 (int)(in ? wr.at[i] : kOutOfRange), k * 2, 0, 0);
+    } else if constexpr (!kBack) {
+      wr.copy(w, to + S::kABytes, wave, lane, k, a.K);
+    } else {
+      wc.copy(w + (int64_t)k * a.N * 2, to + S::kABytes, wave, a.K - k);
+    }
+  };
+
+  f32x16 acc[MI][2];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[mi][half][i] = 0.f;
+
+  char* now = lds;
+  char* next = lds + S::kStage;
+  stage(0, now);
+  for (int k = 0; k < a.K; k += kProdK) {
+    step_barrier();
+    if (k + kProdK < a.K) stage(k + kProdK, next);
+#pragma unroll
+    for (int kk = 0; kk < kProdK / 16; ++kk) {
+      s16x8 xf[MI], wf[2];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) xf[mi] = read_rows(now, (wm * MI + mi) * 32, kk, lane);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if constexpr (kBack) wf[half] = read_cols(now + S::kABytes, half * 128 + wn * 32, kk, lane);
+        else wf[half] = read_rows(now + S::kABytes, half * 128 + wn * 32, kk, lane);
+      }
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) acc[mi][half] = Mma<DT>::wide(wf[half], xf[mi], acc[mi][half]);
+    }
+    char* const swap = now;
+    now = next;
+    next = swap;
+  }
+  finish<DT, EPI, MI, WM>(a, t, acc, lds, wm, wn, lane);
+}
+
+template <int DT, int EPI, int MI, int WM>
+hipError_t run(ProductArgs a, hipStream_t s) {
+  using Sh = Shape<MI, WM>;
+  a.NT = EPI == kProductGate ? (a.N + kKeepGroup - 1) / kKeepGroup : (a.N + kProdN - 1) / kProdN;
+  const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, Sh::kRows), a.NT);
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((product_kernel<DT, EPI, MI, WM>), dim3((unsigned)grid), dim3(Sh::kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, int EPI>
+hipError_t pick(const ProductArgs& a, hipStream_t s) {
+  const int64_t experts = a.S < a.E ? a.S : a.E, mean = a.S / (experts > 0 ? experts : 1);
+  if (mean > 160) return run<DT, EPI, 4, 2>(a, s);
+  if (mean > 80) return run<DT, EPI, 2, 2>(a, s);
+  if (mean > 32) return run<DT, EPI, 2, 1>(a, s);
+  return run<DT, EPI, 1, 1>(a, s);
+}
+
+template <int DT>
+hipError_t pick_kind(const ProductArgs& a, int kind, hipStream_t s) {
+  switch (kind) {
+    case kProductAct: return pick<DT, kProductAct>(a, s);
+    case kProductGate: return pick<DT, kProductGate>(a, s);
+    case kProductBack: return pick<DT, kProductBack>(a, s);
+    default: return pick<DT, kProductGateGrad>(a, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_product(const ProductArgs& a, int dtype, int kind, hipStream_t s) {
+  return dtype == PW_F16 ? pick_kind<PW_F16>(a, kind, s) : pick_kind<PW_BF16>(a, kind, s);
+}
+
+}  // namespace pw

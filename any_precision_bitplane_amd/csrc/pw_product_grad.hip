@@ -1,0 +1,182 @@
+// Gradients of the experts' products that run over an expert's rows:
+//
+//   dW[n][k] = sum_s dz[s][n] x[s][k]        dz = dy act'(pre)
+//   dbias[n] = sum_s dz[s][n]
+//
+// The weight's gradient is a product whose reduction runs over the rows, so both
+// operands are transposed on their way from LDS to the matrix cores.  Every
+// block has 256 x 256 values of one expert; rows past the expert's last read as
+// zero in both operands, so what lies behind (NaN too) adds nothing.
+#include "pw_product.h"
+
+namespace pw {
+
+namespace {
+
+constexpr int kOuterWaves = 8;
+constexpr int kOuterStage = 2 * kProdK * 512;
+
+template <int DT>
+__global__ __launch_bounds__(kOuterWaves * kWave, 2) void outer_kernel(OuterArgs a) {
+  using R = Row<DT>;
+  using elem = typename R::elem;
+  constexpr int MI = 4;
+  __shared__ __align__(1024) char lds[2 * kOuterStage];
+  const unsigned each = (a.tiles + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each + i;
+  if (i >= each || id >= a.tiles) return;
+  const unsigned per = (unsigned)(a.MT * a.NT);
+  const int e = (int)(id / per), local = (int)(id - e * per);
+  const int group = local / (kProdGroup * a.NT), rem = local - group * kProdGroup * a.NT;
+  const int here = min(kProdGroup, a.MT - group * kProdGroup);
+  const int nt = rem / here, mt = group * kProdGroup + rem - nt * here;
+  int row0, rows;
+  expert_rows(a.offsets, e, a.S, row0, rows);
+  row0 = uniform(row0);
+  rows = uniform(rows);
+  const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
+  const int wm = wave / 4, wn = wave % 4, hi = lane / 32;
+  const char* p = static_cast<const char*>(a.p) + ((int64_t)row0 * a.p_stride + mt * 256) * 2;
+  const char* q = static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * 256) * 2;
+  ColsOperand<kOuterWaves> po, qo;
+  po.init(wave, lane, a.p_stride * 2, (a.M - mt * 256 + 7) / 8);
+  qo.init(wave, lane, a.q_stride * 2, (a.N - nt * 256 + 7) / 8);
+  auto stage = [&](int k, char* to) {
+    po.copy(p + (int64_t)k * a.p_stride * 2, to, wave, rows - k);
+    qo.copy(q + (int64_t)k * a.q_stride * 2, to + kProdK * 512, wave, rows - k);
+  };
+  f32x16 acc[MI][2];
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[mi][half][j] = 0.f;
+  char* now = lds;
+  char* next = lds + kOuterStage;
+  if (rows > 0) stage(0, now);
+  for (int k = 0; k < rows; k += kProdK) {
+    step_barrier();
+    if (k + kProdK < rows) stage(k + kProdK, next);
+#pragma unroll
+    for (int kk = 0; kk < kProdK / 16; ++kk) {
+      s16x8 pf[MI], qf[2];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) pf[mi] = read_cols(now, (wm * MI + mi) * 32, kk, lane);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) qf[half] = read_cols(now + kProdK * 512, half * 128 + wn * 32, kk, lane);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) acc[mi][half] = Mma<DT>::wide(qf[half], pf[mi], acc[mi][half]);
+    }
+    char* const swap = now;
+    now = next;
+    next = swap;
+  }
+  elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi) {
+    const int m = mt * 256 + (wm * MI + mi) * 32 + (lane & 31);
+    if (m >= a.M) continue;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int n = nt * 256 + half * 128 + wn * 32 + 8 * (2 * c + hi);
+        const floatx8 v = eight_columns(acc[mi][half], c);   // with all lanes
+        if (n < a.N) R::store(out + (int64_t)m * a.N + n, R::narrow(v));
+      }
+  }
+}
+
+// dz and the columns' sums of stretches of kDzRows rows of one expert: a block
+// has 256 columns, a wave two rows at a time.
+constexpr int kDzRows = 128;
+constexpr int kDzThreads = 256;
+
+template <int DT>
+__global__ __launch_bounds__(kDzThreads) void dz_kernel(DzArgs a) {
+  using R = Row<DT>;
+  using elem = typename R::elem;
+  __shared__ float part[kDzThreads / 32][256];
+  const Tile t = find_tile<kDzRows>(a.offsets, a.E, a.S, (a.N + 255) / 256);
+  if (t.rows <= 0) return;
+  const int lane = threadIdx.x & 31, own = threadIdx.x / 32;
+  const int n = t.nt * 256 + lane * 8;
+  floatx8 sum = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (n < a.N) {
+    const int rows = min(t.rows, kDzRows);
+    for (int r = own; r < rows; r += kDzThreads / 32) {
+      const int64_t row = t.row0 + r;
+      floatx8 d = R::wide(R::load(static_cast<const elem*>(a.dy) + row * a.dy_stride + n));
+      if (a.act != PW_ACT_NONE) {
+        const floatx8 z = R::wide(R::load(static_cast<const elem*>(a.pre) + row * a.pre_stride + n));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] *= act_slope(z[j], a.act);
+        if (a.dz) R::store(static_cast<elem*>(a.dz) + row * a.N + n, R::narrow(d));
+      }
+      sum += d;
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[own][lane * 8 + j] = sum[j];
+  __syncthreads();
+  const int c = t.nt * 256 + (int)threadIdx.x;
+  if (c >= a.N) return;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kDzThreads / 32; ++i) s += part[i][threadIdx.x];
+  // an expert's first stretch lies behind those of the experts before it
+  a.part[((int64_t)t.row0 / kDzRows + t.e) * a.N + c] = s;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kDzThreads) void bias_grad_kernel(DzArgs a) {
+  using elem = typename RowType<DT>::elem;
+  const int c = (int)(blockIdx.x * kDzThreads + threadIdx.x), e = (int)blockIdx.y;
+  if (c >= a.N) return;
+  int row0, rows;
+  expert_rows(a.offsets, e, a.S, row0, rows);
+  float s = 0.f;
+  for (int r = 0; r < rows; r += kDzRows) s += a.part[((int64_t)(row0 + r) / kDzRows + e) * a.N + c];
+  static_cast<elem*>(a.dbias)[(int64_t)e * a.N + c] = (elem)s;
+}
+
+template <int DT>
+hipError_t run_outer(OuterArgs a, hipStream_t s) {
+  a.MT = (a.M + 255) / 256;
+  a.NT = (a.N + 255) / 256;
+  const int64_t tiles = (int64_t)a.E * a.MT * a.NT;
+  if (tiles > 0x7FFFFFF0) return hipErrorInvalidValue;
+  a.tiles = (unsigned)tiles;
+  hipLaunchKernelGGL(outer_kernel<DT>, dim3((unsigned)product_grid(tiles, 1)), dim3(kOuterWaves * kWave), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run_dz(const DzArgs& a, hipStream_t s) {
+  if (a.S > 0) {
+    const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, kDzRows), (a.N + 255) / 256);
+    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(dz_kernel<DT>, dim3((unsigned)grid), dim3(kDzThreads), 0, s, a);
+  }
+  if (a.dbias)
+    hipLaunchKernelGGL(bias_grad_kernel<DT>, dim3((unsigned)((a.N + kDzThreads - 1) / kDzThreads), (unsigned)a.E),
+                       dim3(kDzThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t dz_part_floats(int E, int64_t S, int N) { return (size_t)(S / kDzRows + E) * (size_t)N; }
+
+hipError_t launch_outer(const OuterArgs& a, int dtype, hipStream_t s) {
+  return dtype == PW_F16 ? run_outer<PW_F16>(a, s) : run_outer<PW_BF16>(a, s);
+}
+
+hipError_t launch_dz(const DzArgs& a, int dtype, hipStream_t s) {
+  return dtype == PW_F16 ? run_dz<PW_F16>(a, s) : run_dz<PW_BF16>(a, s);
+}
+
+}  // namespace pw

@@ -487,6 +487,113 @@ pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, co
                              const uint16_t* dx_add, uint16_t* dx, float* drouter_w, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert products in 16 bits: what stands between pw_moe_permute and
+ * pw_moe_unpermute where the experts' matrices are fp16 or bf16 ones (experts
+ * that are trained or calibrated, a shared expert, projections), and the
+ * gradients.  Rows, strides, alignment, overlap, determinism, graphs and
+ * workspaces are as stated above; dtype is PW_F16 or PW_BF16 and holds for
+ * every matrix, bias and gradient of a call but where a type is named.
+ *
+ *   S, offsets  S rows, of which expert e has [offsets[e], offsets[e+1])
+ *               (device int32 [E+1], as pw_moe_permute wrote them; entries
+ *               outside [0, S] count as the nearer end).  Rows from offsets[E]
+ *               on are not read and stay as they were in every output.  NULL:
+ *               one expert (E = 1) with all S rows.
+ *   Matrices and biases of the experts follow each other without gaps, 16-byte
+ *   aligned.  E is 1..256, sizes of rows are as each call says, and a row
+ *   stride is below 2^22 elements (else PW_ERR_UNSUPPORTED_SHAPE).
+ *
+ * Sums are fp32; an output is rounded once.  Between two products of one call
+ * (h, and gradients of gate and up or of the product's sum) values are rounded
+ * to dtype, as the matrix cores take them.
+ *
+ * Activations: act(z) = z, z / (1 + exp(-z)), or z Phi(z) with the normal
+ * distribution function Phi(z) = (1 + erf(z / sqrt 2)) / 2.
+ * ---------------------------------------------------------------------- */
+#define PW_ACT_NONE 0
+#define PW_ACT_SILU 1
+#define PW_ACT_GELU 2
+
+/* Workspace of pw_moe_product and of pw_moe_product_backward for up to S_max
+ * rows (0 on a bad size). */
+size_t pw_moe_product_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K);
+size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K);
+
+/* Product with bias, activation and residual:
+ *     z[s] = w[e] x[s] + bias[e],   y[s] = act(z[s]) + residual[s]
+ *   N, K      multiples of 8, at most 2^22, N K at most 2^30
+ *   x         [S][K];  w  [E][N][K];  bias  [E][N] or NULL
+ *   act       PW_ACT_*
+ *   residual  [S][N] or NULL; may be y itself (same pointer and stride)
+ *   pre       [S][N] or NULL: receives z for the gradient
+ *   y         [S][N], overwritten
+ * S == 0 returns PW_OK and enqueues nothing. */
+pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* x, int64_t x_stride,
+                         const int32_t* offsets, const void* w, const void* bias, int32_t act, const void* residual,
+                         int64_t residual_stride, void* pre, int64_t pre_stride, void* y, int64_t y_stride,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of pw_moe_product (the residual's is dy itself):
+ *     dz = dy act'(pre),  dx = dz w[e],  dw[e] = sum_s dz[s] x[s]^T,  dbias[e] = sum_s dz[s]
+ *   dy     [S][N];  pre  [S][N] as the forward wrote it, NULL with PW_ACT_NONE
+ *   dx     [S][K] or NULL: not wanted (w may be NULL then)
+ *   dw     [E][N][K], zero for an expert without rows, or NULL: not wanted (x
+ *          may be NULL then)
+ *   dbias  [E][N], the same, or NULL
+ * S == 0 sets dw and dbias to zero. */
+pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* dy,
+                                  int64_t dy_stride, const void* x, int64_t x_stride, const int32_t* offsets,
+                                  const void* w, int32_t act, const void* pre, int64_t pre_stride, void* dx,
+                                  int64_t dx_stride, void* dw, void* dbias, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Workspace of pw_moe_ffn and of pw_moe_ffn_backward for up to S_max rows (0 on
+ * a bad shape). */
+size_t pw_moe_ffn_workspace_bytes(const pw_moe_shape* shape /* host */, int32_t S_max);
+size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape /* host */, int32_t S_max);
+
+/* Gated feed-forward block of every expert over its rows:
+ *     [gate | up] = w_gate_up[e] x[s],   h = act(gate) * up,   y[s] = w_down[e] h
+ * (the expert product of pw_moe_forward with matrices of 16 bits and without
+ * the routing weights, which pw_moe_unpermute applies).
+ *   shape      host; hidden H, inter I and num_experts are used
+ *   x          [S][H];  w_gate_up  [E][2I][H], gate rows first;  w_down  [E][H][I]
+ *   act        PW_ACT_SILU or PW_ACT_GELU
+ *   z          NULL, or the gradient's checkpoint [S][2I]: gate and up in
+ *              z_dtype, which is dtype or PW_E4M3 (8 bits; the row stride and
+ *              the first row are then 16-byte aligned too).  In 8 bits
+ *                  value = code * scale,
+ *                  scale = max(largest |value| of the group / 448, 2^-100),
+ *              a group being 128 columns of gate or of up (the last of each
+ *              may have fewer), and
+ *   z_scale    fp32 [S][2 G], G = ceil(I / 128): the scales of gate's groups,
+ *              then those of up's.  A group with a NaN or an infinity gets the
+ *              scale NaN and NaN codes.  NULL otherwise.
+ *              y comes from the unrounded gate and up in either case.
+ *   y          [S][H], overwritten
+ * Two launches.  S == 0 returns PW_OK and enqueues nothing. */
+pw_status pw_moe_ffn(const pw_moe_shape* shape /* host */, int32_t S, int32_t dtype, const void* x, int64_t x_stride,
+                     const int32_t* offsets, const void* w_gate_up, const void* w_down, int32_t act, int32_t z_dtype,
+                     void* z, int64_t z_stride, float* z_scale, void* y, int64_t y_stride, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Gradient of pw_moe_ffn, from the checkpoint z (its values, where it is 8-bit):
+ *     dh = w_down[e]^T dy,   dgate = dh up act'(gate),   dup = dh act(gate)
+ *     dx = w_gate_up[e]^T [dgate | dup]
+ *     dw_gate_up[e] = sum_s [dgate | dup][s] x[s]^T,   dw_down[e] = sum_s dy[s] h[s]^T
+ *   dx         [S][H] or NULL: not wanted
+ *   dw_gate_up [E][2I][H], zero for an expert without rows, or NULL: not wanted
+ *              (x may be NULL then)
+ *   dw_down    [E][H][I], the same, or NULL
+ *   w_gate_up  may be NULL without dx
+ * Up to four launches.  S == 0 sets dw_gate_up and dw_down to zero. */
+pw_status pw_moe_ffn_backward(const pw_moe_shape* shape /* host */, int32_t S, int32_t dtype, const void* dy,
+                              int64_t dy_stride, const void* x, int64_t x_stride, const int32_t* offsets,
+                              const void* w_gate_up, const void* w_down, int32_t act, int32_t z_dtype, const void* z,
+                              int64_t z_stride, const float* z_scale, void* dx, int64_t dx_stride, void* dw_gate_up,
+                              void* dw_down, void* workspace, size_t workspace_bytes, void* stream);
+
 /* The routed half of a transformer block: norm, router and layer in one call,
  *     residual += x;   y = layer(pw_rmsnorm(residual))
  * The next norm's residual addition adds y.  Equal bit for bit to pw_rmsnorm

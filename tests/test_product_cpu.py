@@ -1,0 +1,121 @@
+"""The expert products refuse bad arguments on the host, before any launch: C
+entry points by made-up pointers, the binding by tensors that are not on a GPU.
+No GPU needed."""
+import ctypes
+import os
+
+import pytest
+
+from any_precision_bitplane_amd import binding as B
+
+P = 1 << 20     # a made-up aligned address: every call below ends before it is used
+HUGE = 1 << 60
+BAD, SHAPE, ALIGN = B.PW_ERR_INVALID_ARG, B.PW_ERR_UNSUPPORTED_SHAPE, B.PW_ERR_ALIGNMENT
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        pytest.fail("libpagedweight.so is not built (python -m any_precision_bitplane_amd.build)")
+    return B.load()
+
+
+def test_product_refusals(lib):
+    def call(E=3, S=4, N=64, K=72, dt=B.PW_F16, x=P, xs=72, off=P, w=P, bias=None, act=0, res=None, rs=64, pre=None, ps=64,
+             y=P, ys=64, ws=P, n=HUGE):
+        return lib.pw_moe_product(E, S, N, K, dt, x, xs, off, w, bias, act, res, rs, pre, ps, y, ys, ws, n, None)
+
+    assert call(S=0) == B.PW_OK and call(S=0, x=None, y=None, w=None) == B.PW_OK
+    assert call(E=0) == BAD and call(S=-1) == BAD and call(N=0) == BAD and call(K=-8) == BAD
+    assert call(E=257) == SHAPE and call(N=60) == SHAPE and call(K=68) == SHAPE
+    assert call(N=1 << 23) == SHAPE and call(K=1 << 23) == SHAPE and call(N=1 << 16, K=1 << 15) == SHAPE
+    assert call(xs=1 << 22) == SHAPE and call(ys=1 << 22) == SHAPE
+    assert call(dt=B.PW_F32) == BAD and call(dt=B.PW_E4M3) == BAD and call(dt=9) == BAD
+    assert call(act=3) == BAD and call(act=-1) == BAD
+    assert call(off=None) == BAD and call(off=P + 2) == ALIGN
+    for name in ("x", "w", "y", "ws"):
+        assert call(**{name: None}) == BAD, name
+    assert call(xs=-72) == BAD and call(ys=56) == BAD and call(pre=P, ps=56) == BAD
+    assert call(x=P + 8) == ALIGN and call(w=P + 8) == ALIGN and call(bias=P + 8) == ALIGN and call(y=P + 8) == ALIGN
+    assert call(xs=76) == ALIGN and call(res=P, rs=65) == ALIGN and call(pre=P + 2) == ALIGN and call(ws=P + 16) == ALIGN
+    need = B.pw_moe_product_workspace_bytes(3, 4, 64, 72)
+    assert need > 0 and call(n=need - 1) == B.PW_ERR_WORKSPACE
+    assert B.pw_moe_product_workspace_bytes(3, 4, 60, 72) == 0 and B.pw_moe_product_workspace_bytes(0, 4, 64, 72) == 0
+
+
+def test_product_backward_refusals(lib):
+    def call(E=3, S=4, N=64, K=72, dt=B.PW_BF16, dy=P, dys=64, x=P, xs=72, off=P, w=P, act=0, pre=None, ps=64, dx=P,
+             dxs=72, dw=P, db=P, ws=P, n=HUGE):
+        return lib.pw_moe_product_backward(E, S, N, K, dt, dy, dys, x, xs, off, w, act, pre, ps, dx, dxs, dw, db, ws, n,
+                                           None)
+
+    assert call(S=0, dw=None, db=None) == B.PW_OK
+    assert call(S=-1) == BAD and call(N=4) == SHAPE and call(dt=B.PW_F32) == BAD and call(off=None) == BAD
+    assert call(act=1) == BAD and call(pre=P) == BAD            # the slope needs the sum, and nothing else does
+    assert call(dy=None) == BAD and call(w=None) == BAD and call(x=None) == BAD and call(ws=None) == BAD
+    assert call(dxs=64) == BAD and call(dxs=76) == ALIGN and call(dys=1 << 22) == SHAPE
+    assert call(dw=P + 4) == ALIGN and call(db=P + 2) == ALIGN and call(act=2, pre=P + 8) == ALIGN
+    need = B.pw_moe_product_backward_workspace_bytes(3, 4, 64, 72)
+    assert need >= 4 * 64 * 2 and call(n=need - 1) == B.PW_ERR_WORKSPACE
+    assert B.pw_moe_product_backward_workspace_bytes(3, -4, 64, 72) == 0
+
+
+def test_ffn_refusals(lib):
+    shp = B.shape(64, 96, 3, 2)
+
+    def call(shape=shp, S=4, dt=B.PW_F16, x=P, xs=64, off=P, wg=P, wd=P, act=1, zt=B.PW_F16, z=None, zs=192, sc=None, y=P,
+             ys=64, ws=P, n=HUGE):
+        return lib.pw_moe_ffn(ctypes.byref(shape), S, dt, x, xs, off, wg, wd, act, zt, z, zs, sc, y, ys, ws, n, None)
+
+    assert call(S=0) == B.PW_OK and call(S=-1) == BAD
+    assert call(shape=B.shape(60, 96, 3, 2)) == SHAPE and call(shape=B.shape(64, 96, 300, 2)) == SHAPE
+    assert call(dt=B.PW_F32) == BAD and call(act=0) == BAD and call(act=3) == BAD and call(off=None) == BAD
+    for name in ("x", "wg", "wd", "y", "ws"):
+        assert call(**{name: None}) == BAD, name
+    assert call(sc=P) == BAD and call(z=P, sc=P) == BAD and call(z=P, zt=B.PW_BF16) == BAD
+    assert call(z=P, zt=B.PW_E4M3) == BAD and call(z=P, zt=B.PW_E4M3, sc=P + 2) == ALIGN
+    assert call(z=P, zs=184) == BAD and call(z=P, zt=B.PW_E4M3, sc=P, zs=200) == ALIGN and call(z=P + 4) == ALIGN
+    assert call(xs=68) == ALIGN and call(ys=32) == BAD and call(wd=P + 2) == ALIGN and call(ws=P + 8) == ALIGN
+    need = B.pw_moe_ffn_workspace_bytes(shp, 4)
+    assert need >= 4 * 96 * 2 and call(n=need - 1) == B.PW_ERR_WORKSPACE
+    assert B.pw_moe_ffn_workspace_bytes(B.shape(60, 96, 3, 2), 4) == 0
+
+
+def test_ffn_backward_refusals(lib):
+    shp = B.shape(64, 96, 3, 2)
+
+    def call(shape=shp, S=4, dt=B.PW_F16, dy=P, dys=64, x=P, xs=64, off=P, wg=P, wd=P, act=1, zt=B.PW_F16, z=P, zs=192,
+             sc=None, dx=P, dxs=64, dg=P, dd=P, ws=P, n=HUGE):
+        return lib.pw_moe_ffn_backward(ctypes.byref(shape), S, dt, dy, dys, x, xs, off, wg, wd, act, zt, z, zs, sc, dx, dxs,
+                                       dg, dd, ws, n, None)
+
+    assert call(S=0, dg=None, dd=None) == B.PW_OK and call(S=-1) == BAD
+    assert call(dt=B.PW_E4M3) == BAD and call(act=0) == BAD and call(off=None) == BAD
+    for name in ("dy", "x", "wg", "wd", "z", "ws"):
+        assert call(**{name: None}) == BAD, name
+    assert call(zt=B.PW_E4M3) == BAD and call(sc=P) == BAD and call(zt=B.PW_BF16) == BAD
+    assert call(zs=190) == ALIGN and call(zt=B.PW_E4M3, sc=P, zs=200) == ALIGN
+    assert call(dxs=60) == BAD and call(dg=P + 2) == ALIGN and call(dd=P + 8) == ALIGN and call(dys=68) == ALIGN
+    need = B.pw_moe_ffn_backward_workspace_bytes(shp, 4)
+    assert need >= 4 * 3 * 96 * 2 and call(n=need - 1) == B.PW_ERR_WORKSPACE
+
+
+def test_workspaces_grow_with_rows(lib):
+    shp = B.shape(2048, 1408, 60, 4)
+    for size in (lambda S: B.pw_moe_ffn_workspace_bytes(shp, S), lambda S: B.pw_moe_ffn_backward_workspace_bytes(shp, S),
+                 lambda S: B.pw_moe_product_workspace_bytes(8, S, 4096, 2048),
+                 lambda S: B.pw_moe_product_backward_workspace_bytes(8, S, 4096, 2048)):
+        sizes = [size(S) for S in list(range(0, 700)) + [1000, 4095, 4096, 100000, 1 << 24]]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])) and all(s % 256 == 0 and s > 0 for s in sizes)
+
+
+def test_binding_refuses_tensors_that_are_on_no_gpu():
+    import torch
+    x, w = torch.zeros((4, 64), dtype=torch.float16), torch.zeros((1, 64, 64), dtype=torch.float16)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(B.PwError):
+        B.pw_moe_product(1, 4, 64, 64, x, w, x, ws)
+    with pytest.raises(B.PwError):
+        B.pw_moe_product_backward(1, 4, 64, 64, x, x, w, ws, dx=x)
+    assert B.pw_moe_ffn(B.shape(64, 64, 1, 1), 4, None, w, w, x, ws, check=False) == BAD
+    assert B.pw_moe_ffn_backward(B.shape(64, 64, 1, 1), 4, x, x, w, w, x, ws, check=False) == BAD
