@@ -6,8 +6,8 @@
 // the reduction in steps of 64.  A step's operands are copied from memory to LDS
 // without passing registers, one step ahead of the products, in two buffers.
 // An operand whose reduction index is contiguous in memory lies in LDS as rows
-// of 64 (eight 16-byte pieces, piece c of row r at place c ^ (r & 7), so that
-// the eight rows of a read fall on different banks); one whose other index is
+// of 64 (eight 16-byte pieces, piece c of row r at place c ^ (r / 2 & 7), so that
+// sixteen rows' pieces fall on different banks); one whose other index is
 // contiguous lies as it is and is transposed by the reads.
 #pragma once
 
@@ -127,27 +127,47 @@ inline int64_t product_grid(int64_t row_tiles, int64_t NT) { return (row_tiles *
 
 // ----- a tile's operands ------------------------------------------------------
 
+// 16 bytes a lane from memory to LDS: lane l's land at `to` + 16 l.  Offsets from
+// 2^31 on read as zero.  The compiler does not see that the copy writes LDS:
+// what reads it stands behind a step's barrier, which waits for the copies (with
+// the builtin it waits for every copy before each transposing read).
+typedef uint32_t rsrc_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ rsrc_t copy_rsrc(const void* base) {
+  const uint64_t p = (uint64_t)base;
+  return rsrc_t{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, kRsrcBytes, 0x00020000u};
+}
+__device__ __forceinline__ void copy16(rsrc_t rs, uint32_t to, uint32_t at, uint32_t more) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :
+               : "s"(to), "v"(at), "s"(rs), "s"(more)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
 // Where the lanes of a wave fetch their 16-byte pieces of a tile of R rows of 64
 // (reduction contiguous).  at[i]: byte offset of the lane's piece of copy i.
 template <int R, int WAVES>
 struct RowsOperand {
   static constexpr int kCopies = R / 8 / WAVES;
   uint32_t at[kCopies];
-  // A copy of a wave covers eight rows: lane l fetches row l / 8, piece (l ^ row) & 7.
+  int piece;
+  // A copy of a wave covers eight rows: lane l fetches row l / 8.
   template <class RowOffset>
   __device__ __forceinline__ void init(int wave, int lane, RowOffset offset_of) {
+    piece = (lane & 7) ^ (lane / 16 + 4 * (wave & 1));
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      at[i] = offset_of((i * WAVES + wave) * 8 + lane / 8) + (uint32_t)(((lane ^ (lane >> 3)) & 7) * 16);
+    for (int i = 0; i < kCopies; ++i) at[i] = offset_of((i * WAVES + wave) * 8 + lane / 8) + (uint32_t)(piece * 16);
   }
-  __device__ __forceinline__ void copy(const char* base, char* lds, int wave, int lane, int k, int K) const {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, kRsrcBytes);
-    const bool whole = k + kProdK <= K;
-    const bool in = whole || k + ((lane ^ (lane >> 3)) & 7) * 8 < K;   // past the end reads zero
+  // Copies FROM .. TO - 1 of the step from reduction index k on; past the end, K, reads zero.
+  template <int FROM = 0, int TO = kCopies>
+  __device__ __forceinline__ void copy(const char* base, uint32_t to, int wave, int k, int K) const {
+    const rsrc_t rs = copy_rsrc(base);
+    const bool in = k + piece * 8 < K;
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void)(lds + (i * WAVES + wave) * 1024), 16,
-                                               (int)(in ? at[i] : kOutOfRange), k * 2, 0, 0);
+    for (int i = FROM; i < TO; ++i)
+      copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, in ? at[i] : kOutOfRange, (uint32_t)k * 2u);
   }
 };
 
@@ -157,29 +177,29 @@ template <int WAVES>
 struct ColsOperand {
   static constexpr int kCopies = 32 / WAVES;
   uint32_t at[kCopies];
-  int row[kCopies];
+  int first;
   // A copy of a wave covers two rows: lane l fetches row l / 32.  Columns past the matrix are read from its last piece.
   __device__ __forceinline__ void init(int wave, int lane, int64_t row_bytes, int pieces) {
+    first = wave * 2 + lane / 32;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-      row[i] = (i * WAVES + wave) * 2 + lane / 32;
-      at[i] = (uint32_t)(row[i] * row_bytes) + (uint32_t)(min((lane & 31) ^ cols_place(row[i]), pieces - 1) * 16);
+      const int row = first + i * WAVES * 2;
+      at[i] = (uint32_t)(row * row_bytes) + (uint32_t)(min((lane & 31) ^ cols_place(row), pieces - 1) * 16);
     }
   }
   // base: the first of the step's rows; left: reduction rows from there on
-  __device__ __forceinline__ void copy(const char* base, char* lds, int wave, int left) const {
-    const __amdgpu_buffer_rsrc_t rs = make_rsrc(base, kRsrcBytes);
+  __device__ __forceinline__ void copy(const char* base, uint32_t to, int wave, int left) const {
+    const rsrc_t rs = copy_rsrc(base);
 #pragma unroll
     for (int i = 0; i < kCopies; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void)(lds + (i * WAVES + wave) * 1024), 16,
-                                               (int)(row[i] < left ? at[i] : kOutOfRange), 0, 0, 0);
+      copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, first + i * WAVES * 2 < left ? at[i] : kOutOfRange, 0u);
   }
 };
 
 // Operand of 32 rows (or columns) from `r0` on for the sixteen reduction steps
 // from 16 kk on: lane l holds row l % 32, steps 8 (l / 32) .. + 7.
 __device__ __forceinline__ s16x8 read_rows(const char* lds, int r0, int kk, int lane) {
-  const int r = lane & 31, piece = (2 * kk + lane / 32) ^ (r & 7);
+  const int r = lane & 31, piece = (2 * kk + lane / 32) ^ (r / 2 & 7);
   return *reinterpret_cast<const s16x8*>(lds + (r0 + r) * 128 + piece * 16);
 }
 // The transposing read gives lane i of sixteen column i of four rows of sixteen
@@ -194,9 +214,69 @@ __device__ __forceinline__ s16x8 read_cols(const char* lds, int c0, int kk, int 
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Every wave's copies have landed and every wave is done with the other buffer.
+// Every wave's copies have landed and every wave has read its operands.
 __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Sums of a wave's MI x 2 pieces of 32 x 32 over `steps` steps of 64.  XC, WC:
+// the operand of the rows, of the columns, is read transposed.  stage(t, to)
+// copies step t to LDS at `to`.
+//
+// The operands of sixteen reduction steps are read from LDS while the products
+// of the sixteen before run.  With the last of a step's operands in registers
+// its buffer is free: behind the barrier the copies of the step after the next
+// are started, and the next step's first operands are read, under the products
+// that are left.
+template <int DT, int MI, bool XC, bool WC, int STAGE, class Copy>
+__device__ __forceinline__ void sum_steps(f32x16 (&acc)[MI][2], char* lds, int w_at, int steps, int wm, int wn, int lane,
+                                          Copy stage) {
+#pragma unroll
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[mi][half][i] = 0.f;
+  const uint32_t base = lds_at(lds);
+  s16x8 x[2][MI], w[2][2];
+  auto read = [&](const char* at, int kk, s16x8 (&xf)[MI], s16x8 (&wf)[2]) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int c = half * 128 + wn * 32;
+      wf[half] = WC ? read_cols(at + w_at, c, kk, lane) : read_rows(at + w_at, c, kk, lane);
+    }
+#pragma unroll
+    for (int mi = 0; mi < MI; ++mi) {
+      const int r = (wm * MI + mi) * 32;
+      xf[mi] = XC ? read_cols(at, r, kk, lane) : read_rows(at, r, kk, lane);
+    }
+  };
+  if (steps <= 0) return;
+  stage(0, base);
+  step_barrier();
+  if (steps > 1) stage(1, base + STAGE);
+  read(lds, 0, x[0], w[0]);
+  for (int t = 0; t < steps; ++t) {
+    const char* now = lds + (t & 1) * STAGE;
+    const char* next = lds + (~t & 1) * STAGE;
+#pragma unroll
+    for (int kk = 0; kk < kProdK / 16; ++kk) {
+      const int a = kk & 1, b = a ^ 1;
+      if (kk < kProdK / 16 - 1) {
+        read(now, kk + 1, x[b], w[b]);
+      } else if (t + 1 < steps) {
+        step_barrier();
+        if (t + 2 < steps) stage(t + 2, base + (uint32_t)(t & 1) * STAGE);
+        read(next, 0, x[b], w[b]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) acc[mi][half] = Mma<DT>::wide(w[a][half], x[a][mi], acc[mi][half]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
 }
 
 // ----- activations ------------------------------------------------------------

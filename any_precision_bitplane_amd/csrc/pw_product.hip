@@ -152,74 +152,31 @@ __global__ __launch_bounds__((Shape<MI, WM>::kThreads), 2) void product_kernel(P
   RowsOperand<kProdN, S::kWaves> wr;
   ColsOperand<S::kWaves> wc;
   xo.init(wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
-  if constexpr (EPI == kProductGate) {
-    const int n0 = t.nt * kKeepGroup, last = a.N - 1 - n0;
-    w += (int64_t)n0 * a.K * 2;
-    const uint32_t up = (uint32_t)a.N * (uint32_t)(a.K * 2);   // below 2^32: 2 N K is below 2^31
-    const uint32_t row_bytes = (uint32_t)a.K * 2u;
-    // u's rows lie N rows behind g's: past the 2^31 bytes that a copy reaches where N K is large, so they have a
-    // resource of their own
-    wr.init(wave, lane, [&](int r) { return (uint32_t)min(r & 127, last) * row_bytes; });
-    (void)up;
-  } else if constexpr (!kBack) {
-    const int n0 = t.nt * kProdN, last = a.N - 1 - n0;
-    w += (int64_t)n0 * a.K * 2;
-    wr.init(wave, lane, [&](int r) { return (uint32_t)min(r, last) * (uint32_t)(a.K * 2); });
-  } else {
+  if constexpr (kBack) {
     w += (int64_t)t.nt * kProdN * 2;
     wc.init(wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
+  } else {
+    // gated: rows of g, then the same rows of u, which have a base of their own
+    constexpr int kTile = EPI == kProductGate ? kKeepGroup : kProdN;
+    const int n0 = t.nt * kTile, last = a.N - 1 - n0;
+    w += (int64_t)n0 * a.K * 2;
+    wr.init(wave, lane, [&](int r) { return (uint32_t)min(r & (kTile - 1), last) * (uint32_t)(a.K * 2); });
   }
-  auto stage = [&](int k, char* to) {
-    xo.copy(x, to, wave, lane, k, a.K);
-    if constexpr (EPI == kProductGate) {
-      constexpr int kHalf = RowsOperand<kProdN, S::kWaves>::kCopies / 2;   // the first half of a wave's copies are g's
-      const __amdgpu_buffer_rsrc_t gate = make_rsrc(w, kRsrcBytes), upr = make_rsrc(w + (int64_t)a.N * a.K * 2, kRsrcBytes);
-      const bool in = k + kProdK <= a.K || k + ((lane ^ (lane >> 3)) & 7) * 8 < a.K;
-#pragma unroll
-      for (int i = 0; i < 2 * kHalf; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(i < kHalf ? gate : upr,
-                                                 (lds_void)(to + S::kABytes + (i * S::kWaves + wave) * 1024), 16,
-                                                 (int)(in ? wr.at[i] : kOutOfRange), k * 2, 0, 0);
-    } else if constexpr (!kBack) {
-      wr.copy(w, to + S::kABytes, wave, lane, k, a.K);
-    } else {
-      wc.copy(w + (int64_t)k * a.N * 2, to + S::kABytes, wave, a.K - k);
-    }
-  };
-
   f32x16 acc[MI][2];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[mi][half][i] = 0.f;
-
-  char* now = lds;
-  char* next = lds + S::kStage;
-  stage(0, now);
-  for (int k = 0; k < a.K; k += kProdK) {
-    step_barrier();
-    if (k + kProdK < a.K) stage(k + kProdK, next);
-#pragma unroll
-    for (int kk = 0; kk < kProdK / 16; ++kk) {
-      s16x8 xf[MI], wf[2];
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) xf[mi] = read_rows(now, (wm * MI + mi) * 32, kk, lane);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if constexpr (kBack) wf[half] = read_cols(now + S::kABytes, half * 128 + wn * 32, kk, lane);
-        else wf[half] = read_rows(now + S::kABytes, half * 128 + wn * 32, kk, lane);
-      }
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) acc[mi][half] = Mma<DT>::wide(wf[half], xf[mi], acc[mi][half]);
+  sum_steps<DT, MI, false, kBack, S::kStage>(acc, lds, S::kABytes, (a.K + kProdK - 1) / kProdK, wm, wn, lane,
+                                             [&](int step, uint32_t to) {
+    const int k = step * kProdK;
+    xo.copy(x, to, wave, k, a.K);
+    if constexpr (kBack) {
+      wc.copy(w + (int64_t)k * a.N * 2, to + S::kABytes, wave, a.K - k);
+    } else if constexpr (EPI == kProductGate) {
+      constexpr int kHalf = RowsOperand<kProdN, S::kWaves>::kCopies / 2;
+      wr.template copy<0, kHalf>(w, to + S::kABytes, wave, k, a.K);
+      wr.template copy<kHalf, 2 * kHalf>(w + (int64_t)a.N * a.K * 2, to + S::kABytes, wave, k, a.K);
+    } else {
+      wr.copy(w, to + S::kABytes, wave, k, a.K);
     }
-    char* const swap = now;
-    now = next;
-    next = swap;
-  }
+  });
   finish<DT, EPI, MI, WM>(a, t, acc, lds, wm, wn, lane);
 }
 

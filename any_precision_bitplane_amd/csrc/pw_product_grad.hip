@@ -40,39 +40,13 @@ __global__ __launch_bounds__(kOuterWaves * kWave, 2) void outer_kernel(OuterArgs
   ColsOperand<kOuterWaves> po, qo;
   po.init(wave, lane, a.p_stride * 2, (a.M - mt * 256 + 7) / 8);
   qo.init(wave, lane, a.q_stride * 2, (a.N - nt * 256 + 7) / 8);
-  auto stage = [&](int k, char* to) {
+  f32x16 acc[MI][2];
+  sum_steps<DT, MI, true, true, kOuterStage>(acc, lds, kProdK * 512, (rows + kProdK - 1) / kProdK, wm, wn, lane,
+                                             [&](int step, uint32_t to) {
+    const int k = step * kProdK;
     po.copy(p + (int64_t)k * a.p_stride * 2, to, wave, rows - k);
     qo.copy(q + (int64_t)k * a.q_stride * 2, to + kProdK * 512, wave, rows - k);
-  };
-  f32x16 acc[MI][2];
-#pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) acc[mi][half][j] = 0.f;
-  char* now = lds;
-  char* next = lds + kOuterStage;
-  if (rows > 0) stage(0, now);
-  for (int k = 0; k < rows; k += kProdK) {
-    step_barrier();
-    if (k + kProdK < rows) stage(k + kProdK, next);
-#pragma unroll
-    for (int kk = 0; kk < kProdK / 16; ++kk) {
-      s16x8 pf[MI], qf[2];
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi) pf[mi] = read_cols(now, (wm * MI + mi) * 32, kk, lane);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) qf[half] = read_cols(now + kProdK * 512, half * 128 + wn * 32, kk, lane);
-#pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) acc[mi][half] = Mma<DT>::wide(qf[half], pf[mi], acc[mi][half]);
-    }
-    char* const swap = now;
-    now = next;
-    next = swap;
-  }
+  });
   elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
