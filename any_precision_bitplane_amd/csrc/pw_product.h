@@ -3,12 +3,13 @@
 // and pw_product_few.hip share.
 //
 // Tiles.  A block takes a tile of BM rows by 256 columns of one expert and walks
-// the reduction in steps of 64.  A step's operands are copied from memory to LDS
-// without passing registers, one step ahead of the products, in two buffers.
-// An operand whose reduction index is contiguous in memory lies in LDS as rows
-// of 64 (eight 16-byte pieces, piece c of row r at place c ^ (r / 2 & 7), so that
-// sixteen rows' pieces fall on different banks); one whose other index is
-// contiguous lies as it is and is transposed by the reads.
+// the reduction in steps of 64, a cache line of every row (with steps of 32 the
+// L2s serve every line twice: 8192 x 8192 x 8192 bf16 907 us against 760).  A
+// step's operands are copied from memory to LDS without passing registers, ahead
+// of the products.  An operand whose reduction index is contiguous in memory lies
+// in LDS as rows of 64 (eight 16-byte pieces, piece c of row r at place c ^ (r /
+// 2 & 7), so that sixteen rows' pieces fall on different banks); one whose other
+// index is contiguous lies as it is and is transposed by the reads.
 #pragma once
 
 #include "pw_device.h"
@@ -18,7 +19,7 @@
 namespace pw {
 
 constexpr int kProdN = 256;       // columns of a tile: two halves of 128
-constexpr int kProdK = 64;        // reduction steps
+constexpr int kProdK = 64;        // reduction steps that are copied together
 constexpr int kProdGroup = 8;     // row tiles that go through all columns together
 constexpr uint32_t kRsrcBytes = 0x80000000u;
 
@@ -147,38 +148,34 @@ __device__ __forceinline__ uint32_t lds_at(const void* p) {
 }
 
 // Where the lanes of a wave fetch their 16-byte pieces of a tile of R rows of 64
-// (reduction contiguous).  at[i]: byte offset of the lane's piece of copy i.
+// (reduction contiguous).  at[i]: byte offset of the lane's piece of copy i.  A
+// copy of a wave covers eight rows: lane l fetches row l / 8.
 template <int R, int WAVES>
 struct RowsOperand {
   static constexpr int kCopies = R / 8 / WAVES;
   uint32_t at[kCopies];
   int piece;
-  // A copy of a wave covers eight rows: lane l fetches row l / 8.
   template <class RowOffset>
   __device__ __forceinline__ void init(int wave, int lane, RowOffset offset_of) {
     piece = (lane & 7) ^ (lane / 16 + 4 * (wave & 1));
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) at[i] = offset_of((i * WAVES + wave) * 8 + lane / 8) + (uint32_t)(piece * 16);
   }
-  // Copies FROM .. TO - 1 of the step from reduction index k on; past the end, K, reads zero.
-  template <int FROM = 0, int TO = kCopies>
-  __device__ __forceinline__ void copy(const char* base, uint32_t to, int wave, int k, int K) const {
-    const rsrc_t rs = copy_rsrc(base);
-    const bool in = k + piece * 8 < K;
-#pragma unroll
-    for (int i = FROM; i < TO; ++i)
-      copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, in ? at[i] : kOutOfRange, (uint32_t)k * 2u);
+  // Copy i of the step from reduction index k on; past the end, K, reads zero.
+  __device__ __forceinline__ void copy(int i, rsrc_t rs, uint32_t to, int wave, int k, int K) const {
+    copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, k + piece * 8 < K ? at[i] : kOutOfRange, (uint32_t)k * 2u);
   }
 };
 
-// The same of a tile of 64 reduction rows of 256 contiguous columns.
+// The same of a tile of 64 reduction rows of 256 contiguous columns; a copy of a
+// wave covers two rows: lane l fetches row l / 32.
 __device__ __forceinline__ int cols_place(int k) { return 4 * (k & 3); }   // piece c of row k lies at place c ^ this
 template <int WAVES>
 struct ColsOperand {
-  static constexpr int kCopies = 32 / WAVES;
+  static constexpr int kCopies = kProdK / 2 / WAVES;
   uint32_t at[kCopies];
   int first;
-  // A copy of a wave covers two rows: lane l fetches row l / 32.  Columns past the matrix are read from its last piece.
+  // Columns past the matrix are read from its last piece.
   __device__ __forceinline__ void init(int wave, int lane, int64_t row_bytes, int pieces) {
     first = wave * 2 + lane / 32;
 #pragma unroll
@@ -187,12 +184,9 @@ struct ColsOperand {
       at[i] = (uint32_t)(row * row_bytes) + (uint32_t)(min((lane & 31) ^ cols_place(row), pieces - 1) * 16);
     }
   }
-  // base: the first of the step's rows; left: reduction rows from there on
-  __device__ __forceinline__ void copy(const char* base, uint32_t to, int wave, int left) const {
-    const rsrc_t rs = copy_rsrc(base);
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i)
-      copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, first + i * WAVES * 2 < left ? at[i] : kOutOfRange, 0u);
+  // rs: from the first of the step's rows on; left: reduction rows from there on
+  __device__ __forceinline__ void copy(int i, rsrc_t rs, uint32_t to, int wave, int left) const {
+    copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, first + i * WAVES * 2 < left ? at[i] : kOutOfRange, 0u);
   }
 };
 
@@ -214,69 +208,89 @@ __device__ __forceinline__ s16x8 read_cols(const char* lds, int c0, int kk, int 
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Every wave's copies have landed and every wave has read its operands.
+// All but the newest LEFT copies of every wave have landed, and every wave has
+// read its operands.
+template <int LEFT>
 __device__ __forceinline__ void step_barrier() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LEFT) : "memory");
 }
 
-// Sums of a wave's MI x 2 pieces of 32 x 32 over `steps` steps of 64.  XC, WC:
-// the operand of the rows, of the columns, is read transposed.  stage(t, to)
-// copies step t to LDS at `to`.
+// Sums of a wave's MI x 2 NP pieces of 32 x 32 over `steps` steps of 64: MI
+// pieces of rows from 32 MI wm on, and NP of columns in either half of the tile,
+// from 32 NP wn on.  XC, WC: the operand of the rows, of the columns, is read
+// transposed.  copy(i, t, to): copy i of COPIES of step t, to LDS at `to`; past
+// the last step it writes zeros.  LDS holds NS steps.
 //
 // The operands of sixteen reduction steps are read from LDS while the products
 // of the sixteen before run.  With the last of a step's operands in registers
-// its buffer is free: behind the barrier the copies of the step after the next
-// are started, and the next step's first operands are read, under the products
-// that are left.
-template <int DT, int MI, bool XC, bool WC, int STAGE, class Copy>
-__device__ __forceinline__ void sum_steps(f32x16 (&acc)[MI][2], char* lds, int w_at, int steps, int wm, int wn, int lane,
-                                          Copy stage) {
+// its buffer is free: behind the barrier the copies of the step that comes NS
+// later are started, and the next step's first operands are read.  Both are
+// dealt out between the products, which take longer than issuing them; the
+// copies over the products of two parts, since all waves make theirs at once.
+template <int DT, int MI, int NP, bool XC, bool WC, int NS, int STAGE, int COPIES, class Copy>
+__device__ __forceinline__ void sum_steps(f32x16 (&acc)[MI][2 * NP], char* lds, int w_at, int steps, int wm, int wn,
+                                          int lane, Copy copy) {
+  constexpr int NJ = 2 * NP, kProducts = MI * NJ, kReads = MI + NJ, kParts = kProdK / 16;
+  constexpr int kEarly = (COPIES + 1) / 2, kLate = COPIES - kEarly;   // behind the barrier, and a part later
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int nj = 0; nj < NJ; ++nj)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[mi][half][i] = 0.f;
+      for (int i = 0; i < 16; ++i) acc[mi][nj][i] = 0.f;
   const uint32_t base = lds_at(lds);
-  s16x8 x[2][MI], w[2][2];
-  auto read = [&](const char* at, int kk, s16x8 (&xf)[MI], s16x8 (&wf)[2]) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int c = half * 128 + wn * 32;
-      wf[half] = WC ? read_cols(at + w_at, c, kk, lane) : read_rows(at + w_at, c, kk, lane);
-    }
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      const int r = (wm * MI + mi) * 32;
-      xf[mi] = XC ? read_cols(at, r, kk, lane) : read_rows(at, r, kk, lane);
+  s16x8 x[2][MI], w[2][NJ];
+  // operand j of MI + NJ in the order of their use: the first of x behind the first of w
+  auto read = [&](const char* at, int kk, int j) {
+    if (j == 0 || (j > 1 && j <= NJ)) {
+      const int nj = j == 0 ? 0 : j - 1, c = nj / NP * 128 + (wn * NP + nj % NP) * 32;
+      w[kk & 1][nj] = WC ? read_cols(at + w_at, c, kk, lane) : read_rows(at + w_at, c, kk, lane);
+    } else {
+      const int mi = j == 1 ? 0 : j - NJ, r = (wm * MI + mi) * 32;
+      x[kk & 1][mi] = XC ? read_cols(at, r, kk, lane) : read_rows(at, r, kk, lane);
     }
   };
   if (steps <= 0) return;
-  stage(0, base);
-  step_barrier();
-  if (steps > 1) stage(1, base + STAGE);
-  read(lds, 0, x[0], w[0]);
-  for (int t = 0; t < steps; ++t) {
-    const char* now = lds + (t & 1) * STAGE;
-    const char* next = lds + (~t & 1) * STAGE;
 #pragma unroll
-    for (int kk = 0; kk < kProdK / 16; ++kk) {
-      const int a = kk & 1, b = a ^ 1;
-      if (kk < kProdK / 16 - 1) {
-        read(now, kk + 1, x[b], w[b]);
-      } else if (t + 1 < steps) {
-        step_barrier();
-        if (t + 2 < steps) stage(t + 2, base + (uint32_t)(t & 1) * STAGE);
-        read(next, 0, x[b], w[b]);
+  for (int t = 0; t < NS; ++t)
+#pragma unroll
+    for (int i = 0; i < (t < NS - 1 ? COPIES : kEarly); ++i) copy(i, t, base + t * STAGE);
+  step_barrier<(NS - 2) * COPIES + kEarly>();
+#pragma unroll
+  for (int j = 0; j < kReads; ++j) read(lds, 0, j);
+  int now = 0;   // buffer of step t
+  uint32_t freed = base + (NS - 1) * STAGE;
+  for (int t = 0; t < steps; ++t) {
+    const char* const at = lds + now * STAGE;
+    now = now == NS - 1 ? 0 : now + 1;
+    const char* const then = lds + now * STAGE;
+#pragma unroll
+    for (int kk = 0; kk < kParts; ++kk) {
+      const bool last = kk == kParts - 1;
+      if (last) {
+        step_barrier<(NS - 2) * COPIES>();
+        freed = lds_at(at);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int mi = 0; mi < MI; ++mi)
+      for (int j = 0; j < kProducts; ++j) {
+        acc[j / NJ][j % NJ] = Mma<DT>::wide(w[kk & 1][j % NJ], x[kk & 1][j / NJ], acc[j / NJ][j % NJ]);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) acc[mi][half] = Mma<DT>::wide(w[a][half], x[a][mi], acc[mi][half]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < kReads; ++i)
+          if (i * kProducts / (kReads + 2) == j) {
+            if (last) read(then, 0, i);   // behind the last step: not used
+            else read(at, kk + 1, i);
+          }
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) {
+          if (last && i < kEarly && i * kProducts / kEarly == j) copy(i, t + NS, freed);
+          if (kk == 0 && i >= kEarly && (i - kEarly) * kProducts / kLate == j) copy(i, t + NS - 1, freed);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
+  step_barrier<0>();   // no copy is under way when LDS is used otherwise or the block ends
 }
 
 // ----- activations ------------------------------------------------------------

@@ -13,49 +13,54 @@ namespace pw {
 
 namespace {
 
-template <int MI, int WM>
+// WM x WN waves, each with MI pieces of rows and NP of columns in either half.
+template <int MI, int WM, int WN>
 struct Shape {
+  static constexpr int NP = 4 / WN;
   static constexpr int kRows = MI * WM * 32;
-  static constexpr int kWaves = WM * 4;
+  static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = kWaves * kWave;
-  static constexpr int kABytes = kRows * 128;
-  static constexpr int kStage = kABytes + kProdN * 128;
+  static constexpr int kABytes = kRows * kProdK * 2;
+  static constexpr int kStage = kABytes + kProdN * kProdK * 2;
+  static constexpr int kStages = 2;
 };
 
-template <int DT, int EPI, int MI, int WM>
-__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x16 (&acc)[MI][2], char* lds, int wm, int wn,
-                                       int lane) {
+template <int DT, int EPI, int MI, int WM, int WN>
+__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
+                                       f32x16 (&acc)[MI][8 / WN], char* lds, int wm, int wn, int lane) {
   using R = Row<DT>;
   using elem = typename R::elem;
+  constexpr int NP = Shape<MI, WM, WN>::NP, kRows = Shape<MI, WM, WN>::kRows;
   const int hi = lane / 32;
   constexpr bool kGate = EPI == kProductGate;
-  const int n0 = t.nt * (kGate ? kKeepGroup : kProdN) + wn * 32;
+  const int n0 = t.nt * (kGate ? kKeepGroup : kProdN) + wn * NP * 32;
   float scale[MI][2];
   if (kGate && a.z8) {
-    // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the four waves'
+    // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the waves'
     float* part = reinterpret_cast<float*>(lds);
-    __syncthreads();
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float most = 0.f;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const bool in = n0 + 8 * (2 * p + hi) < a.N;
-          const floatx8 v = eight_columns(acc[mi][half], p);
+        for (int c = 0; c < 2 * NP; ++c) {
+          const bool in = n0 + c / 2 * 32 + 8 * (c % 2 * 2 + hi) < a.N;
+          const floatx8 v = eight_columns(acc[mi][half * NP + c / 2], c % 2);
           if (in) most = most_of(v, most);
         }
         most = fmaxf(most, __shfl_xor(most, 32, kWave));
-        if (hi == 0) part[(half * Shape<MI, WM>::kRows + (wm * MI + mi) * 32 + lane) * 4 + wn] = most;
+        if (hi == 0) part[(half * kRows + (wm * MI + mi) * 32 + lane) * WN + wn] = most;
       }
     __syncthreads();
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float* p = part + (half * Shape<MI, WM>::kRows + (wm * MI + mi) * 32 + (lane & 31)) * 4;
-        scale[mi][half] = scale_of(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])));
+        const float* p = part + (half * kRows + (wm * MI + mi) * 32 + (lane & 31)) * WN;
+        float most = fmaxf(p[0], p[1]);
+        if constexpr (WN == 4) most = fmaxf(most, fmaxf(p[2], p[3]));
+        scale[mi][half] = scale_of(most);
       }
   }
 #pragma unroll
@@ -70,9 +75,9 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x
         s[a.groups] = scale[mi][1];
       }
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const int n = n0 + 8 * (2 * p + hi);
-        const floatx8 g = eight_columns(acc[mi][0], p), u = eight_columns(acc[mi][1], p);   // with all lanes
+      for (int c = 0; c < 2 * NP; ++c) {
+        const int n = n0 + c / 2 * 32 + 8 * (c % 2 * 2 + hi);
+        const floatx8 g = eight_columns(acc[mi][c / 2], c % 2), u = eight_columns(acc[mi][NP + c / 2], c % 2);
         if (n >= a.N) continue;
         floatx8 h;
 #pragma unroll
@@ -90,61 +95,58 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x
       }
     } else {
 #pragma unroll
-      for (int half = 0; half < 2; ++half)
+      for (int c = 0; c < 4 * NP; ++c) {
+        const int n = n0 + c / (2 * NP) * 128 + c / 2 % NP * 32 + 8 * (c % 2 * 2 + hi);
+        floatx8 v = eight_columns(acc[mi][c / 2], c % 2);   // with all lanes
+        if (n >= a.N) continue;
+        if constexpr (EPI == kProductAct) {
+          if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)t.e * a.N + n));
+          if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
+          if (a.act != PW_ACT_NONE)
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const int n = n0 + half * 128 + 8 * (2 * p + hi);
-          floatx8 v = eight_columns(acc[mi][half], p);   // with all lanes
-          if (n >= a.N) continue;
-          if constexpr (EPI == kProductAct) {
-            if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)t.e * a.N + n));
-            if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
-            if (a.act != PW_ACT_NONE)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] = act_of(v[j], a.act);
-            if (a.residual)
-              v += R::wide(R::load(static_cast<const elem*>(a.residual) + row * a.residual_stride + n));
-          }
-          if constexpr (EPI == kProductGateGrad) {
-            floatx8 g, u, dg, du, h;
-            if (a.z8) {
-              const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
-              const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
-              g = values_of(*reinterpret_cast<const uint2*>(z), s[0]);
-              u = values_of(*reinterpret_cast<const uint2*>(z + a.N), s[a.groups]);
-            } else {
-              const elem* z = static_cast<const elem*>(a.z) + row * a.z_stride + n;
-              g = R::wide(R::load(z));
-              u = R::wide(R::load(z + a.N));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float s = act_of(g[j], a.act);
-              dg[j] = v[j] * u[j] * act_slope(g[j], a.act);
-              du[j] = v[j] * s;
-              h[j] = s * u[j];
-            }
-            elem* dz = static_cast<elem*>(a.pre) + row * a.pre_stride + n;
-            R::store(dz, R::narrow(dg));
-            R::store(dz + a.N, R::narrow(du));
-            if (a.y) R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
-          } else {
-            R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(v));
-          }
+            for (int j = 0; j < 8; ++j) v[j] = act_of(v[j], a.act);
+          if (a.residual) v += R::wide(R::load(static_cast<const elem*>(a.residual) + row * a.residual_stride + n));
         }
+        if constexpr (EPI == kProductGateGrad) {
+          floatx8 g, u, dg, du, h;
+          if (a.z8) {
+            const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
+            const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
+            g = values_of(*reinterpret_cast<const uint2*>(z), s[0]);
+            u = values_of(*reinterpret_cast<const uint2*>(z + a.N), s[a.groups]);
+          } else {
+            const elem* z = static_cast<const elem*>(a.z) + row * a.z_stride + n;
+            g = R::wide(R::load(z));
+            u = R::wide(R::load(z + a.N));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float s = act_of(g[j], a.act);
+            dg[j] = v[j] * u[j] * act_slope(g[j], a.act);
+            du[j] = v[j] * s;
+            h[j] = s * u[j];
+          }
+          elem* dz = static_cast<elem*>(a.pre) + row * a.pre_stride + n;
+          R::store(dz, R::narrow(dg));
+          R::store(dz + a.N, R::narrow(du));
+          if (a.y) R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
+        } else {
+          R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(v));
+        }
+      }
     }
   }
 }
 
-template <int DT, int EPI, int MI, int WM>
-__global__ __launch_bounds__((Shape<MI, WM>::kThreads), 2) void product_kernel(ProductArgs a) {
-  using S = Shape<MI, WM>;
+template <int DT, int EPI, int MI, int WM, int WN>
+__global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), (MI * WM == 8 && WN == 2 ? 1 : 2)) void product_kernel(ProductArgs a) {
+  using S = Shape<MI, WM, WN>;
   constexpr bool kBack = EPI == kProductBack || EPI == kProductGateGrad;
-  __shared__ __align__(1024) char lds[2 * S::kStage];
+  __shared__ __align__(1024) char lds[S::kStages * S::kStage];
   const Tile t = find_tile<S::kRows>(a.offsets, a.E, a.S, a.NT);
   if (t.rows <= 0) return;
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
-  const int wm = wave / 4, wn = wave % 4;
+  const int wm = wave / WN, wn = wave % WN;
   const char* x = static_cast<const char*>(a.x) + (int64_t)t.row0 * a.x_stride * 2;
   const char* w = static_cast<const char*>(a.w) + (int64_t)t.e * a.w_expert * 2;
 
@@ -162,41 +164,38 @@ __global__ __launch_bounds__((Shape<MI, WM>::kThreads), 2) void product_kernel(P
     w += (int64_t)n0 * a.K * 2;
     wr.init(wave, lane, [&](int r) { return (uint32_t)min(r & (kTile - 1), last) * (uint32_t)(a.K * 2); });
   }
-  f32x16 acc[MI][2];
-  sum_steps<DT, MI, false, kBack, S::kStage>(acc, lds, S::kABytes, (a.K + kProdK - 1) / kProdK, wm, wn, lane,
-                                             [&](int step, uint32_t to) {
-    const int k = step * kProdK;
-    xo.copy(x, to, wave, k, a.K);
-    if constexpr (kBack) {
-      wc.copy(w + (int64_t)k * a.N * 2, to + S::kABytes, wave, a.K - k);
-    } else if constexpr (EPI == kProductGate) {
-      constexpr int kHalf = RowsOperand<kProdN, S::kWaves>::kCopies / 2;
-      wr.template copy<0, kHalf>(w, to + S::kABytes, wave, k, a.K);
-      wr.template copy<kHalf, 2 * kHalf>(w + (int64_t)a.N * a.K * 2, to + S::kABytes, wave, k, a.K);
-    } else {
-      wr.copy(w, to + S::kABytes, wave, k, a.K);
-    }
-  });
-  finish<DT, EPI, MI, WM>(a, t, acc, lds, wm, wn, lane);
+  constexpr int kXCopies = RowsOperand<S::kRows, S::kWaves>::kCopies;
+  constexpr int kWCopies = RowsOperand<kProdN, S::kWaves>::kCopies;
+  static_assert(kWCopies == ColsOperand<S::kWaves>::kCopies, "as many copies of W by rows as by columns");
+  const rsrc_t xs = copy_rsrc(x), ws = copy_rsrc(w), us = copy_rsrc(w + (int64_t)a.N * a.K * 2);
+  f32x16 acc[MI][2 * S::NP];
+  sum_steps<DT, MI, S::NP, false, kBack, S::kStages, S::kStage, kXCopies + kWCopies>(
+      acc, lds, S::kABytes, (a.K + kProdK - 1) / kProdK, wm, wn, lane, [&](int i, int step, uint32_t to) {
+        const int k = step * kProdK, j = i - kXCopies;
+        if (j < 0) xo.copy(i, xs, to, wave, k, a.K);
+        else if constexpr (kBack) wc.copy(j, copy_rsrc(w + (int64_t)k * a.N * 2), to + S::kABytes, wave, a.K - k);
+        else wr.copy(j, EPI == kProductGate && j >= kWCopies / 2 ? us : ws, to + S::kABytes, wave, k, a.K);
+      });
+  finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, wm, wn, lane);
 }
 
-template <int DT, int EPI, int MI, int WM>
+template <int DT, int EPI, int MI, int WM, int WN>
 hipError_t run(ProductArgs a, hipStream_t s) {
-  using Sh = Shape<MI, WM>;
+  using Sh = Shape<MI, WM, WN>;
   a.NT = EPI == kProductGate ? (a.N + kKeepGroup - 1) / kKeepGroup : (a.N + kProdN - 1) / kProdN;
   const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, Sh::kRows), a.NT);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((product_kernel<DT, EPI, MI, WM>), dim3((unsigned)grid), dim3(Sh::kThreads), 0, s, a);
+  hipLaunchKernelGGL((product_kernel<DT, EPI, MI, WM, WN>), dim3((unsigned)grid), dim3(Sh::kThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT, int EPI>
 hipError_t pick(const ProductArgs& a, hipStream_t s) {
   const int64_t experts = a.S < a.E ? a.S : a.E, mean = a.S / (experts > 0 ? experts : 1);
-  if (mean > 160) return run<DT, EPI, 4, 2>(a, s);
-  if (mean > 80) return run<DT, EPI, 2, 2>(a, s);
-  if (mean > 32) return run<DT, EPI, 2, 1>(a, s);
-  return run<DT, EPI, 1, 1>(a, s);
+  if (mean > 160) return run<DT, EPI, 4, 2, 2>(a, s);
+  if (mean > 80) return run<DT, EPI, 2, 2, 4>(a, s);
+  if (mean > 32) return run<DT, EPI, 2, 1, 4>(a, s);
+  return run<DT, EPI, 1, 1, 4>(a, s);
 }
 
 template <int DT>

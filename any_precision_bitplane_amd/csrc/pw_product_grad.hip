@@ -13,14 +13,14 @@ namespace pw {
 
 namespace {
 
-constexpr int kOuterWaves = 8;
+constexpr int kOuterWaves = 4;
 constexpr int kOuterStage = 2 * kProdK * 512;
 
 template <int DT>
-__global__ __launch_bounds__(kOuterWaves * kWave, 2) void outer_kernel(OuterArgs a) {
+__global__ __launch_bounds__(kOuterWaves * kWave, kOuterWaves / 4) void outer_kernel(OuterArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int MI = 4;
+  constexpr int MI = 4, WN = kOuterWaves / 2, NP = 4 / WN;
   __shared__ __align__(1024) char lds[2 * kOuterStage];
   const unsigned each = (a.tiles + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each + i;
   if (i >= each || id >= a.tiles) return;
@@ -34,32 +34,31 @@ __global__ __launch_bounds__(kOuterWaves * kWave, 2) void outer_kernel(OuterArgs
   row0 = uniform(row0);
   rows = uniform(rows);
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
-  const int wm = wave / 4, wn = wave % 4, hi = lane / 32;
+  const int wm = wave / WN, wn = wave % WN, hi = lane / 32;
   const char* p = static_cast<const char*>(a.p) + ((int64_t)row0 * a.p_stride + mt * 256) * 2;
   const char* q = static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * 256) * 2;
   ColsOperand<kOuterWaves> po, qo;
   po.init(wave, lane, a.p_stride * 2, (a.M - mt * 256 + 7) / 8);
   qo.init(wave, lane, a.q_stride * 2, (a.N - nt * 256 + 7) / 8);
-  f32x16 acc[MI][2];
-  sum_steps<DT, MI, true, true, kOuterStage>(acc, lds, kProdK * 512, (rows + kProdK - 1) / kProdK, wm, wn, lane,
-                                             [&](int step, uint32_t to) {
-    const int k = step * kProdK;
-    po.copy(p + (int64_t)k * a.p_stride * 2, to, wave, rows - k);
-    qo.copy(q + (int64_t)k * a.q_stride * 2, to + kProdK * 512, wave, rows - k);
-  });
+  constexpr int kCopies = ColsOperand<kOuterWaves>::kCopies;
+  f32x16 acc[MI][2 * NP];
+  sum_steps<DT, MI, NP, true, true, 2, kOuterStage, 2 * kCopies>(
+      acc, lds, kProdK * 512, (rows + kProdK - 1) / kProdK, wm, wn, lane, [&](int i, int step, uint32_t to) {
+        const int k = step * kProdK;
+        if (i < kCopies) po.copy(i, copy_rsrc(p + (int64_t)k * a.p_stride * 2), to, wave, rows - k);
+        else qo.copy(i - kCopies, copy_rsrc(q + (int64_t)k * a.q_stride * 2), to + kProdK * 512, wave, rows - k);
+      });
   elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     const int m = mt * 256 + (wm * MI + mi) * 32 + (lane & 31);
     if (m >= a.M) continue;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int n = nt * 256 + half * 128 + wn * 32 + 8 * (2 * c + hi);
-        const floatx8 v = eight_columns(acc[mi][half], c);   // with all lanes
-        if (n < a.N) R::store(out + (int64_t)m * a.N + n, R::narrow(v));
-      }
+    for (int c = 0; c < 4 * NP; ++c) {
+      const int n = nt * 256 + c / (2 * NP) * 128 + (wn * NP + c / 2 % NP) * 32 + 8 * (c % 2 * 2 + hi);
+      const floatx8 v = eight_columns(acc[mi][c / 2], c % 2);   // with all lanes
+      if (n < a.N) R::store(out + (int64_t)m * a.N + n, R::narrow(v));
+    }
   }
 }
 
