@@ -23,7 +23,6 @@ constexpr int kProdK = 64;        // reduction steps that are copied together
 constexpr int kProdGroup = 8;     // row tiles that go through all columns together
 constexpr uint32_t kRsrcBytes = 0x80000000u;
 
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -34,20 +33,14 @@ struct Mma;
 template <>
 struct Mma<PW_F16> {
   typedef _Float16 frag __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x16 wide(s16x8 a, s16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f32x4 slim(s16x8 a, s16x8 b, f32x4 c) {
+  static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
   }
 };
 template <>
 struct Mma<PW_BF16> {
   typedef __bf16 frag __attribute__((ext_vector_type(8)));
-  static __device__ __forceinline__ f32x16 wide(s16x8 a, s16x8 b, f32x16 c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f32x4 slim(s16x8 a, s16x8 b, f32x4 c) {
+  static __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
   }
 };
@@ -169,7 +162,7 @@ struct RowsOperand {
 
 // The same of a tile of 64 reduction rows of 256 contiguous columns; a copy of a
 // wave covers two rows: lane l fetches row l / 32.
-__device__ __forceinline__ int cols_place(int k) { return 4 * (k & 3); }   // piece c of row k lies at place c ^ this
+__device__ __forceinline__ int cols_place(int k) { return 2 * (k & 3) + (k & 8); }   // piece c of row k lies at place c ^ this
 template <int WAVES>
 struct ColsOperand {
   static constexpr int kCopies = kProdK / 2 / WAVES;
@@ -190,17 +183,17 @@ struct ColsOperand {
   }
 };
 
-// Operand of 32 rows (or columns) from `r0` on for the sixteen reduction steps
-// from 16 kk on: lane l holds row l % 32, steps 8 (l / 32) .. + 7.
+// Operand of 16 rows (or columns) from `r0` on for the 32 reduction steps from
+// 32 kk on: lane l holds row l % 16, steps 8 (l / 16) .. + 7.
 __device__ __forceinline__ s16x8 read_rows(const char* lds, int r0, int kk, int lane) {
-  const int r = lane & 31, piece = (2 * kk + lane / 32) ^ (r / 2 & 7);
+  const int r = lane & 15, piece = (4 * kk + lane / 16) ^ (r / 2);
   return *reinterpret_cast<const s16x8*>(lds + (r0 + r) * 128 + piece * 16);
 }
 // The transposing read gives lane i of sixteen column i of four rows of sixteen
 // columns, lanes 4 j .. 4 j + 3 of which hold the address of row j's.
 __device__ __forceinline__ s16x8 read_cols(const char* lds, int c0, int kk, int lane) {
-  const int k = 16 * kk + 8 * (lane / 32) + (lane & 15) / 4;
-  const int c = c0 + (lane & 16) + 4 * (lane & 3);
+  const int k = 32 * kk + 8 * (lane / 16) + (lane & 15) / 4;
+  const int c = c0 + 4 * (lane & 3);
   typedef __attribute__((address_space(3))) s16x4* p4;
   const char* p = lds + k * 512 + (((c / 8) ^ cols_place(k)) * 16) + (c & 4) * 2;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p));
@@ -215,77 +208,86 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LEFT) : "memory");
 }
 
-// Sums of a wave's MI x 2 NP pieces of 32 x 32 over `steps` steps of 64: MI
-// pieces of rows from 32 MI wm on, and NP of columns in either half of the tile,
-// from 32 NP wn on.  XC, WC: the operand of the rows, of the columns, is read
-// transposed.  copy(i, t, to): copy i of COPIES of step t, to LDS at `to`; past
-// the last step it writes zeros.  LDS holds NS steps.
+// Sums of a wave's 16 RI rows, from 16 RI wm on, by 8 CJ columns of either half
+// of the tile, from 8 CJ wn on, over `steps` steps of 64.  XC, WC: the operand of
+// the rows, of the columns, is read transposed.  copy_x(i, t, to), copy_w: copy i
+// of XN, WN of step t, to LDS at `to`; past the last step they write zeros.  LDS
+// holds XB steps of x (XBYTES each), then two of w.
 //
-// The operands of sixteen reduction steps are read from LDS while the products
-// of the sixteen before run.  With the last of a step's operands in registers
-// its buffer is free: behind the barrier the copies of the step that comes NS
-// later are started, and the next step's first operands are read.  Both are
-// dealt out between the products, which take longer than issuing them; the
-// copies over the products of two parts, since all waves make theirs at once.
-template <int DT, int MI, int NP, bool XC, bool WC, int NS, int STAGE, int COPIES, class Copy>
-__device__ __forceinline__ void sum_steps(f32x16 (&acc)[MI][2 * NP], char* lds, int w_at, int steps, int wm, int wn,
-                                          int lane, Copy copy) {
-  constexpr int NJ = 2 * NP, kProducts = MI * NJ, kReads = MI + NJ, kParts = kProdK / 16;
-  constexpr int kEarly = (COPIES + 1) / 2, kLate = COPIES - kEarly;   // behind the barrier, and a part later
+// The products are 16 x 16 x 32 (a wave's sums are read and written half as often
+// as by 32 x 32 x 16 ones, which the clock shows).  The operands of 32 reduction
+// steps are read from LDS while the products of the 32 before run.  With the last
+// of a step's operands in registers its buffers are free: behind the barrier the
+// next step's first operands are read and the copies of w of the step after it
+// are started, those of x with them (XB 2) or a part later (XB 3: a step ahead
+// more, and the waves' copies do not all come at once).  Reads and copies are
+// dealt out between the products, which take longer than issuing them.
+template <int DT, int RI, int CJ, bool XC, bool WC, int XB, int XBYTES, int XN, int WN, class CopyX, class CopyW>
+__device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int steps, int wm, int wn, int lane,
+                                          CopyX copy_x, CopyW copy_w) {
+  constexpr int kProducts = RI * CJ, kReads = RI + CJ, kParts = kProdK / 32, kWBytes = kProdN * kProdK * 2;
+  constexpr int kLast = XB == 2 ? WN + XN : WN;   // copies behind the barrier
+  constexpr int kReadEvery = kProducts / (kReads + 2), kXEvery = kProducts / XN;
+  // a copy every so many products, or so many copies with each
+  constexpr int kSpread = XB == 2 ? kLast : 2 * kLast, kCopyEvery = kProducts < kSpread ? 1 : kProducts / kSpread;
+  constexpr int kTogether = (kLast + kProducts - 1) / kProducts;
+  static_assert(kReadEvery > 0 && kXEvery > 0 && kParts == 2, "a product for every read and every copy");
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
+  for (int r = 0; r < RI; ++r)
 #pragma unroll
-    for (int nj = 0; nj < NJ; ++nj)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[mi][nj][i] = 0.f;
-  const uint32_t base = lds_at(lds);
-  s16x8 x[2][MI], w[2][NJ];
-  // operand j of MI + NJ in the order of their use: the first of x behind the first of w
-  auto read = [&](const char* at, int kk, int j) {
-    if (j == 0 || (j > 1 && j <= NJ)) {
-      const int nj = j == 0 ? 0 : j - 1, c = nj / NP * 128 + (wn * NP + nj % NP) * 32;
-      w[kk & 1][nj] = WC ? read_cols(at + w_at, c, kk, lane) : read_rows(at + w_at, c, kk, lane);
+    for (int c = 0; c < CJ; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t base = lds_at(lds), base_w = base + XB * XBYTES;
+  s16x8 x[2][RI], w[2][CJ];
+  // operand j of RI + CJ in the order of their use: the first of x behind the first of w
+  auto read = [&](const char* at_x, const char* at_w, int kk, int j) {
+    if (j == 0 || (j > 1 && j <= CJ)) {
+      const int i = j == 0 ? 0 : j - 1, c = i / (CJ / 2) * 128 + (wn * (CJ / 2) + i % (CJ / 2)) * 16;
+      w[kk & 1][i] = WC ? read_cols(at_w, c, kk, lane) : read_rows(at_w, c, kk, lane);
     } else {
-      const int mi = j == 1 ? 0 : j - NJ, r = (wm * MI + mi) * 32;
-      x[kk & 1][mi] = XC ? read_cols(at, r, kk, lane) : read_rows(at, r, kk, lane);
+      const int i = j == 1 ? 0 : j - CJ, r = (wm * RI + i) * 16;
+      x[kk & 1][i] = XC ? read_cols(at_x, r, kk, lane) : read_rows(at_x, r, kk, lane);
     }
   };
   if (steps <= 0) return;
 #pragma unroll
-  for (int t = 0; t < NS; ++t)
+  for (int t = 0; t < 2; ++t) {
 #pragma unroll
-    for (int i = 0; i < (t < NS - 1 ? COPIES : kEarly); ++i) copy(i, t, base + t * STAGE);
-  step_barrier<(NS - 2) * COPIES + kEarly>();
+    for (int i = 0; i < XN; ++i) copy_x(i, t, base + t * XBYTES);
 #pragma unroll
-  for (int j = 0; j < kReads; ++j) read(lds, 0, j);
-  int now = 0;   // buffer of step t
-  uint32_t freed = base + (NS - 1) * STAGE;
+    for (int i = 0; i < WN; ++i) copy_w(i, t, base_w + t * kWBytes);
+  }
+  step_barrier<XN + WN>();
+#pragma unroll
+  for (int j = 0; j < kReads; ++j) read(lds, lds + XB * XBYTES, 0, j);
+  int bx = 0;   // x's buffer of step t
   for (int t = 0; t < steps; ++t) {
-    const char* const at = lds + now * STAGE;
-    now = now == NS - 1 ? 0 : now + 1;
-    const char* const then = lds + now * STAGE;
+    const char* const at_x = lds + bx * XBYTES;
+    const char* const at_w = lds + XB * XBYTES + (t & 1) * kWBytes;
+    bx = bx == XB - 1 ? 0 : bx + 1;
+    const char* const then_x = lds + bx * XBYTES;
+    const char* const then_w = lds + XB * XBYTES + (~t & 1) * kWBytes;
+    const uint32_t to_x = base + (uint32_t)((XB == 2 ? bx ^ 1 : bx == XB - 1 ? 0 : bx + 1) * XBYTES);   // step t + 2's
+    const uint32_t to_w = base_w + (uint32_t)((t & 1) * kWBytes);
 #pragma unroll
     for (int kk = 0; kk < kParts; ++kk) {
       const bool last = kk == kParts - 1;
-      if (last) {
-        step_barrier<(NS - 2) * COPIES>();
-        freed = lds_at(at);
-      }
+      if (last) step_barrier<XB == 2 ? 0 : XN>();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < kProducts; ++j) {
-        acc[j / NJ][j % NJ] = Mma<DT>::wide(w[kk & 1][j % NJ], x[kk & 1][j / NJ], acc[j / NJ][j % NJ]);
-#pragma unroll
-        for (int i = 0; i < kReads; ++i)
-          if (i * kProducts / (kReads + 2) == j) {
-            if (last) read(then, 0, i);   // behind the last step: not used
-            else read(at, kk + 1, i);
-          }
-#pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-          if (last && i < kEarly && i * kProducts / kEarly == j) copy(i, t + NS, freed);
-          if (kk == 0 && i >= kEarly && (i - kEarly) * kProducts / kLate == j) copy(i, t + NS - 1, freed);
+        acc[j / CJ][j % CJ] = Mma<DT>::mma(w[kk & 1][j % CJ], x[kk & 1][j / CJ], acc[j / CJ][j % CJ]);
+        if (j % kReadEvery == 0 && j / kReadEvery < kReads) {
+          if (last) read(then_x, then_w, 0, j / kReadEvery);   // behind the last step: not used
+          else read(at_x, at_w, 1, j / kReadEvery);
         }
+        if (last && j % kCopyEvery == 0) {
+#pragma unroll
+          for (int i = j / kCopyEvery * kTogether; i < (j / kCopyEvery + 1) * kTogether; ++i) {
+            if (i < WN) copy_w(i, t + 2, to_w);
+            else if (i < kLast) copy_x(i - WN, t + 2, to_x);
+          }
+        }
+        if (XB == 3 && kk == 0 && j % kXEvery == 0 && j / kXEvery < XN) copy_x(j / kXEvery, t + 2, to_x);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -353,20 +355,42 @@ __device__ __forceinline__ floatx8 values_of(uint2 codes, float scale) {
   return v;
 }
 
-// Sums of 32 rows by 32 columns come with lane l holding row l % 32 and columns
-// 8 q + 4 (l / 32) .. + 3 in registers 4 q .. 4 q + 3.  Half of them exchanged
-// with lane l ^ 32, a lane holds eight neighbouring columns: 8 (2 p + l / 32) ..
-// + 7 for p = 0, 1.  Both lanes of a pair have to be active.
-__device__ __forceinline__ floatx8 eight_columns(const f32x16& acc, int p) {
+// Sums of 16 rows by 16 columns come with lane l holding row l % 16 and columns
+// 4 (l / 16) .. + 3.  Of two such pieces, the second's rows behind the first's,
+// exchanged between the sixteens of a wave, a lane holds eight neighbouring
+// columns: row l % 32, columns 8 (l / 32) .. + 7.  All lanes have to be active.
+__device__ __forceinline__ floatx8 eight_columns(f32x4 first, f32x4 second) {
   floatx8 v;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[8 * p + i]), __float_as_uint(acc[8 * p + 4 + i]),
-                                                    false, false);
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(first[i]), __float_as_uint(second[i]), false, false);
     v[i] = __uint_as_float(r[0]);
     v[4 + i] = __uint_as_float(r[1]);
   }
   return v;
 }
+
+// What a lane's sums become is written once for a piece of 32 rows by 16 columns
+// and looped over: unrolled over a wave's pieces it would be longer than the
+// instruction cache.  The pieces' sums of 32 rows wait in LDS, each lane's own.
+template <int CJ>
+struct Sums {
+  float4* at;   // of the wave: [CJ][2][64]
+  __device__ __forceinline__ Sums(char* lds, int wave, int lane)
+      : at(reinterpret_cast<float4*>(lds) + wave * (CJ * 2 * kWave) + lane) {}
+  static constexpr int kBytes = CJ * 2 * kWave * 16;
+  __device__ __forceinline__ void put(const f32x4 (&first)[CJ], const f32x4 (&second)[CJ]) {
+#pragma unroll
+    for (int c = 0; c < CJ; ++c) {
+      const floatx8 v = eight_columns(first[c], second[c]);
+      at[2 * c * kWave] = float4{v[0], v[1], v[2], v[3]};
+      at[(2 * c + 1) * kWave] = float4{v[4], v[5], v[6], v[7]};
+    }
+  }
+  __device__ __forceinline__ floatx8 get(int c) const {
+    const float4 a = at[2 * c * kWave], b = at[(2 * c + 1) * kWave];
+    return floatx8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+};
 
 }  // namespace pw

@@ -13,41 +13,42 @@ namespace pw {
 
 namespace {
 
-// WM x WN waves, each with MI pieces of rows and NP of columns in either half.
+// WM x WN waves, each with 32 MI rows and 128 / WN columns in either half.
 template <int MI, int WM, int WN>
 struct Shape {
-  static constexpr int NP = 4 / WN;
+  static constexpr int RI = 2 * MI, CJ = 16 / WN;   // pieces of 16 rows and of 16 columns
   static constexpr int kRows = MI * WM * 32;
   static constexpr int kWaves = WM * WN;
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int kABytes = kRows * kProdK * 2;
-  static constexpr int kStage = kABytes + kProdN * kProdK * 2;
-  static constexpr int kStages = 2;
+  static constexpr int kXBuffers = MI * WM == 2 ? 2 : 3;   // two blocks a CU with tiles of 32 and 64 rows
+  static constexpr int kLds = kXBuffers * kABytes + 2 * kProdN * kProdK * 2;
+  static_assert(kWaves * Sums<CJ>::kBytes + 2 * kRows * WN * 4 <= kLds, "LDS of what follows the products");
 };
 
 template <int DT, int EPI, int MI, int WM, int WN>
 __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
-                                       f32x16 (&acc)[MI][8 / WN], char* lds, int wm, int wn, int lane) {
+                                       f32x4 (&acc)[2 * MI][16 / WN], char* lds, int wave, int lane) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int NP = Shape<MI, WM, WN>::NP, kRows = Shape<MI, WM, WN>::kRows;
-  const int hi = lane / 32;
+  constexpr int kHalf = Shape<MI, WM, WN>::CJ / 2, kRows = Shape<MI, WM, WN>::kRows;   // pieces of columns in a half
+  const int hi = lane / 32, wm = wave / WN, wn = wave % WN;
+  Sums<16 / WN> sums(lds, wave, lane);
   constexpr bool kGate = EPI == kProductGate;
-  const int n0 = t.nt * (kGate ? kKeepGroup : kProdN) + wn * NP * 32;
+  const int n0 = t.nt * (kGate ? kKeepGroup : kProdN) + wn * kHalf * 16 + 8 * hi;   // of the lane's first eight columns
   float scale[MI][2];
   if (kGate && a.z8) {
     // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the waves'
-    float* part = reinterpret_cast<float*>(lds);
+    float* part = reinterpret_cast<float*>(lds + Shape<MI, WM, WN>::kWaves * Sums<16 / WN>::kBytes);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float most = 0.f;
 #pragma unroll
-        for (int c = 0; c < 2 * NP; ++c) {
-          const bool in = n0 + c / 2 * 32 + 8 * (c % 2 * 2 + hi) < a.N;
-          const floatx8 v = eight_columns(acc[mi][half * NP + c / 2], c % 2);
-          if (in) most = most_of(v, most);
+        for (int c = 0; c < kHalf; ++c) {
+          const floatx8 v = eight_columns(acc[2 * mi][half * kHalf + c], acc[2 * mi + 1][half * kHalf + c]);
+          if (n0 + 16 * c < a.N) most = most_of(v, most);
         }
         most = fmaxf(most, __shfl_xor(most, 32, kWave));
         if (hi == 0) part[(half * kRows + (wm * MI + mi) * 32 + lane) * WN + wn] = most;
@@ -65,6 +66,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
   }
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
+    sums.put(acc[2 * mi], acc[2 * mi + 1]);
     const int r = (wm * MI + mi) * 32 + (lane & 31);
     if (r >= t.rows) continue;
     const int64_t row = t.row0 + r;
@@ -74,11 +76,11 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
         s[0] = scale[mi][0];
         s[a.groups] = scale[mi][1];
       }
-#pragma unroll
-      for (int c = 0; c < 2 * NP; ++c) {
-        const int n = n0 + c / 2 * 32 + 8 * (c % 2 * 2 + hi);
-        const floatx8 g = eight_columns(acc[mi][c / 2], c % 2), u = eight_columns(acc[mi][NP + c / 2], c % 2);
+#pragma unroll 1
+      for (int c = 0; c < kHalf; ++c) {
+        const int n = n0 + 16 * c;
         if (n >= a.N) continue;
+        const floatx8 g = sums.get(c), u = sums.get(kHalf + c);
         floatx8 h;
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = act_of(g[j], a.act) * u[j];
@@ -94,11 +96,11 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
         }
       }
     } else {
-#pragma unroll
-      for (int c = 0; c < 4 * NP; ++c) {
-        const int n = n0 + c / (2 * NP) * 128 + c / 2 % NP * 32 + 8 * (c % 2 * 2 + hi);
-        floatx8 v = eight_columns(acc[mi][c / 2], c % 2);   // with all lanes
+#pragma unroll 1
+      for (int c = 0; c < 2 * kHalf; ++c) {
+        const int n = n0 + c / kHalf * 128 + c % kHalf * 16;
         if (n >= a.N) continue;
+        floatx8 v = sums.get(c);
         if constexpr (EPI == kProductAct) {
           if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)t.e * a.N + n));
           if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
@@ -142,7 +144,7 @@ template <int DT, int EPI, int MI, int WM, int WN>
 __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), (MI * WM == 8 && WN == 2 ? 1 : 2)) void product_kernel(ProductArgs a) {
   using S = Shape<MI, WM, WN>;
   constexpr bool kBack = EPI == kProductBack || EPI == kProductGateGrad;
-  __shared__ __align__(1024) char lds[S::kStages * S::kStage];
+  __shared__ __align__(1024) char lds[S::kLds];
   const Tile t = find_tile<S::kRows>(a.offsets, a.E, a.S, a.NT);
   if (t.rows <= 0) return;
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
@@ -168,15 +170,16 @@ __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), (MI * WM == 8 && WN 
   constexpr int kWCopies = RowsOperand<kProdN, S::kWaves>::kCopies;
   static_assert(kWCopies == ColsOperand<S::kWaves>::kCopies, "as many copies of W by rows as by columns");
   const rsrc_t xs = copy_rsrc(x), ws = copy_rsrc(w), us = copy_rsrc(w + (int64_t)a.N * a.K * 2);
-  f32x16 acc[MI][2 * S::NP];
-  sum_steps<DT, MI, S::NP, false, kBack, S::kStages, S::kStage, kXCopies + kWCopies>(
-      acc, lds, S::kABytes, (a.K + kProdK - 1) / kProdK, wm, wn, lane, [&](int i, int step, uint32_t to) {
-        const int k = step * kProdK, j = i - kXCopies;
-        if (j < 0) xo.copy(i, xs, to, wave, k, a.K);
-        else if constexpr (kBack) wc.copy(j, copy_rsrc(w + (int64_t)k * a.N * 2), to + S::kABytes, wave, a.K - k);
-        else wr.copy(j, EPI == kProductGate && j >= kWCopies / 2 ? us : ws, to + S::kABytes, wave, k, a.K);
+  f32x4 acc[S::RI][S::CJ];
+  sum_steps<DT, S::RI, S::CJ, false, kBack, S::kXBuffers, S::kABytes, kXCopies, kWCopies>(
+      acc, lds, (a.K + kProdK - 1) / kProdK, wm, wn, lane,
+      [&](int i, int step, uint32_t to) { xo.copy(i, xs, to, wave, step * kProdK, a.K); },
+      [&](int i, int step, uint32_t to) {
+        const int k = step * kProdK;
+        if constexpr (kBack) wc.copy(i, copy_rsrc(w + (int64_t)k * a.N * 2), to, wave, a.K - k);
+        else wr.copy(i, EPI == kProductGate && i >= kWCopies / 2 ? us : ws, to, wave, k, a.K);
       });
-  finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, wm, wn, lane);
+  finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, wave, lane);
 }
 
 template <int DT, int EPI, int MI, int WM, int WN>

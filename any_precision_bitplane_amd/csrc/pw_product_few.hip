@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void few_kernel(ProductArgs a) {
 #pragma unroll
         for (int f = 0; f < NF; ++f)
 #pragma unroll
-          for (int i = 0; i < RT; ++i) acc[f][i] = Mma<DT>::slim(wf[u][f][h], xf[u][i][h], acc[f][i]);
+          for (int i = 0; i < RT; ++i) acc[f][i] = Mma<DT>::mma(wf[u][f][h], xf[u][i][h], acc[f][i]);
   }
 #pragma unroll
   for (int f = 0; f < NF; ++f)

@@ -14,14 +14,14 @@ namespace pw {
 namespace {
 
 constexpr int kOuterWaves = 4;
-constexpr int kOuterStage = 2 * kProdK * 512;
+constexpr int kOuterBytes = kProdK * 512;   // of a step of either operand
 
 template <int DT>
 __global__ __launch_bounds__(kOuterWaves * kWave, kOuterWaves / 4) void outer_kernel(OuterArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int MI = 4, WN = kOuterWaves / 2, NP = 4 / WN;
-  __shared__ __align__(1024) char lds[2 * kOuterStage];
+  constexpr int MI = 4, WN = kOuterWaves / 2, kHalf = 8 / WN;
+  __shared__ __align__(1024) char lds[5 * kOuterBytes];
   const unsigned each = (a.tiles + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each + i;
   if (i >= each || id >= a.tiles) return;
   const unsigned per = (unsigned)(a.MT * a.NT);
@@ -41,23 +41,29 @@ __global__ __launch_bounds__(kOuterWaves * kWave, kOuterWaves / 4) void outer_ke
   po.init(wave, lane, a.p_stride * 2, (a.M - mt * 256 + 7) / 8);
   qo.init(wave, lane, a.q_stride * 2, (a.N - nt * 256 + 7) / 8);
   constexpr int kCopies = ColsOperand<kOuterWaves>::kCopies;
-  f32x16 acc[MI][2 * NP];
-  sum_steps<DT, MI, NP, true, true, 2, kOuterStage, 2 * kCopies>(
-      acc, lds, kProdK * 512, (rows + kProdK - 1) / kProdK, wm, wn, lane, [&](int i, int step, uint32_t to) {
+  f32x4 acc[2 * MI][2 * kHalf];
+  sum_steps<DT, 2 * MI, 2 * kHalf, true, true, 3, kOuterBytes, kCopies, kCopies>(
+      acc, lds, (rows + kProdK - 1) / kProdK, wm, wn, lane,
+      [&](int i, int step, uint32_t to) {
         const int k = step * kProdK;
-        if (i < kCopies) po.copy(i, copy_rsrc(p + (int64_t)k * a.p_stride * 2), to, wave, rows - k);
-        else qo.copy(i - kCopies, copy_rsrc(q + (int64_t)k * a.q_stride * 2), to + kProdK * 512, wave, rows - k);
+        po.copy(i, copy_rsrc(p + (int64_t)k * a.p_stride * 2), to, wave, rows - k);
+      },
+      [&](int i, int step, uint32_t to) {
+        const int k = step * kProdK;
+        qo.copy(i, copy_rsrc(q + (int64_t)k * a.q_stride * 2), to, wave, rows - k);
       });
   elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
+    floatx8 sums[2 * kHalf];
+#pragma unroll
+    for (int c = 0; c < 2 * kHalf; ++c) sums[c] = eight_columns(acc[2 * mi][c], acc[2 * mi + 1][c]);   // with all lanes
     const int m = mt * 256 + (wm * MI + mi) * 32 + (lane & 31);
     if (m >= a.M) continue;
 #pragma unroll
-    for (int c = 0; c < 4 * NP; ++c) {
-      const int n = nt * 256 + c / (2 * NP) * 128 + (wn * NP + c / 2 % NP) * 32 + 8 * (c % 2 * 2 + hi);
-      const floatx8 v = eight_columns(acc[mi][c / 2], c % 2);   // with all lanes
-      if (n < a.N) R::store(out + (int64_t)m * a.N + n, R::narrow(v));
+    for (int c = 0; c < 2 * kHalf; ++c) {
+      const int n = nt * 256 + c / kHalf * 128 + (wn * kHalf + c % kHalf) * 16 + 8 * hi;
+      if (n < a.N) R::store(out + (int64_t)m * a.N + n, R::narrow(sums[c]));
     }
   }
 }
