@@ -12,6 +12,8 @@
 // index is contiguous lies as it is and is transposed by the reads.
 #pragma once
 
+#include <type_traits>
+
 #include "pw_device.h"
 #include "pw_internal.h"
 #include "pw_rows.h"
@@ -130,11 +132,13 @@ __device__ __forceinline__ rsrc_t copy_rsrc(const void* base) {
   const uint64_t p = (uint64_t)base;
   return rsrc_t{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, kRsrcBytes, 0x00020000u};
 }
+// `to` + AWAY: the wave's place, `more`: bytes that every lane adds
+template <int AWAY>
 __device__ __forceinline__ void copy16(rsrc_t rs, uint32_t to, uint32_t at, uint32_t more) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+  asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
                :
-               : "s"(to), "v"(at), "s"(rs), "s"(more)
-               : "memory");
+               : "s"(to), "n"(AWAY), "v"(at), "s"(rs), "s"(more)
+               : "memory", "scc");
 }
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
@@ -142,44 +146,70 @@ __device__ __forceinline__ uint32_t lds_at(const void* p) {
 
 // Where the lanes of a wave fetch their 16-byte pieces of a tile of R rows of 64
 // (reduction contiguous).  at[i]: byte offset of the lane's piece of copy i.  A
-// copy of a wave covers eight rows: lane l fetches row l / 8.
-template <int R, int WAVES>
+// copy of a wave covers eight rows: lane l fetches row l / 8.  SPLIT: the second
+// half of the rows has a base of its own.
+template <int R, int WAVES, bool SPLIT = false>
 struct RowsOperand {
-  static constexpr int kCopies = R / 8 / WAVES;
-  uint32_t at[kCopies];
-  int piece;
+  static constexpr int kCopies = R / 8 / WAVES, kApart = WAVES * 1024;
+  uint32_t at[kCopies], more;
+  int piece, K;
+  rsrc_t rs, second;
   template <class RowOffset>
-  __device__ __forceinline__ void init(int wave, int lane, RowOffset offset_of) {
+  __device__ __forceinline__ void init(const char* base, const char* base2, int K_, int wave, int lane, RowOffset offset_of) {
+    rs = copy_rsrc(base);
+    second = copy_rsrc(base2);
+    K = K_;
     piece = (lane & 7) ^ (lane / 16 + 4 * (wave & 1));
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) at[i] = offset_of((i * WAVES + wave) * 8 + lane / 8) + (uint32_t)(piece * 16);
   }
-  // Copy i of the step from reduction index k on; past the end, K, reads zero.
-  __device__ __forceinline__ void copy(int i, rsrc_t rs, uint32_t to, int wave, int k, int K) const {
-    copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, k + piece * 8 < K ? at[i] : kOutOfRange, (uint32_t)k * 2u);
+  // The copies from now on are step t's, in rising order of t; past the end, K, reads zero.
+  __device__ __forceinline__ void begin(int t) {
+    const int k = t * kProdK;
+    more = (uint32_t)k * 2u;
+    if (k + kProdK > K)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) at[i] = k + piece * 8 < K ? at[i] : kOutOfRange;
+  }
+  template <int I>
+  __device__ __forceinline__ void copy(uint32_t to) const {
+    copy16<I * kApart>(SPLIT && I >= kCopies / 2 ? second : rs, to, at[I], more);
   }
 };
 
-// The same of a tile of 64 reduction rows of 256 contiguous columns; a copy of a
-// wave covers two rows: lane l fetches row l / 32.
+// The same of a tile of 64 reduction rows of C contiguous columns; a copy of a
+// wave covers 512 / C rows.
 __device__ __forceinline__ int cols_place(int k) { return 2 * (k & 3) + (k & 8); }   // piece c of row k lies at place c ^ this
-template <int WAVES>
+template <int C, int WAVES>
 struct ColsOperand {
-  static constexpr int kCopies = kProdK / 2 / WAVES;
+  static constexpr int kCopies = kProdK * C / 512 / WAVES, kApart = WAVES * 1024;
   uint32_t at[kCopies];
-  int first;
-  // Columns past the matrix are read from its last piece.
-  __device__ __forceinline__ void init(int wave, int lane, int64_t row_bytes, int pieces) {
-    first = wave * 2 + lane / 32;
+  int first, K;
+  const char* base;
+  int64_t step_bytes;
+  rsrc_t rs;
+  // base: the first of K reduction rows.  Columns past the matrix are read from its last piece.
+  __device__ __forceinline__ void init(const char* base_, int K_, int wave, int lane, int64_t row_bytes, int pieces) {
+    base = base_;
+    K = K_;
+    step_bytes = kProdK * row_bytes;
+    first = wave * (512 / C) + lane / (C / 8);
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
-      const int row = first + i * WAVES * 2;
-      at[i] = (uint32_t)(row * row_bytes) + (uint32_t)(min((lane & 31) ^ cols_place(row), pieces - 1) * 16);
+      const int row = first + i * WAVES * (512 / C);
+      at[i] = (uint32_t)(row * row_bytes) + (uint32_t)(min((lane & (C / 8 - 1)) ^ cols_place(row), pieces - 1) * 16);
     }
   }
-  // rs: from the first of the step's rows on; left: reduction rows from there on
-  __device__ __forceinline__ void copy(int i, rsrc_t rs, uint32_t to, int wave, int left) const {
-    copy16(rs, to + (uint32_t)(i * WAVES + wave) * 1024u, first + i * WAVES * 2 < left ? at[i] : kOutOfRange, 0u);
+  __device__ __forceinline__ void begin(int t) {
+    const int left = K - t * kProdK;
+    rs = copy_rsrc(base + t * step_bytes);
+    if (left < kProdK)
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) at[i] = first + i * WAVES * (512 / C) < left ? at[i] : kOutOfRange;
+  }
+  template <int I>
+  __device__ __forceinline__ void copy(uint32_t to) const {
+    copy16<I * kApart>(rs, to, at[I], 0u);
   }
 };
 
@@ -191,13 +221,14 @@ __device__ __forceinline__ s16x8 read_rows(const char* lds, int r0, int kk, int 
 }
 // The transposing read gives lane i of sixteen column i of four rows of sixteen
 // columns, lanes 4 j .. 4 j + 3 of which hold the address of row j's.
+template <int C>
 __device__ __forceinline__ s16x8 read_cols(const char* lds, int c0, int kk, int lane) {
   const int k = 32 * kk + 8 * (lane / 16) + (lane & 15) / 4;
   const int c = c0 + 4 * (lane & 3);
   typedef __attribute__((address_space(3))) s16x4* p4;
-  const char* p = lds + k * 512 + (((c / 8) ^ cols_place(k)) * 16) + (c & 4) * 2;
+  const char* p = lds + k * (C * 2) + (((c / 8) ^ cols_place(k)) * 16) + (c & 4) * 2;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * 512));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((p4)(p + 4 * (C * 2)));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -208,11 +239,11 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(LEFT) : "memory");
 }
 
-// Sums of a wave's 16 RI rows, from 16 RI wm on, by 8 CJ columns of either half
-// of the tile, from 8 CJ wn on, over `steps` steps of 64.  XC, WC: the operand of
-// the rows, of the columns, is read transposed.  copy_x(i, t, to), copy_w: copy i
-// of XN, WN of step t, to LDS at `to`; past the last step they write zeros.  LDS
-// holds XB steps of x (XBYTES each), then two of w.
+// Sums of a wave's 16 RI rows, from 16 RI wm on, by 16 CJ columns of the tile's TN,
+// from 16 CJ wn on (HALVES: by 8 CJ columns of either half, from 8 CJ wn on), over
+// `steps` steps of 64.  XC, WC: the operand of
+// the rows, of the columns, is read transposed.  xo, wo: their copies; past the
+// last step they write zeros.  LDS holds XB steps of x (TM rows), then two of w.
 //
 // The products are 16 x 16 x 32 (a wave's sums are read and written half as often
 // as by 32 x 32 x 16 ones, which the clock shows).  The operands of 32 reduction
@@ -222,10 +253,35 @@ __device__ __forceinline__ void step_barrier() {
 // are started, those of x with them (XB 2) or a part later (XB 3: a step ahead
 // more, and the waves' copies do not all come at once).  Reads and copies are
 // dealt out between the products, which take longer than issuing them.
-template <int DT, int RI, int CJ, bool XC, bool WC, int XB, int XBYTES, int XN, int WN, class CopyX, class CopyW>
-__device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int steps, int wm, int wn, int lane,
-                                          CopyX copy_x, CopyW copy_w) {
-  constexpr int kProducts = RI * CJ, kReads = RI + CJ, kParts = kProdK / 32, kWBytes = kProdN * kProdK * 2;
+template <int I, int N, class F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<I + 1, N>(f);
+  }
+}
+
+// Copies of the first two steps: LDS has to be free.
+template <int TM, int XB, class XOperand, class WOperand>
+__device__ __forceinline__ void start_steps(char* lds, int wave, XOperand& xo, WOperand& wo) {
+  constexpr int XBYTES = TM * kProdK * 2, kWBytes = WOperand::kCopies * WOperand::kApart;
+  const uint32_t base = lds_at(lds) + (uint32_t)wave * 1024u;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    xo.begin(t);
+    wo.begin(t);
+    each<0, XOperand::kCopies>([&](auto i) { xo.template copy<i>(base + t * XBYTES); });
+    each<0, WOperand::kCopies>([&](auto i) { wo.template copy<i>(base + XB * XBYTES + t * kWBytes); });
+  }
+}
+
+template <int DT, int RI, int CJ, int TM, int TN, bool HALVES, bool XC, bool WC, int XB, class XOperand, class WOperand>
+__device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int steps, int wave, int wm, int wn, int lane,
+                                          XOperand& xo, WOperand& wo) {
+  constexpr int XN = XOperand::kCopies, WN = WOperand::kCopies;
+  constexpr int kProducts = RI * CJ, kReads = RI + CJ, kParts = kProdK / 32;
+  constexpr int XBYTES = TM * kProdK * 2, kWBytes = TN * kProdK * 2;
+  static_assert(kWBytes == WOperand::kCopies * WOperand::kApart, "the copies fill a step");
   constexpr int kLast = XB == 2 ? WN + XN : WN;   // copies behind the barrier
   constexpr int kReadEvery = kProducts / (kReads + 2), kXEvery = kProducts / XN;
   // a copy every so many products, or so many copies with each
@@ -236,26 +292,22 @@ __device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int s
   for (int r = 0; r < RI; ++r)
 #pragma unroll
     for (int c = 0; c < CJ; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint32_t base = lds_at(lds), base_w = base + XB * XBYTES;
-  s16x8 x[2][RI], w[2][CJ];
-  // operand j of RI + CJ in the order of their use: the first of x behind the first of w
+  const uint32_t base = lds_at(lds) + (uint32_t)wave * 1024u, base_w = base + XB * XBYTES;   // of the wave's copies
+  // The first half of x's operands is used up early and read again into the same registers.
+  constexpr int kOnce = RI / 2, kTwice = RI - kOnce;
+  s16x8 xa[kOnce], xb[2][kTwice], w[2][CJ];
+  // operand j of RI + CJ of part kk, in the order of their reads
   auto read = [&](const char* at_x, const char* at_w, int kk, int j) {
-    if (j == 0 || (j > 1 && j <= CJ)) {
-      const int i = j == 0 ? 0 : j - 1, c = i / (CJ / 2) * 128 + (wn * (CJ / 2) + i % (CJ / 2)) * 16;
-      w[kk & 1][i] = WC ? read_cols(at_w, c, kk, lane) : read_rows(at_w, c, kk, lane);
+    if (j < CJ) {
+      const int c = HALVES ? j / (CJ / 2) * (TN / 2) + (wn * (CJ / 2) + j % (CJ / 2)) * 16 : (wn * CJ + j) * 16;
+      w[kk & 1][j] = WC ? read_cols<TN>(at_w, c, kk, lane) : read_rows(at_w, c, kk, lane);
     } else {
-      const int i = j == 1 ? 0 : j - CJ, r = (wm * RI + i) * 16;
-      x[kk & 1][i] = XC ? read_cols(at_x, r, kk, lane) : read_rows(at_x, r, kk, lane);
+      const int i = j < CJ + kTwice ? j - CJ + kOnce : j - CJ - kTwice, r = (wm * RI + i) * 16;
+      (i < kOnce ? xa[i < kOnce ? i : 0] : xb[kk & 1][i < kOnce ? 0 : i - kOnce]) =
+          XC ? read_cols<TM>(at_x, r, kk, lane) : read_rows(at_x, r, kk, lane);
     }
   };
-  if (steps <= 0) return;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-#pragma unroll
-    for (int i = 0; i < XN; ++i) copy_x(i, t, base + t * XBYTES);
-#pragma unroll
-    for (int i = 0; i < WN; ++i) copy_w(i, t, base_w + t * kWBytes);
-  }
+  start_steps<TM, XB>(lds, wave, xo, wo);
   step_barrier<XN + WN>();
 #pragma unroll
   for (int j = 0; j < kReads; ++j) read(lds, lds + XB * XBYTES, 0, j);
@@ -268,29 +320,34 @@ __device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int s
     const char* const then_w = lds + XB * XBYTES + (~t & 1) * kWBytes;
     const uint32_t to_x = base + (uint32_t)((XB == 2 ? bx ^ 1 : bx == XB - 1 ? 0 : bx + 1) * XBYTES);   // step t + 2's
     const uint32_t to_w = base_w + (uint32_t)((t & 1) * kWBytes);
-#pragma unroll
-    for (int kk = 0; kk < kParts; ++kk) {
-      const bool last = kk == kParts - 1;
-      if (last) step_barrier<XB == 2 ? 0 : XN>();
+    xo.begin(t + 2);
+    wo.begin(t + 2);
+    each<0, kParts>([&](auto kk) {
+      constexpr bool last = kk == kParts - 1;
+      if constexpr (last) step_barrier<XB == 2 ? 0 : XN>();
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < kProducts; ++j) {
-        acc[j / CJ][j % CJ] = Mma<DT>::mma(w[kk & 1][j % CJ], x[kk & 1][j / CJ], acc[j / CJ][j % CJ]);
-        if (j % kReadEvery == 0 && j / kReadEvery < kReads) {
-          if (last) read(then_x, then_w, 0, j / kReadEvery);   // behind the last step: not used
-          else read(at_x, at_w, 1, j / kReadEvery);
-        }
-        if (last && j % kCopyEvery == 0) {
-#pragma unroll
-          for (int i = j / kCopyEvery * kTogether; i < (j / kCopyEvery + 1) * kTogether; ++i) {
-            if (i < WN) copy_w(i, t + 2, to_w);
-            else if (i < kLast) copy_x(i - WN, t + 2, to_x);
+      each<0, kProducts>([&](auto j) {
+        constexpr int row = j / CJ;
+        acc[row][j % CJ] = Mma<DT>::mma(w[kk & 1][j % CJ], row < kOnce ? xa[row < kOnce ? row : 0] : xb[kk & 1][row < kOnce ? 0 : row - kOnce],
+                                        acc[row][j % CJ]);
+        each<0, kReads>([&](auto i) {
+          // not before the last product with what is in its registers
+          constexpr int own = i - CJ - kTwice, slot = own >= 0 && (own + 1) * CJ - 1 > i * kReadEvery ? (own + 1) * CJ - 1 : i * kReadEvery;
+          static_assert(slot < kProducts, "a product for every read");
+          if constexpr (slot == j) {
+            if constexpr (last) read(then_x, then_w, 0, i);   // behind the last step: not used
+            else read(at_x, at_w, 1, i);
           }
-        }
-        if (XB == 3 && kk == 0 && j % kXEvery == 0 && j / kXEvery < XN) copy_x(j / kXEvery, t + 2, to_x);
+        });
+        if constexpr (last && j % kCopyEvery == 0)
+          each<j / kCopyEvery * kTogether, (j / kCopyEvery + 1) * kTogether>([&](auto i) {
+            if constexpr (i < WN) wo.template copy<i>(to_w);
+            else if constexpr (i < kLast) xo.template copy<i - WN>(to_x);
+          });
+        if constexpr (XB == 3 && kk == 0 && j % kXEvery == 0 && j / kXEvery < XN) xo.template copy<j / kXEvery>(to_x);
         __builtin_amdgcn_sched_barrier(0);
-      }
-    }
+      });
+    });
   }
   step_barrier<0>();   // no copy is under way when LDS is used otherwise or the block ends
 }
@@ -370,25 +427,37 @@ __device__ __forceinline__ floatx8 eight_columns(f32x4 first, f32x4 second) {
   return v;
 }
 
-// What a lane's sums become is written once for a piece of 32 rows by 16 columns
-// and looped over: unrolled over a wave's pieces it would be longer than the
-// instruction cache.  The pieces' sums of 32 rows wait in LDS, each lane's own.
-template <int CJ>
+// A wave's sums of 32 rows by 64 columns on their way to rows: they come with a
+// lane holding eight columns of one of 32 rows and go on with eight lanes holding
+// a row's 64, so that loads and stores take whole lines of 128 bytes (stored as
+// they come, 256 x 256 bf16 values a block go out at 3 TB/s).  What they become is
+// written once and looped over: unrolled it would be longer than the instruction
+// cache.  In LDS, the wave's own; sixteen bytes of row r lie at place c ^ (r & 15).
 struct Sums {
-  float4* at;   // of the wave: [CJ][2][64]
-  __device__ __forceinline__ Sums(char* lds, int wave, int lane)
-      : at(reinterpret_cast<float4*>(lds) + wave * (CJ * 2 * kWave) + lane) {}
-  static constexpr int kBytes = CJ * 2 * kWave * 16;
-  __device__ __forceinline__ void put(const f32x4 (&first)[CJ], const f32x4 (&second)[CJ]) {
-#pragma unroll
-    for (int c = 0; c < CJ; ++c) {
-      const floatx8 v = eight_columns(first[c], second[c]);
-      at[2 * c * kWave] = float4{v[0], v[1], v[2], v[3]};
-      at[(2 * c + 1) * kWave] = float4{v[4], v[5], v[6], v[7]};
-    }
+  static constexpr int kBytes = 32 * 64 * 4;
+  char* at;
+  int lane;
+  __device__ __forceinline__ Sums(char* lds, int wave, int lane_) : at(lds + wave * kBytes), lane(lane_) {}
+  static __device__ __forceinline__ void order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
-  __device__ __forceinline__ floatx8 get(int c) const {
-    const float4 a = at[2 * c * kWave], b = at[(2 * c + 1) * kWave];
+  __device__ __forceinline__ float4* place(int row, int c) const {
+    return reinterpret_cast<float4*>(at + row * 256 + ((c ^ (row & 15)) * 16));
+  }
+  __device__ __forceinline__ void put(const f32x4 (&first)[4], const f32x4 (&second)[4]) {
+    order();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const floatx8 v = eight_columns(first[c], second[c]);
+      *place(lane & 31, 4 * c + 2 * (lane / 32)) = float4{v[0], v[1], v[2], v[3]};
+      *place(lane & 31, 4 * c + 2 * (lane / 32) + 1) = float4{v[4], v[5], v[6], v[7]};
+    }
+    order();
+  }
+  // columns 8 c .. 8 c + 7 of a row
+  __device__ __forceinline__ floatx8 get(int row, int c) const {
+    const float4 a = *place(row, 2 * c), b = *place(row, 2 * c + 1);
     return floatx8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
 };

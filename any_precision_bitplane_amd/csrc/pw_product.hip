@@ -13,7 +13,7 @@ namespace pw {
 
 namespace {
 
-// WM x WN waves, each with 32 MI rows and 128 / WN columns in either half.
+// WM x WN waves, each with 32 MI rows and 64 columns.
 template <int MI, int WM, int WN>
 struct Shape {
   static constexpr int RI = 2 * MI, CJ = 16 / WN;   // pieces of 16 rows and of 16 columns
@@ -23,84 +23,72 @@ struct Shape {
   static constexpr int kABytes = kRows * kProdK * 2;
   static constexpr int kXBuffers = MI * WM == 2 ? 2 : 3;   // two blocks a CU with tiles of 32 and 64 rows
   static constexpr int kLds = kXBuffers * kABytes + 2 * kProdN * kProdK * 2;
-  static_assert(kWaves * Sums<CJ>::kBytes + 2 * kRows * WN * 4 <= kLds, "LDS of what follows the products");
+  static_assert(WN == 4 && kWaves * Sums::kBytes + 2 * kRows * 16 <= kLds, "LDS of what follows the products");
 };
 
 template <int DT, int EPI, int MI, int WM, int WN>
-__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
-                                       f32x4 (&acc)[2 * MI][16 / WN], char* lds, int wave, int lane) {
+__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x4 (&acc)[2 * MI][16 / WN], char* lds,
+                                       int wave, int lane) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int kHalf = Shape<MI, WM, WN>::CJ / 2, kRows = Shape<MI, WM, WN>::kRows;   // pieces of columns in a half
-  const int hi = lane / 32, wm = wave / WN, wn = wave % WN;
-  Sums<16 / WN> sums(lds, wave, lane);
+  using S = Shape<MI, WM, WN>;
   constexpr bool kGate = EPI == kProductGate;
-  const int n0 = t.nt * (kGate ? kKeepGroup : kProdN) + wn * kHalf * 16 + 8 * hi;   // of the lane's first eight columns
-  float scale[MI][2];
+  const int wm = wave / WN, wn = wave % WN;
+  Sums sums(lds, wave, lane);
+  // gated: eight lanes hold 32 columns of g and of u of two rows (four lanes each), else 64 of one row
+  constexpr int kLanes = kGate ? 4 : 8;
+  const int own = lane & (kLanes - 1), n = kGate ? t.nt * kKeepGroup + wn * 32 + own * 8 : t.nt * kProdN + wn * 64 + own * 8;
+  // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the waves'
+  float4* const most = reinterpret_cast<float4*>(lds + S::kWaves * Sums::kBytes);   // [2][kRows]
   if (kGate && a.z8) {
-    // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the waves'
-    float* part = reinterpret_cast<float*>(lds + Shape<MI, WM, WN>::kWaves * Sums<16 / WN>::kBytes);
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float most = 0.f;
+        float m = 0.f;
 #pragma unroll
-        for (int c = 0; c < kHalf; ++c) {
-          const floatx8 v = eight_columns(acc[2 * mi][half * kHalf + c], acc[2 * mi + 1][half * kHalf + c]);
-          if (n0 + 16 * c < a.N) most = most_of(v, most);
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+          const floatx8 v = eight_columns(acc[2 * mi][c], acc[2 * mi + 1][c]);
+          if (t.nt * kKeepGroup + wn * 32 + c % 2 * 16 + lane / 32 * 8 < a.N) m = most_of(v, m);
         }
-        most = fmaxf(most, __shfl_xor(most, 32, kWave));
-        if (hi == 0) part[(half * kRows + (wm * MI + mi) * 32 + lane) * WN + wn] = most;
+        m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        if (lane < 32) reinterpret_cast<float*>(most + half * S::kRows + (wm * MI + mi) * 32 + lane)[wn] = m;
       }
     __syncthreads();
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float* p = part + (half * kRows + (wm * MI + mi) * 32 + (lane & 31)) * WN;
-        float most = fmaxf(p[0], p[1]);
-        if constexpr (WN == 4) most = fmaxf(most, fmaxf(p[2], p[3]));
-        scale[mi][half] = scale_of(most);
-      }
   }
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     sums.put(acc[2 * mi], acc[2 * mi + 1]);
-    const int r = (wm * MI + mi) * 32 + (lane & 31);
-    if (r >= t.rows) continue;
-    const int64_t row = t.row0 + r;
-    if constexpr (kGate) {
-      if (a.z8 && wn == 0 && hi == 0) {
-        float* s = a.z_scale + row * 2 * a.groups + t.nt;
-        s[0] = scale[mi][0];
-        s[a.groups] = scale[mi][1];
-      }
 #pragma unroll 1
-      for (int c = 0; c < kHalf; ++c) {
-        const int n = n0 + 16 * c;
-        if (n >= a.N) continue;
-        const floatx8 g = sums.get(c), u = sums.get(kHalf + c);
+    for (int i = lane / kLanes; i < 32; i += kWave / kLanes) {
+      const int r = (wm * MI + mi) * 32 + i;
+      if (r >= t.rows || n >= a.N) continue;
+      const int64_t row = t.row0 + r;
+      if constexpr (kGate) {
+        const floatx8 g = sums.get(i, own), u = sums.get(i, 4 + own);
         floatx8 h;
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[j] = act_of(g[j], a.act) * u[j];
         R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
         if (a.z8) {
+          const float4 mg = most[r], mu = most[S::kRows + r];
+          const float sg = scale_of(fmaxf(fmaxf(mg.x, mg.y), fmaxf(mg.z, mg.w)));
+          const float su = scale_of(fmaxf(fmaxf(mu.x, mu.y), fmaxf(mu.z, mu.w)));
+          if (wn == 0 && own == 0) {
+            float* s = a.z_scale + row * 2 * a.groups + t.nt;
+            s[0] = sg;
+            s[a.groups] = su;
+          }
           uint8_t* z = static_cast<uint8_t*>(a.z) + row * a.z_stride + n;
-          *reinterpret_cast<uint2*>(z) = codes_of(g, scale[mi][0]);
-          *reinterpret_cast<uint2*>(z + a.N) = codes_of(u, scale[mi][1]);
+          *reinterpret_cast<uint2*>(z) = codes_of(g, sg);
+          *reinterpret_cast<uint2*>(z + a.N) = codes_of(u, su);
         } else if (a.z) {
           elem* z = static_cast<elem*>(a.z) + row * a.z_stride + n;
           R::store_once(z, R::narrow(g));
           R::store_once(z + a.N, R::narrow(u));
         }
-      }
-    } else {
-#pragma unroll 1
-      for (int c = 0; c < 2 * kHalf; ++c) {
-        const int n = n0 + c / kHalf * 128 + c % kHalf * 16;
-        if (n >= a.N) continue;
-        floatx8 v = sums.get(c);
+      } else {
+        floatx8 v = sums.get(i, own);
         if constexpr (EPI == kProductAct) {
           if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)t.e * a.N + n));
           if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
@@ -141,7 +129,7 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t,
 }
 
 template <int DT, int EPI, int MI, int WM, int WN>
-__global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), (MI * WM == 8 && WN == 2 ? 1 : 2)) void product_kernel(ProductArgs a) {
+__global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), 2) void product_kernel(ProductArgs a) {
   using S = Shape<MI, WM, WN>;
   constexpr bool kBack = EPI == kProductBack || EPI == kProductGateGrad;
   __shared__ __align__(1024) char lds[S::kLds];
@@ -153,32 +141,23 @@ __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), (MI * WM == 8 && WN 
   const char* w = static_cast<const char*>(a.w) + (int64_t)t.e * a.w_expert * 2;
 
   RowsOperand<S::kRows, S::kWaves> xo;
-  RowsOperand<kProdN, S::kWaves> wr;
-  ColsOperand<S::kWaves> wc;
-  xo.init(wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
+  xo.init(x, x, a.K, wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
+  f32x4 acc[S::RI][S::CJ];
+  const int steps = (a.K + kProdK - 1) / kProdK;
   if constexpr (kBack) {
-    w += (int64_t)t.nt * kProdN * 2;
-    wc.init(wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
+    ColsOperand<kProdN, S::kWaves> wo;
+    wo.init(w + (int64_t)t.nt * kProdN * 2, a.K, wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
+    sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, false, false, true, S::kXBuffers>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
   } else {
     // gated: rows of g, then the same rows of u, which have a base of their own
     constexpr int kTile = EPI == kProductGate ? kKeepGroup : kProdN;
     const int n0 = t.nt * kTile, last = a.N - 1 - n0;
     w += (int64_t)n0 * a.K * 2;
-    wr.init(wave, lane, [&](int r) { return (uint32_t)min(r & (kTile - 1), last) * (uint32_t)(a.K * 2); });
+    RowsOperand<kProdN, S::kWaves, EPI == kProductGate> wo;
+    wo.init(w, w + (int64_t)a.N * a.K * 2, a.K, wave, lane,
+            [&](int r) { return (uint32_t)min(r & (kTile - 1), last) * (uint32_t)(a.K * 2); });
+    sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, EPI == kProductGate, false, false, S::kXBuffers>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
   }
-  constexpr int kXCopies = RowsOperand<S::kRows, S::kWaves>::kCopies;
-  constexpr int kWCopies = RowsOperand<kProdN, S::kWaves>::kCopies;
-  static_assert(kWCopies == ColsOperand<S::kWaves>::kCopies, "as many copies of W by rows as by columns");
-  const rsrc_t xs = copy_rsrc(x), ws = copy_rsrc(w), us = copy_rsrc(w + (int64_t)a.N * a.K * 2);
-  f32x4 acc[S::RI][S::CJ];
-  sum_steps<DT, S::RI, S::CJ, false, kBack, S::kXBuffers, S::kABytes, kXCopies, kWCopies>(
-      acc, lds, (a.K + kProdK - 1) / kProdK, wm, wn, lane,
-      [&](int i, int step, uint32_t to) { xo.copy(i, xs, to, wave, step * kProdK, a.K); },
-      [&](int i, int step, uint32_t to) {
-        const int k = step * kProdK;
-        if constexpr (kBack) wc.copy(i, copy_rsrc(w + (int64_t)k * a.N * 2), to, wave, a.K - k);
-        else wr.copy(i, EPI == kProductGate && i >= kWCopies / 2 ? us : ws, to, wave, k, a.K);
-      });
   finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, wave, lane);
 }
 
@@ -195,7 +174,7 @@ hipError_t run(ProductArgs a, hipStream_t s) {
 template <int DT, int EPI>
 hipError_t pick(const ProductArgs& a, hipStream_t s) {
   const int64_t experts = a.S < a.E ? a.S : a.E, mean = a.S / (experts > 0 ? experts : 1);
-  if (mean > 160) return run<DT, EPI, 4, 2, 2>(a, s);
+  if (mean > 160) return run<DT, EPI, 4, 2, 4>(a, s);
   if (mean > 80) return run<DT, EPI, 2, 2, 4>(a, s);
   if (mean > 32) return run<DT, EPI, 2, 1, 4>(a, s);
   return run<DT, EPI, 1, 1, 4>(a, s);

@@ -13,17 +13,22 @@ namespace pw {
 
 namespace {
 
-constexpr int kOuterWaves = 4;
-constexpr int kOuterBytes = kProdK * 512;   // of a step of either operand
+// Tiles of T x T: 256, of eight waves, one block a CU; or 128, of four, two a CU.
+template <int T>
+struct OuterShape {
+  static constexpr int WM = 2, WN = T / 64, kWaves = WM * WN, RI = T / 16 / WM, CJ = T / 16 / WN;
+  static constexpr int kBuffers = T == 256 ? 3 : 2, kLds = (kBuffers + 2) * T * kProdK * 2;
+};
 
-template <int DT>
-__global__ __launch_bounds__(kOuterWaves * kWave, kOuterWaves / 4) void outer_kernel(OuterArgs a) {
+template <int DT, int T>
+__global__ __launch_bounds__((OuterShape<T>::kWaves * kWave), 2) void outer_kernel(OuterArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  constexpr int MI = 4, WN = kOuterWaves / 2, kHalf = 8 / WN;
-  __shared__ __align__(1024) char lds[5 * kOuterBytes];
-  const unsigned each = (a.tiles + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each + i;
-  if (i >= each || id >= a.tiles) return;
+  using Sh = OuterShape<T>;
+  static_assert(Sh::CJ == 4 && Sh::kWaves * Sums::kBytes <= Sh::kLds, "64 columns a wave");
+  __shared__ __align__(1024) char lds[Sh::kLds];
+  const unsigned each_xcd = (a.tiles + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each_xcd + i;
+  if (i >= each_xcd || id >= a.tiles) return;
   const unsigned per = (unsigned)(a.MT * a.NT);
   const int e = (int)(id / per), local = (int)(id - e * per);
   const int group = local / (kProdGroup * a.NT), rem = local - group * kProdGroup * a.NT;
@@ -34,36 +39,26 @@ __global__ __launch_bounds__(kOuterWaves * kWave, kOuterWaves / 4) void outer_ke
   row0 = uniform(row0);
   rows = uniform(rows);
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
-  const int wm = wave / WN, wn = wave % WN, hi = lane / 32;
-  const char* p = static_cast<const char*>(a.p) + ((int64_t)row0 * a.p_stride + mt * 256) * 2;
-  const char* q = static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * 256) * 2;
-  ColsOperand<kOuterWaves> po, qo;
-  po.init(wave, lane, a.p_stride * 2, (a.M - mt * 256 + 7) / 8);
-  qo.init(wave, lane, a.q_stride * 2, (a.N - nt * 256 + 7) / 8);
-  constexpr int kCopies = ColsOperand<kOuterWaves>::kCopies;
-  f32x4 acc[2 * MI][2 * kHalf];
-  sum_steps<DT, 2 * MI, 2 * kHalf, true, true, 3, kOuterBytes, kCopies, kCopies>(
-      acc, lds, (rows + kProdK - 1) / kProdK, wm, wn, lane,
-      [&](int i, int step, uint32_t to) {
-        const int k = step * kProdK;
-        po.copy(i, copy_rsrc(p + (int64_t)k * a.p_stride * 2), to, wave, rows - k);
-      },
-      [&](int i, int step, uint32_t to) {
-        const int k = step * kProdK;
-        qo.copy(i, copy_rsrc(q + (int64_t)k * a.q_stride * 2), to, wave, rows - k);
-      });
+  const int wm = wave / Sh::WN, wn = wave % Sh::WN;
+  ColsOperand<T, Sh::kWaves> po, qo;
+  po.init(static_cast<const char*>(a.p) + ((int64_t)row0 * a.p_stride + mt * T) * 2, rows, wave, lane, a.p_stride * 2,
+          (a.M - mt * T + 7) / 8);
+  qo.init(static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * T) * 2, rows, wave, lane, a.q_stride * 2,
+          (a.N - nt * T + 7) / 8);
+  f32x4 acc[Sh::RI][Sh::CJ];
+  sum_steps<DT, Sh::RI, Sh::CJ, T, T, false, true, true, Sh::kBuffers>(acc, lds, (rows + kProdK - 1) / kProdK, wave, wm, wn, lane,
+                                                                po, qo);
   elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
+  Sums sums(lds, wave, lane);
+  const int n = nt * T + wn * 64 + (lane & 7) * 8;
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi) {
-    floatx8 sums[2 * kHalf];
+  for (int mi = 0; mi < Sh::RI / 2; ++mi) {
+    sums.put(acc[2 * mi], acc[2 * mi + 1]);
 #pragma unroll
-    for (int c = 0; c < 2 * kHalf; ++c) sums[c] = eight_columns(acc[2 * mi][c], acc[2 * mi + 1][c]);   // with all lanes
-    const int m = mt * 256 + (wm * MI + mi) * 32 + (lane & 31);
-    if (m >= a.M) continue;
-#pragma unroll
-    for (int c = 0; c < 2 * kHalf; ++c) {
-      const int n = nt * 256 + c / kHalf * 128 + (wn * kHalf + c % kHalf) * 16 + 8 * hi;
-      if (n < a.N) R::store(out + (int64_t)m * a.N + n, R::narrow(sums[c]));
+    for (int r = lane / 8; r < 32; r += 8) {
+      const int m = mt * T + (wm * (Sh::RI / 2) + mi) * 32 + r;
+      const floatx8 v = sums.get(r, lane & 7);
+      if (m < a.M && n < a.N) R::store_once(out + (int64_t)m * a.N + n, R::narrow(v));
     }
   }
 }
@@ -122,15 +117,21 @@ __global__ __launch_bounds__(kDzThreads) void bias_grad_kernel(DzArgs a) {
   static_cast<elem*>(a.dbias)[(int64_t)e * a.N + c] = (elem)s;
 }
 
-template <int DT>
+template <int DT, int T>
 hipError_t run_outer(OuterArgs a, hipStream_t s) {
-  a.MT = (a.M + 255) / 256;
-  a.NT = (a.N + 255) / 256;
+  a.MT = (a.M + T - 1) / T;
+  a.NT = (a.N + T - 1) / T;
   const int64_t tiles = (int64_t)a.E * a.MT * a.NT;
   if (tiles > 0x7FFFFFF0) return hipErrorInvalidValue;
   a.tiles = (unsigned)tiles;
-  hipLaunchKernelGGL(outer_kernel<DT>, dim3((unsigned)product_grid(tiles, 1)), dim3(kOuterWaves * kWave), 0, s, a);
+  hipLaunchKernelGGL((outer_kernel<DT, T>), dim3((unsigned)product_grid(tiles, 1)), dim3(OuterShape<T>::kWaves * kWave), 0,
+                     s, a);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t pick_outer(const OuterArgs& a, hipStream_t s) {
+  return a.S > 512ll * a.E ? run_outer<DT, 256>(a, s) : run_outer<DT, 128>(a, s);
 }
 
 template <int DT>
@@ -151,7 +152,7 @@ hipError_t run_dz(const DzArgs& a, hipStream_t s) {
 size_t dz_part_floats(int E, int64_t S, int N) { return (size_t)(S / kDzRows + E) * (size_t)N; }
 
 hipError_t launch_outer(const OuterArgs& a, int dtype, hipStream_t s) {
-  return dtype == PW_F16 ? run_outer<PW_F16>(a, s) : run_outer<PW_BF16>(a, s);
+  return dtype == PW_F16 ? pick_outer<PW_F16>(a, s) : pick_outer<PW_BF16>(a, s);
 }
 
 hipError_t launch_dz(const DzArgs& a, int dtype, hipStream_t s) {
