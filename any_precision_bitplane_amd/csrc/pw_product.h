@@ -275,28 +275,25 @@ __device__ __forceinline__ void start_steps(char* lds, int wave, XOperand& xo, W
   }
 }
 
-template <int DT, int RI, int CJ, int TM, int TN, bool HALVES, bool XC, bool WC, int XB, class XOperand, class WOperand>
-__device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int steps, int wave, int wm, int wn, int lane,
-                                          XOperand& xo, WOperand& wo) {
+// LIVE: pieces of 16 rows with rows of the expert among them; the other sums stay zero.
+template <int DT, int LIVE, int RI, int CJ, int TM, int TN, bool HALVES, bool XC, bool WC, int XB, class XOperand, class WOperand>
+__device__ __forceinline__ void sum_live(f32x4 (&acc)[RI][CJ], char* lds, int steps, int wave, int wm, int wn, int lane,
+                                         XOperand& xo, WOperand& wo) {
   constexpr int XN = XOperand::kCopies, WN = WOperand::kCopies;
-  constexpr int kProducts = RI * CJ, kReads = RI + CJ, kParts = kProdK / 32;
+  constexpr int kProducts = LIVE * CJ, kReads = LIVE ? LIVE + CJ : 0, kSlots = LIVE ? kProducts : 1, kParts = kProdK / 32;
   constexpr int XBYTES = TM * kProdK * 2, kWBytes = TN * kProdK * 2;
   static_assert(kWBytes == WOperand::kCopies * WOperand::kApart, "the copies fill a step");
   constexpr int kLast = XB == 2 ? WN + XN : WN;   // copies behind the barrier
-  constexpr int kReadEvery = kProducts / (kReads + 2), kXEvery = kProducts / XN;
+  constexpr int kReadEvery = kSlots / (kReads + 2), kXEvery = kSlots < XN ? 1 : kSlots / XN;
   // a copy every so many products, or so many copies with each
-  constexpr int kSpread = XB == 2 ? kLast : 2 * kLast, kCopyEvery = kProducts < kSpread ? 1 : kProducts / kSpread;
-  constexpr int kTogether = (kLast + kProducts - 1) / kProducts;
-  static_assert(kReadEvery > 0 && kXEvery > 0 && kParts == 2, "a product for every read and every copy");
-#pragma unroll
-  for (int r = 0; r < RI; ++r)
-#pragma unroll
-    for (int c = 0; c < CJ; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  constexpr int kSpread = XB == 2 ? kLast : 2 * kLast, kCopyEvery = kSlots < kSpread ? 1 : kSlots / kSpread;
+  constexpr int kTogether = (kLast + kSlots - 1) / kSlots, kXTogether = (XN + kSlots - 1) / kSlots;
+  static_assert((kReadEvery > 0 || !LIVE) && kParts == 2, "a product for every read");
   const uint32_t base = lds_at(lds) + (uint32_t)wave * 1024u, base_w = base + XB * XBYTES;   // of the wave's copies
   // The first half of x's operands is used up early and read again into the same registers.
-  constexpr int kOnce = RI / 2, kTwice = RI - kOnce;
-  s16x8 xa[kOnce], xb[2][kTwice], w[2][CJ];
-  // operand j of RI + CJ of part kk, in the order of their reads
+  constexpr int kOnce = LIVE / 2, kTwice = LIVE - kOnce;
+  s16x8 xa[kOnce + 1], xb[2][kTwice + 1], w[2][CJ];
+  // operand j of LIVE + CJ of part kk, in the order of their reads
   auto read = [&](const char* at_x, const char* at_w, int kk, int j) {
     if (j < CJ) {
       const int c = HALVES ? j / (CJ / 2) * (TN / 2) + (wn * (CJ / 2) + j % (CJ / 2)) * 16 : (wn * CJ + j) * 16;
@@ -307,7 +304,6 @@ __device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int s
           XC ? read_cols<TM>(at_x, r, kk, lane) : read_rows(at_x, r, kk, lane);
     }
   };
-  start_steps<TM, XB>(lds, wave, xo, wo);
   step_barrier<XN + WN>();
 #pragma unroll
   for (int j = 0; j < kReads; ++j) read(lds, lds + XB * XBYTES, 0, j);
@@ -326,14 +322,15 @@ __device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int s
       constexpr bool last = kk == kParts - 1;
       if constexpr (last) step_barrier<XB == 2 ? 0 : XN>();
       __builtin_amdgcn_sched_barrier(0);
-      each<0, kProducts>([&](auto j) {
+      each<0, kSlots>([&](auto j) {
         constexpr int row = j / CJ;
-        acc[row][j % CJ] = Mma<DT>::mma(w[kk & 1][j % CJ], row < kOnce ? xa[row < kOnce ? row : 0] : xb[kk & 1][row < kOnce ? 0 : row - kOnce],
-                                        acc[row][j % CJ]);
+        if constexpr (LIVE > 0)
+          acc[row][j % CJ] = Mma<DT>::mma(w[kk & 1][j % CJ], row < kOnce ? xa[row < kOnce ? row : 0] : xb[kk & 1][row < kOnce ? 0 : row - kOnce],
+                                          acc[row][j % CJ]);
         each<0, kReads>([&](auto i) {
           // not before the last product with what is in its registers
           constexpr int own = i - CJ - kTwice, slot = own >= 0 && (own + 1) * CJ - 1 > i * kReadEvery ? (own + 1) * CJ - 1 : i * kReadEvery;
-          static_assert(slot < kProducts, "a product for every read");
+          static_assert(slot < kSlots, "a product for every read");
           if constexpr (slot == j) {
             if constexpr (last) read(then_x, then_w, 0, i);   // behind the last step: not used
             else read(at_x, at_w, 1, i);
@@ -344,11 +341,34 @@ __device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int s
             if constexpr (i < WN) wo.template copy<i>(to_w);
             else if constexpr (i < kLast) xo.template copy<i - WN>(to_x);
           });
-        if constexpr (XB == 3 && kk == 0 && j % kXEvery == 0 && j / kXEvery < XN) xo.template copy<j / kXEvery>(to_x);
+        if constexpr (XB == 3 && kk == 0 && j % kXEvery == 0)
+          each<j / kXEvery * kXTogether, (j / kXEvery + 1) * kXTogether>([&](auto i) {
+            if constexpr (i < XN) xo.template copy<i>(to_x);
+          });
         __builtin_amdgcn_sched_barrier(0);
       });
     });
   }
+}
+
+// live: 16-row pieces of the wave that the expert has rows in (a wave may have
+// none).  An expert's last tile so costs by the quarter of its rows.
+template <int DT, int RI, int CJ, int TM, int TN, bool HALVES, bool XC, bool WC, int XB, class XOperand, class WOperand>
+__device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int steps, int live, int wave, int wm, int wn,
+                                          int lane, XOperand& xo, WOperand& wo) {
+#pragma unroll
+  for (int r = 0; r < RI; ++r)
+#pragma unroll
+    for (int c = 0; c < CJ; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (steps <= 0) return;
+  start_steps<TM, XB>(lds, wave, xo, wo);
+  constexpr int kFew = RI / 2 < 2 ? RI : RI / 2;
+  if (live > RI / 2 || (live > 0 && kFew == RI))
+    sum_live<DT, RI, RI, CJ, TM, TN, HALVES, XC, WC, XB>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+  else if (live > 0)
+    sum_live<DT, kFew, RI, CJ, TM, TN, HALVES, XC, WC, XB>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+  else
+    sum_live<DT, 0, RI, CJ, TM, TN, HALVES, XC, WC, XB>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
   step_barrier<0>();   // no copy is under way when LDS is used otherwise or the block ends
 }
 

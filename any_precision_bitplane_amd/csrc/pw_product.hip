@@ -143,11 +143,12 @@ __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), 2) void product_kern
   RowsOperand<S::kRows, S::kWaves> xo;
   xo.init(x, x, a.K, wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
   f32x4 acc[S::RI][S::CJ];
-  const int steps = (a.K + kProdK - 1) / kProdK;
+  const int steps = (a.K + kProdK - 1) / kProdK, live = (t.rows - wm * MI * 32 + 15) / 16;
   if constexpr (kBack) {
     ColsOperand<kProdN, S::kWaves> wo;
     wo.init(w + (int64_t)t.nt * kProdN * 2, a.K, wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
-    sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, false, false, true, S::kXBuffers>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+    sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, false, false, true, S::kXBuffers>(acc, lds, steps, live, wave, wm, wn, lane,
+                                                                                   xo, wo);
   } else {
     // gated: rows of g, then the same rows of u, which have a base of their own
     constexpr int kTile = EPI == kProductGate ? kKeepGroup : kProdN;
@@ -156,7 +157,8 @@ __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), 2) void product_kern
     RowsOperand<kProdN, S::kWaves, EPI == kProductGate> wo;
     wo.init(w, w + (int64_t)a.N * a.K * 2, a.K, wave, lane,
             [&](int r) { return (uint32_t)min(r & (kTile - 1), last) * (uint32_t)(a.K * 2); });
-    sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, EPI == kProductGate, false, false, S::kXBuffers>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+    sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, EPI == kProductGate, false, false, S::kXBuffers>(acc, lds, steps, live, wave, wm, wn, lane,
+                                                                                   xo, wo);
   }
   finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, wave, lane);
 }

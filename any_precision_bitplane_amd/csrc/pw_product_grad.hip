@@ -46,8 +46,9 @@ __global__ __launch_bounds__((OuterShape<T>::kWaves * kWave), 2) void outer_kern
   qo.init(static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * T) * 2, rows, wave, lane, a.q_stride * 2,
           (a.N - nt * T + 7) / 8);
   f32x4 acc[Sh::RI][Sh::CJ];
-  sum_steps<DT, Sh::RI, Sh::CJ, T, T, false, true, true, Sh::kBuffers>(acc, lds, (rows + kProdK - 1) / kProdK, wave, wm, wn, lane,
-                                                                po, qo);
+  sum_steps<DT, Sh::RI, Sh::CJ, T, T, false, true, true, Sh::kBuffers>(
+      acc, lds, (rows + kProdK - 1) / kProdK, nt * T + wn * 64 < a.N ? (a.M - mt * T - wm * Sh::RI * 16 + 15) / 16 : 0, wave,
+      wm, wn, lane, po, qo);
   elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
   Sums sums(lds, wave, lane);
   const int n = nt * T + wn * 64 + (lane & 7) * 8;
@@ -131,7 +132,8 @@ hipError_t run_outer(OuterArgs a, hipStream_t s) {
 
 template <int DT>
 hipError_t pick_outer(const OuterArgs& a, hipStream_t s) {
-  return a.S > 512ll * a.E ? run_outer<DT, 256>(a, s) : run_outer<DT, 128>(a, s);
+  const int64_t tiles = (int64_t)a.E * ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  return tiles >= kNumCUs ? run_outer<DT, 256>(a, s) : run_outer<DT, 128>(a, s);
 }
 
 template <int DT>
