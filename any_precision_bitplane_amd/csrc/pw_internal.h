@@ -449,8 +449,14 @@ struct ProductArgs {
   float* z_scale;             // [S][2 groups], of 8-bit z
   int groups;
   bool z8;
+  float* part;                // kProductPartBytes of scratch for tiles that are cut, or null
   int NT;                     // set by the launch: column tiles
 };
+// Scratch of the products of up to S rows: the sums of up to kNumCUs parts of
+// tiles of 256 x 256, where tiles of 256 rows are used.
+constexpr int kWideRows = 160;   // mean rows of an expert from which on they are
+constexpr size_t kProductPartBytes = (size_t)kNumCUs * 256 * 256 * sizeof(float);
+inline size_t product_part_bytes(int E, int64_t S) { return S >= (int64_t)kWideRows * E ? kProductPartBytes : 0; }
 hipError_t launch_product(const ProductArgs& a, int dtype, int kind, hipStream_t s);
 bool few_rows(const ProductArgs& a, int kind);
 hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s);

@@ -67,50 +67,87 @@ struct Tile {
   int e, row0, rows, nt;   // rows: the expert's from row0 on; 0: no tile for this block
 };
 
+// Where every expert's row tiles of BM rows begin: lane l has experts 4 l .. 4 l + 3.
+template <int BM>
+struct TileScan {
+  int first[4], count[4], before, upto, tiles;   // tiles: row tiles of all experts
+  __device__ __forceinline__ TileScan(const int32_t* offsets, int E, int S) {
+    const int lane = (int)threadIdx.x & (kWave - 1);
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = 4 * lane + j;
+      first[j] = count[j] = 0;
+      if (e < E) expert_rows(offsets, e, S, first[j], count[j]);
+      mine += (count[j] + BM - 1) / BM;
+    }
+    upto = mine;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+      const int v = __shfl_up(upto, d, kWave);
+      if (lane >= d) upto += v;
+    }
+    before = upto - mine;
+    tiles = __builtin_amdgcn_readlane(upto, kWave - 1);
+  }
+  // Tile `id` of tiles * NT.
+  __device__ __forceinline__ Tile at(unsigned id, int NT) const {
+    const int lane = (int)threadIdx.x & (kWave - 1);
+    const int m = (int)(id / (unsigned)NT);
+    const int owner = __builtin_ctzll(__ballot(before <= m && m < upto));
+    int e = 4 * lane, from = first[0], n = count[0], done = before;
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      const int t = (count[j] + BM - 1) / BM;
+      if (e == 4 * lane + j && done + t <= m) {
+        done += t;
+        e = 4 * lane + j + 1;
+        from = first[j + 1];
+        n = count[j + 1];
+      }
+    }
+    e = __builtin_amdgcn_readlane(e, owner);
+    from = __builtin_amdgcn_readlane(from, owner);
+    n = __builtin_amdgcn_readlane(n, owner);
+    done = __builtin_amdgcn_readlane(done, owner);
+    const int of_e = (n + BM - 1) / BM;
+    const int local = (int)(id - (unsigned)done * (unsigned)NT);
+    const int group = local / (kProdGroup * NT), rem = local - group * kProdGroup * NT;
+    const int here = min(kProdGroup, of_e - group * kProdGroup);
+    const int nt = rem / here, mt = group * kProdGroup + rem - nt * here;
+    return {e, from + mt * BM, n - mt * BM, nt};
+  }
+};
+
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int E, int S, int NT) {
-  const int lane = (int)threadIdx.x & (kWave - 1);
-  int first[4] = {0, 0, 0, 0}, count[4] = {0, 0, 0, 0}, mine = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int e = 4 * lane + j;
-    if (e < E) expert_rows(offsets, e, S, first[j], count[j]);
-    mine += (count[j] + BM - 1) / BM;
-  }
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < kWave; d *= 2) {
-    const int v = __shfl_up(upto, d, kWave);
-    if (lane >= d) upto += v;
-  }
-  const unsigned total = (unsigned)__builtin_amdgcn_readlane(upto, kWave - 1) * (unsigned)NT;
+  const TileScan<BM> scan(offsets, E, S);
+  const unsigned total = (unsigned)scan.tiles * (unsigned)NT;
   const unsigned each = (total + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each + i;
   if (i >= each || id >= total) return {0, 0, 0, 0};
-  const int m = (int)(id / (unsigned)NT);
-  int before = upto - mine;
-  const int owner = __builtin_ctzll(__ballot(before <= m && m < upto));
-  int e = 4 * lane, from = first[0], n = count[0];
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int t = (count[j] + BM - 1) / BM;
-    if (e == 4 * lane + j && before + t <= m) {
-      before += t;
-      e = 4 * lane + j + 1;
-      from = first[j + 1];
-      n = count[j + 1];
+  return scan.at(id, NT);
+}
+
+// The tiles that do not fill a last round of the CUs are cut along the reduction,
+// so that they do: each of the last `rest` tiles into `parts`, whose sums go to
+// memory and are added, in their order, by a launch of their own.  That costs
+// some 25 us (64 MB written and read), a step of 64 about 1.4.
+struct Rounds {
+  unsigned whole, rest, parts;
+  __device__ __forceinline__ Rounds(unsigned total, int steps, bool cut) {
+    rest = cut ? total % kNumCUs : 0;
+    whole = total - rest;
+    parts = 1;
+    if (rest) {
+      const unsigned most = min(min((unsigned)kNumCUs / rest, (unsigned)steps / 8), 8u);
+      if (most > 1 && (unsigned)steps * (most - 1) >= 20 * most) parts = most;
+    }
+    if (parts == 1) {
+      whole = total;
+      rest = 0;
     }
   }
-  e = __builtin_amdgcn_readlane(e, owner);
-  from = __builtin_amdgcn_readlane(from, owner);
-  n = __builtin_amdgcn_readlane(n, owner);
-  before = __builtin_amdgcn_readlane(before, owner);
-  const int tiles = (n + BM - 1) / BM;
-  const int local = (int)(id - (unsigned)before * (unsigned)NT);
-  const int group = local / (kProdGroup * NT), rem = local - group * kProdGroup * NT;
-  const int here = min(kProdGroup, tiles - group * kProdGroup);
-  const int nt = rem / here, mt = group * kProdGroup + rem - nt * here;
-  return {e, from + mt * BM, n - mt * BM, nt};
-}
+};
 
 // Blocks that cover every tile whatever the offsets: a row tile more per expert
 // with rows than the rows fill.

@@ -26,30 +26,92 @@ struct Shape {
   static_assert(WN == 4 && kWaves * Sums::kBytes + 2 * kRows * 16 <= kLds, "LDS of what follows the products");
 };
 
-template <int DT, int EPI, int MI, int WM, int WN>
-__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x4 (&acc)[2 * MI][16 / WN], char* lds,
-                                       int wave, int lane) {
+// What becomes of eight columns from n on of a row's sums v (gated: of g, and u).
+template <int DT, int EPI>
+__device__ __forceinline__ void emit(const ProductArgs& a, int e, int64_t row, int n, floatx8 v, floatx8 u, float sv,
+                                     float su) {
   using R = Row<DT>;
   using elem = typename R::elem;
+  elem* const y = static_cast<elem*>(a.y) + row * a.y_stride + n;
+  if constexpr (EPI == kProductGate) {
+    floatx8 h;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = act_of(v[j], a.act) * u[j];
+    R::store(y, R::narrow(h));
+    if (a.z8) {
+      uint8_t* z = static_cast<uint8_t*>(a.z) + row * a.z_stride + n;
+      *reinterpret_cast<uint2*>(z) = codes_of(v, sv);
+      *reinterpret_cast<uint2*>(z + a.N) = codes_of(u, su);
+      if (n % kKeepGroup == 0) {
+        float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
+        s[0] = sv;
+        s[a.groups] = su;
+      }
+    } else if (a.z) {
+      elem* z = static_cast<elem*>(a.z) + row * a.z_stride + n;
+      R::store_once(z, R::narrow(v));
+      R::store_once(z + a.N, R::narrow(u));
+    }
+  } else if constexpr (EPI == kProductGateGrad) {
+    floatx8 g, dg, du, h;
+    if (a.z8) {
+      const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
+      const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
+      g = values_of(*reinterpret_cast<const uint2*>(z), s[0]);
+      u = values_of(*reinterpret_cast<const uint2*>(z + a.N), s[a.groups]);
+    } else {
+      const elem* z = static_cast<const elem*>(a.z) + row * a.z_stride + n;
+      g = R::wide(R::load(z));
+      u = R::wide(R::load(z + a.N));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float s = act_of(g[j], a.act);
+      dg[j] = v[j] * u[j] * act_slope(g[j], a.act);
+      du[j] = v[j] * s;
+      h[j] = s * u[j];
+    }
+    elem* dz = static_cast<elem*>(a.pre) + row * a.pre_stride + n;
+    R::store(dz, R::narrow(dg));
+    R::store(dz + a.N, R::narrow(du));
+    if (a.y) R::store(y, R::narrow(h));
+  } else {
+    if constexpr (EPI == kProductAct) {
+      if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)e * a.N + n));
+      if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
+      if (a.act != PW_ACT_NONE)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = act_of(v[j], a.act);
+      if (a.residual) v += R::wide(R::load(static_cast<const elem*>(a.residual) + row * a.residual_stride + n));
+    }
+    R::store(y, R::narrow(v));
+  }
+}
+
+// A tile's sums, on their way to `part` (fp32 [kRows][256], gated g's 128 columns
+// and u's) or to what becomes of them.
+template <int DT, int EPI, int MI, int WM, int WN>
+__device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x4 (&acc)[2 * MI][16 / WN], char* lds,
+                                       float* part, int wave, int lane) {
   using S = Shape<MI, WM, WN>;
   constexpr bool kGate = EPI == kProductGate;
   const int wm = wave / WN, wn = wave % WN;
   Sums sums(lds, wave, lane);
   // gated: eight lanes hold 32 columns of g and of u of two rows (four lanes each), else 64 of one row
   constexpr int kLanes = kGate ? 4 : 8;
-  const int own = lane & (kLanes - 1), n = kGate ? t.nt * kKeepGroup + wn * 32 + own * 8 : t.nt * kProdN + wn * 64 + own * 8;
+  const int own = lane & (kLanes - 1), c = (kGate ? wn * 32 : wn * 64) + own * 8, n = t.nt * (kGate ? kKeepGroup : kProdN) + c;
   // the largest |g| and |u| of each row over the tile's 128 columns: over a lane's, its pair's and the waves'
   float4* const most = reinterpret_cast<float4*>(lds + S::kWaves * Sums::kBytes);   // [2][kRows]
-  if (kGate && a.z8) {
+  if (kGate && a.z8 && !part) {
 #pragma unroll
     for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float m = 0.f;
 #pragma unroll
-        for (int c = 2 * half; c < 2 * half + 2; ++c) {
-          const floatx8 v = eight_columns(acc[2 * mi][c], acc[2 * mi + 1][c]);
-          if (t.nt * kKeepGroup + wn * 32 + c % 2 * 16 + lane / 32 * 8 < a.N) m = most_of(v, m);
+        for (int p = 2 * half; p < 2 * half + 2; ++p) {
+          const floatx8 v = eight_columns(acc[2 * mi][p], acc[2 * mi + 1][p]);
+          if (t.nt * kKeepGroup + wn * 32 + p % 2 * 16 + lane / 32 * 8 < a.N) m = most_of(v, m);
         }
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
         if (lane < 32) reinterpret_cast<float*>(most + half * S::kRows + (wm * MI + mi) * 32 + lane)[wn] = m;
@@ -63,67 +125,22 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x
     for (int i = lane / kLanes; i < 32; i += kWave / kLanes) {
       const int r = (wm * MI + mi) * 32 + i;
       if (r >= t.rows || n >= a.N) continue;
-      const int64_t row = t.row0 + r;
-      if constexpr (kGate) {
-        const floatx8 g = sums.get(i, own), u = sums.get(i, 4 + own);
-        floatx8 h;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = act_of(g[j], a.act) * u[j];
-        R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
-        if (a.z8) {
-          const float4 mg = most[r], mu = most[S::kRows + r];
-          const float sg = scale_of(fmaxf(fmaxf(mg.x, mg.y), fmaxf(mg.z, mg.w)));
-          const float su = scale_of(fmaxf(fmaxf(mu.x, mu.y), fmaxf(mu.z, mu.w)));
-          if (wn == 0 && own == 0) {
-            float* s = a.z_scale + row * 2 * a.groups + t.nt;
-            s[0] = sg;
-            s[a.groups] = su;
-          }
-          uint8_t* z = static_cast<uint8_t*>(a.z) + row * a.z_stride + n;
-          *reinterpret_cast<uint2*>(z) = codes_of(g, sg);
-          *reinterpret_cast<uint2*>(z + a.N) = codes_of(u, su);
-        } else if (a.z) {
-          elem* z = static_cast<elem*>(a.z) + row * a.z_stride + n;
-          R::store_once(z, R::narrow(g));
-          R::store_once(z + a.N, R::narrow(u));
-        }
-      } else {
-        floatx8 v = sums.get(i, own);
-        if constexpr (EPI == kProductAct) {
-          if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)t.e * a.N + n));
-          if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
-          if (a.act != PW_ACT_NONE)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = act_of(v[j], a.act);
-          if (a.residual) v += R::wide(R::load(static_cast<const elem*>(a.residual) + row * a.residual_stride + n));
-        }
-        if constexpr (EPI == kProductGateGrad) {
-          floatx8 g, u, dg, du, h;
-          if (a.z8) {
-            const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
-            const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
-            g = values_of(*reinterpret_cast<const uint2*>(z), s[0]);
-            u = values_of(*reinterpret_cast<const uint2*>(z + a.N), s[a.groups]);
-          } else {
-            const elem* z = static_cast<const elem*>(a.z) + row * a.z_stride + n;
-            g = R::wide(R::load(z));
-            u = R::wide(R::load(z + a.N));
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float s = act_of(g[j], a.act);
-            dg[j] = v[j] * u[j] * act_slope(g[j], a.act);
-            du[j] = v[j] * s;
-            h[j] = s * u[j];
-          }
-          elem* dz = static_cast<elem*>(a.pre) + row * a.pre_stride + n;
-          R::store(dz, R::narrow(dg));
-          R::store(dz + a.N, R::narrow(du));
-          if (a.y) R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(h));
-        } else {
-          R::store(static_cast<elem*>(a.y) + row * a.y_stride + n, R::narrow(v));
-        }
+      const floatx8 v = sums.get(i, own);
+      floatx8 u = v;
+      if constexpr (kGate) u = sums.get(i, 4 + own);
+      if (part) {
+        float* to = part + r * kProdN + c;
+        *reinterpret_cast<floatx8*>(to) = v;
+        if constexpr (kGate) *reinterpret_cast<floatx8*>(to + kKeepGroup) = u;
+        continue;
       }
+      float sv = 0.f, su = 0.f;
+      if (kGate && a.z8) {
+        const float4 mg = most[r], mu = most[S::kRows + r];
+        sv = scale_of(fmaxf(fmaxf(mg.x, mg.y), fmaxf(mg.z, mg.w)));
+        su = scale_of(fmaxf(fmaxf(mu.x, mu.y), fmaxf(mu.z, mu.w)));
+      }
+      emit<DT, EPI>(a, t.e, t.row0 + r, n, v, u, sv, su);
     }
   }
 }
@@ -133,50 +150,117 @@ __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), 2) void product_kern
   using S = Shape<MI, WM, WN>;
   constexpr bool kBack = EPI == kProductBack || EPI == kProductGateGrad;
   __shared__ __align__(1024) char lds[S::kLds];
-  const Tile t = find_tile<S::kRows>(a.offsets, a.E, a.S, a.NT);
-  if (t.rows <= 0) return;
+  const TileScan<S::kRows> scan(a.offsets, a.E, a.S);
+  const int all_steps = (a.K + kProdK - 1) / kProdK;
+  const Rounds rounds((unsigned)scan.tiles * (unsigned)a.NT, all_steps, a.part != nullptr);
+  unsigned id = blockIdx.x;
+  int k0 = 0, k1 = a.K;
+  float* part = nullptr;
+  if (id < (rounds.whole + 7) / 8 * 8) {
+    const unsigned each_xcd = (rounds.whole + 7) / 8, i = id / 8;
+    id = (id % 8) * each_xcd + i;
+    if (id >= rounds.whole) return;
+  } else {
+    const unsigned p = id - (rounds.whole + 7) / 8 * 8, of = p / rounds.parts, which = p - of * rounds.parts;
+    if (of >= rounds.rest) return;
+    id = rounds.whole + of;
+    k0 = (int)(all_steps * which / rounds.parts) * kProdK;
+    k1 = min((int)(all_steps * (which + 1) / rounds.parts) * kProdK, a.K);
+    part = a.part + (int64_t)p * (S::kRows * kProdN);
+  }
+  const Tile t = scan.at(id, a.NT);
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
   const int wm = wave / WN, wn = wave % WN;
-  const char* x = static_cast<const char*>(a.x) + (int64_t)t.row0 * a.x_stride * 2;
+  const char* x = static_cast<const char*>(a.x) + ((int64_t)t.row0 * a.x_stride + k0) * 2;
   const char* w = static_cast<const char*>(a.w) + (int64_t)t.e * a.w_expert * 2;
 
   RowsOperand<S::kRows, S::kWaves> xo;
-  xo.init(x, x, a.K, wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
+  xo.init(x, x, k1 - k0, wave, lane, [&](int r) { return (uint32_t)min(r, t.rows - 1) * (uint32_t)(a.x_stride * 2); });
   f32x4 acc[S::RI][S::CJ];
-  const int steps = (a.K + kProdK - 1) / kProdK, live = (t.rows - wm * MI * 32 + 15) / 16;
+  const int steps = (k1 - k0 + kProdK - 1) / kProdK, live = (t.rows - wm * MI * 32 + 15) / 16;
   if constexpr (kBack) {
     ColsOperand<kProdN, S::kWaves> wo;
-    wo.init(w + (int64_t)t.nt * kProdN * 2, a.K, wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
+    wo.init(w + ((int64_t)k0 * a.N + t.nt * kProdN) * 2, k1 - k0, wave, lane, (int64_t)a.N * 2, (a.N - t.nt * kProdN + 7) / 8);
     sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, false, false, true, S::kXBuffers>(acc, lds, steps, live, wave, wm, wn, lane,
                                                                                    xo, wo);
   } else {
     // gated: rows of g, then the same rows of u, which have a base of their own
     constexpr int kTile = EPI == kProductGate ? kKeepGroup : kProdN;
     const int n0 = t.nt * kTile, last = a.N - 1 - n0;
-    w += (int64_t)n0 * a.K * 2;
+    w += ((int64_t)n0 * a.K + k0) * 2;
     RowsOperand<kProdN, S::kWaves, EPI == kProductGate> wo;
-    wo.init(w, w + (int64_t)a.N * a.K * 2, a.K, wave, lane,
+    wo.init(w, w + (int64_t)a.N * a.K * 2, k1 - k0, wave, lane,
             [&](int r) { return (uint32_t)min(r & (kTile - 1), last) * (uint32_t)(a.K * 2); });
     sum_steps<DT, S::RI, S::CJ, S::kRows, kProdN, EPI == kProductGate, false, false, S::kXBuffers>(acc, lds, steps, live, wave, wm, wn, lane,
                                                                                    xo, wo);
   }
-  finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, wave, lane);
+  finish<DT, EPI, MI, WM, WN>(a, t, acc, lds, part, wave, lane);
+}
+
+// The tiles that were cut: a block has 16 rows of one, sixteen lanes a row.
+template <int DT, int EPI, int ROWS>
+__global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
+  constexpr bool kGate = EPI == kProductGate;
+  const TileScan<ROWS> scan(a.offsets, a.E, a.S);
+  const Rounds rounds((unsigned)scan.tiles * (unsigned)a.NT, (a.K + kProdK - 1) / kProdK, true);
+  const unsigned of = blockIdx.x / (ROWS / 16);
+  if (of >= rounds.rest) return;
+  const Tile t = scan.at(rounds.whole + of, a.NT);
+  const int r = (int)(blockIdx.x % (ROWS / 16)) * 16 + (int)threadIdx.x / 16, lane = (int)threadIdx.x & 15;
+  if (r >= t.rows) return;
+  const float* from = a.part + (int64_t)of * rounds.parts * (ROWS * kProdN) + r * kProdN;
+  floatx8 v[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const float* p = from + half * 128 + lane * 8;
+    v[half] = *reinterpret_cast<const floatx8*>(p);
+    for (unsigned i = 1; i < rounds.parts; ++i) v[half] += *reinterpret_cast<const floatx8*>(p + (int64_t)i * (ROWS * kProdN));
+  }
+  if constexpr (kGate) {
+    const int n = t.nt * kKeepGroup + lane * 8;
+    const bool in = n < a.N;
+    float sv = 0.f, su = 0.f;
+    if (a.z8) {
+      sv = in ? most_of(v[0], 0.f) : 0.f;   // over the sixteen lanes of the row
+      su = in ? most_of(v[1], 0.f) : 0.f;
+#pragma unroll
+      for (int d = 1; d < 16; d *= 2) {
+        sv = fmaxf(sv, __shfl_xor(sv, d, kWave));
+        su = fmaxf(su, __shfl_xor(su, d, kWave));
+      }
+      sv = scale_of(sv);
+      su = scale_of(su);
+    }
+    if (in) emit<DT, EPI>(a, t.e, t.row0 + r, n, v[0], v[1], sv, su);
+  } else {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int n = t.nt * kProdN + half * 128 + lane * 8;
+      if (n < a.N) emit<DT, EPI>(a, t.e, t.row0 + r, n, v[half], v[half], 0.f, 0.f);
+    }
+  }
 }
 
 template <int DT, int EPI, int MI, int WM, int WN>
 hipError_t run(ProductArgs a, hipStream_t s) {
   using Sh = Shape<MI, WM, WN>;
   a.NT = EPI == kProductGate ? (a.N + kKeepGroup - 1) / kKeepGroup : (a.N + kProdN - 1) / kProdN;
-  const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, Sh::kRows), a.NT);
+  // cut only where a few steps are saved at least
+  const bool cut = a.part && (a.K + kProdK - 1) / kProdK >= 40 && Sh::kRows == 256;
+  if (!cut) a.part = nullptr;
+  const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, Sh::kRows), a.NT) + (cut ? kNumCUs : 0);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((product_kernel<DT, EPI, MI, WM, WN>), dim3((unsigned)grid), dim3(Sh::kThreads), 0, s, a);
+  if constexpr (Sh::kRows == 256)
+    if (cut)
+      hipLaunchKernelGGL((join_kernel<DT, EPI, Sh::kRows>), dim3(kNumCUs / 2 * (Sh::kRows / 16)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT, int EPI>
 hipError_t pick(const ProductArgs& a, hipStream_t s) {
   const int64_t experts = a.S < a.E ? a.S : a.E, mean = a.S / (experts > 0 ? experts : 1);
-  if (mean > 160) return run<DT, EPI, 4, 2, 4>(a, s);
+  if (a.S >= (int64_t)kWideRows * a.E) return run<DT, EPI, 4, 2, 4>(a, s);
   if (mean > 80) return run<DT, EPI, 2, 2, 4>(a, s);
   if (mean > 32) return run<DT, EPI, 2, 1, 4>(a, s);
   return run<DT, EPI, 1, 1, 4>(a, s);

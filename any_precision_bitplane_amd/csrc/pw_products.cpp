@@ -67,18 +67,23 @@ pw_status run_product(const ProductArgs& a, int dtype, int kind, void* stream) {
 }
 
 size_t dz_bytes(int64_t S, int64_t N) { return align_up((size_t)S * (size_t)N * 2, kAlign); }
+size_t dz_sum_bytes(int E, int64_t S, int N) { return align_up(sizeof(float) * dz_part_floats(E, S, N), kAlign); }
+size_t h_bytes(int64_t S, int64_t I) { return align_up((size_t)S * (size_t)I * 2 + 1, kAlign); }
+
+// The scratch of cut tiles at `at`, or null where none is set apart for S rows.
+float* parts_at(uint8_t* at, int E, int64_t S) { return product_part_bytes(E, S) ? reinterpret_cast<float*>(at) : nullptr; }
 
 }  // namespace
 
 extern "C" {
 
 size_t pw_moe_product_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
-  return check_product(E, S_max, N, K) == PW_OK ? kAlign : 0;
+  return check_product(E, S_max, N, K) == PW_OK ? kAlign + product_part_bytes(E, S_max) : 0;
 }
 
 size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
   if (check_product(E, S_max, N, K) != PW_OK) return 0;
-  return dz_bytes(S_max, N) + align_up(sizeof(float) * dz_part_floats(E, S_max, N), kAlign);
+  return dz_bytes(S_max, N) + dz_sum_bytes(E, S_max, N) + product_part_bytes(E, S_max);
 }
 
 pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* x, int64_t x_stride,
@@ -106,6 +111,7 @@ pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dty
   a.pre = pre; a.pre_stride = pre_stride;
   a.y = y; a.y_stride = y_stride;
   a.act = act;
+  a.part = parts_at(static_cast<uint8_t*>(workspace), E, S);
   return run_product(a, dtype, kProductAct, stream);
 }
 
@@ -150,6 +156,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
     a.x = dz; a.x_stride = dz_stride;
     a.w = w; a.w_expert = (int64_t)N * K;
     a.y = dx; a.y_stride = dx_stride;
+    a.part = parts_at(ws + dz_bytes(S, N) + dz_sum_bytes(E, S, N), E, S);
     PW_TRY(run_product(a, dtype, kProductBack, stream));
   }
   if (!dw) return PW_OK;
@@ -164,12 +171,13 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
 
 size_t pw_moe_ffn_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
   if (check_ffn(shape, S_max) != PW_OK) return 0;
-  return align_up((size_t)S_max * (size_t)shape->inter * 2 + 1, kAlign);
+  return h_bytes(S_max, shape->inter) + product_part_bytes(shape->num_experts, S_max);
 }
 
 size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
   if (check_ffn(shape, S_max) != PW_OK) return 0;
-  return dz_bytes(S_max, 2 * (int64_t)shape->inter) + align_up((size_t)S_max * (size_t)shape->inter * 2 + 1, kAlign);
+  return dz_bytes(S_max, 2 * (int64_t)shape->inter) + h_bytes(S_max, shape->inter) +
+         product_part_bytes(shape->num_experts, S_max);
 }
 
 pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const void* x, int64_t x_stride,
@@ -197,6 +205,7 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const 
   a.z = z; a.z_stride = z_stride;
   a.z_scale = z_scale; a.groups = kept_groups(I);
   a.z8 = z && z_dtype == PW_E4M3;
+  a.part = parts_at(static_cast<uint8_t*>(workspace) + h_bytes(S, I), E, S);
   PW_TRY(run_product(a, dtype, kProductGate, stream));
   ProductArgs d{};
   d.E = E; d.S = S; d.N = H; d.K = I;
@@ -205,6 +214,7 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const 
   d.w = w_down; d.w_expert = (int64_t)I * H;
   d.y = y; d.y_stride = y_stride;
   d.act = PW_ACT_NONE;
+  d.part = a.part;
   return run_product(d, dtype, kProductAct, stream);
 }
 
@@ -232,6 +242,7 @@ pw_status pw_moe_ffn_backward(const pw_moe_shape* shape, int32_t S, int32_t dtyp
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* dz = static_cast<uint8_t*>(workspace);
   uint8_t* h = dz + dz_bytes(S, 2 * (int64_t)I);
+  float* const part = parts_at(h + h_bytes(S, I), E, S);
   if (S > 0 && (dx || dw_gate_up || dw_down)) {
     ProductArgs a{};
     a.E = E; a.S = S; a.N = I; a.K = H;
@@ -244,6 +255,7 @@ pw_status pw_moe_ffn_backward(const pw_moe_shape* shape, int32_t S, int32_t dtyp
     a.z = const_cast<void*>(z); a.z_stride = z_stride;
     a.z_scale = const_cast<float*>(z_scale); a.groups = kept_groups(I);
     a.z8 = z_dtype == PW_E4M3;
+    a.part = part;
     PW_TRY(run_product(a, dtype, kProductGateGrad, stream));
   }
   OuterArgs o{};
@@ -263,6 +275,7 @@ pw_status pw_moe_ffn_backward(const pw_moe_shape* shape, int32_t S, int32_t dtyp
     a.x = dz; a.x_stride = 2 * (int64_t)I;
     a.w = w_gate_up; a.w_expert = 2 * (int64_t)I * H;
     a.y = dx; a.y_stride = dx_stride;
+    a.part = part;
     PW_TRY(run_product(a, dtype, kProductBack, stream));
   }
   if (!dw_gate_up) return PW_OK;

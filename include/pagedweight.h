@@ -572,7 +572,7 @@ size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape /* host */,
  *              scale NaN and NaN codes.  NULL otherwise.
  *              y comes from the unrounded gate and up in either case.
  *   y          [S][H], overwritten
- * Two launches.  S == 0 returns PW_OK and enqueues nothing. */
+ * Two to four launches.  S == 0 returns PW_OK and enqueues nothing. */
 pw_status pw_moe_ffn(const pw_moe_shape* shape /* host */, int32_t S, int32_t dtype, const void* x, int64_t x_stride,
                      const int32_t* offsets, const void* w_gate_up, const void* w_down, int32_t act, int32_t z_dtype,
                      void* z, int64_t z_stride, float* z_scale, void* y, int64_t y_stride, void* workspace,
@@ -587,7 +587,7 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape /* host */, int32_t S, int32_t dt
  *              (x may be NULL then)
  *   dw_down    [E][H][I], the same, or NULL
  *   w_gate_up  may be NULL without dx
- * Up to four launches.  S == 0 sets dw_gate_up and dw_down to zero. */
+ * Up to six launches.  S == 0 sets dw_gate_up and dw_down to zero. */
 pw_status pw_moe_ffn_backward(const pw_moe_shape* shape /* host */, int32_t S, int32_t dtype, const void* dy,
                               int64_t dy_stride, const void* x, int64_t x_stride, const int32_t* offsets,
                               const void* w_gate_up, const void* w_down, int32_t act, int32_t z_dtype, const void* z,

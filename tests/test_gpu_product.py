@@ -107,7 +107,7 @@ SIZES = [  # E, S, N, K, offsets
     (1, 1, 8, 8, False), (1, 3, 264, 72, False), (1, 17, 48, 264, True), (1, 40, 1032, 136, False),
     (1, 49, 264, 64, False), (1, 100, 520, 200, False), (1, 129, 256, 320, True), (1, 513, 776, 72, False),
     (5, 4, 64, 64, True), (60, 16, 96, 544, True), (60, 300, 136, 128, True), (8, 500, 264, 72, True),
-    (7, 630, 504, 136, True), (3, 1000, 248, 1000, True), (256, 700, 40, 56, True), (2, 1537, 1024, 136, True),
+    (7, 630, 504, 136, True), (2, 600, 328, 2696, True), (1, 4100, 4104, 2568, False), (3, 1000, 248, 1000, True), (256, 700, 40, 56, True), (2, 1537, 1024, 136, True),
 ]
 IDS = [f"E{e}-S{s}-N{n}-K{k}" for e, s, n, k, _ in SIZES]
 
@@ -220,7 +220,7 @@ def test_product_backward_through_the_activation(torch, E, S, N, K, name, act):
 FFN = [  # E, S, H, I, ragged
     (1, 1, 64, 32, False), (1, 1, 2048, 352, False), (1, 20, 96, 160, True), (60, 16, 256, 96, True),
     (8, 32, 256, 512, True), (8, 200, 96, 160, True), (5, 400, 160, 288, True), (1, 130, 128, 128, False),
-    (3, 900, 256, 416, True), (256, 300, 32, 32, True),
+    (3, 900, 256, 416, True), (2, 700, 2624, 288, True), (2, 500, 160, 2720, True), (256, 300, 32, 32, True),
 ]
 FFN_IDS = [f"E{e}-S{s}-H{h}-I{i}" for e, s, h, i, _ in FFN]
 
