@@ -449,15 +449,40 @@ struct ProductArgs {
   float* z_scale;             // [S][2 groups], of 8-bit z
   int groups;
   bool z8;
-  float* part;                // kProductPartBytes of scratch for tiles that are cut, or null
+  float* part;                // product_part_bytes of scratch for tiles that are cut, or null
   int NT;                     // set by the launch: column tiles
 };
-// Scratch of the products of up to S rows: the sums of up to kNumCUs parts of
-// tiles of 256 x 256, where tiles of 256 rows are used.
-constexpr int kWideRows = 160;   // mean rows of an expert from which on they are
-constexpr size_t kProductPartBytes = (size_t)kNumCUs * 256 * 256 * sizeof(float);
-inline size_t product_part_bytes(int E, int64_t S) { return S >= (int64_t)kWideRows * E ? kProductPartBytes : 0; }
+// Rows of a tile: 256 from a mean of kWideRows rows an expert on, below 128, 64 or
+// 32.  Where tiles of 256 would be fewer than a quarter of the CUs, 32 rows and
+// the reduction cut are faster (fp16, one expert, us: S 511, N = K = 2048 22 of 36;
+// S 256, N = K = 4096 26 of 34; S 128 24 of 28), up to three eighths 128 rows
+// (S 1024 47 of 54).  As many blocks run together as have tiles cut into parts,
+// whose sums a call needs scratch for.
+constexpr int kWideRows = 160, kMidRows = 80, kNarrowRows = 32;
+constexpr int kProdParts = 16;   // most parts of a tile
+constexpr unsigned product_blocks(int rows) { return rows <= 64 ? 2 * kNumCUs : kNumCUs; }
+inline int product_mean_rows(int E, int64_t S) {
+  return S >= (int64_t)kWideRows * E ? 256 : S > (int64_t)kMidRows * E ? 128 : S > (int64_t)kNarrowRows * E ? 64 : 32;
+}
+inline int product_rows(int E, int64_t S, int64_t NT) {
+  const int rows = product_mean_rows(E, S);
+  const int64_t wide = ((S + 255) / 256 + (E > 1 ? (S < E ? S : E) : 0)) * NT;
+  return wide < kNumCUs / 4 ? 32 : rows == 256 && wide < kNumCUs * 3 / 8 ? 128 : rows;
+}
+inline size_t product_part_bytes(int E, int64_t S) {
+  // 64 MB, 32, 32 and 16: no fewer rows, and no smaller tiles, have more
+  const int rows = product_mean_rows(E, S);
+  return (size_t)product_blocks(rows) * rows * 256 * sizeof(float);
+}
 hipError_t launch_product(const ProductArgs& a, int dtype, int kind, hipStream_t s);
+// Few rows take the form without tiles: up to kFewRows an expert on average, or up
+// to 64 with matrices so small that a call is as long as its launches.  Against
+// tiles (us): one expert, H 2048, I 5632, 8 rows 27 of 43, 32 rows 45 of 46, 64
+// rows 59 of 51; H 4096, I 14336, 8 rows 84 of 89, 16 rows 98 of 90; N = K = 1024,
+// 64 rows 8 of 16; E 60, H 2048, I 1408, 256 rows 228 of 215; E 8, H 4096, I 14336,
+// 128 rows 748 of 487.
+constexpr int kFewRows = 2;
+constexpr int64_t kFewWork = (int64_t)1 << 30;   // rows times an expert's matrix
 bool few_rows(const ProductArgs& a, int kind);
 hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s);
 

@@ -152,7 +152,7 @@ __global__ __launch_bounds__((Shape<MI, WM, WN>::kThreads), 2) void product_kern
   __shared__ __align__(1024) char lds[S::kLds];
   const TileScan<S::kRows> scan(a.offsets, a.E, a.S);
   const int all_steps = (a.K + kProdK - 1) / kProdK;
-  const Rounds rounds((unsigned)scan.tiles * (unsigned)a.NT, all_steps, a.part != nullptr);
+  const Rounds<S::kRows> rounds((unsigned)scan.tiles * (unsigned)a.NT, all_steps, a.part != nullptr);
   unsigned id = blockIdx.x;
   int k0 = 0, k1 = a.K;
   float* part = nullptr;
@@ -202,7 +202,7 @@ template <int DT, int EPI, int ROWS>
 __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
   constexpr bool kGate = EPI == kProductGate;
   const TileScan<ROWS> scan(a.offsets, a.E, a.S);
-  const Rounds rounds((unsigned)scan.tiles * (unsigned)a.NT, (a.K + kProdK - 1) / kProdK, true);
+  const Rounds<ROWS> rounds((unsigned)scan.tiles * (unsigned)a.NT, (a.K + kProdK - 1) / kProdK, true);
   const unsigned of = blockIdx.x / (ROWS / 16);
   if (of >= rounds.rest) return;
   const Tile t = scan.at(rounds.whole + of, a.NT);
@@ -245,25 +245,31 @@ template <int DT, int EPI, int MI, int WM, int WN>
 hipError_t run(ProductArgs a, hipStream_t s) {
   using Sh = Shape<MI, WM, WN>;
   a.NT = EPI == kProductGate ? (a.N + kKeepGroup - 1) / kKeepGroup : (a.N + kProdN - 1) / kProdN;
-  // cut only where a few steps are saved at least
-  const bool cut = a.part && (a.K + kProdK - 1) / kProdK >= 40 && Sh::kRows == 256;
+  // Cut where it can save what its launch costs: with one round or less (the
+  // host sees no more than a bound of a ragged call's tiles), or a long reduction.
+  const int64_t tiles = product_row_tiles(a.offsets, a.E, a.S, Sh::kRows) * a.NT, most = product_blocks(Sh::kRows);
+  const int steps = (a.K + kProdK - 1) / kProdK;
+  const bool cut = a.part && (a.offsets ? steps >= 40 || (tiles <= most && steps >= 8) : tiles % most && steps >= 6);
   if (!cut) a.part = nullptr;
-  const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, Sh::kRows), a.NT) + (cut ? kNumCUs : 0);
+  const int64_t grid = (tiles + 7) / 8 * 8 + (cut ? most : 0);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((product_kernel<DT, EPI, MI, WM, WN>), dim3((unsigned)grid), dim3(Sh::kThreads), 0, s, a);
-  if constexpr (Sh::kRows == 256)
-    if (cut)
-      hipLaunchKernelGGL((join_kernel<DT, EPI, Sh::kRows>), dim3(kNumCUs / 2 * (Sh::kRows / 16)), dim3(256), 0, s, a);
+  if (cut) {
+    const int64_t joined = tiles < most / 2 ? tiles : most / 2;
+    hipLaunchKernelGGL((join_kernel<DT, EPI, Sh::kRows>), dim3((unsigned)joined * (Sh::kRows / 16)), dim3(256), 0, s, a);
+  }
   return hipGetLastError();
 }
 
 template <int DT, int EPI>
 hipError_t pick(const ProductArgs& a, hipStream_t s) {
-  const int64_t experts = a.S < a.E ? a.S : a.E, mean = a.S / (experts > 0 ? experts : 1);
-  if (a.S >= (int64_t)kWideRows * a.E) return run<DT, EPI, 4, 2, 4>(a, s);
-  if (mean > 80) return run<DT, EPI, 2, 2, 4>(a, s);
-  if (mean > 32) return run<DT, EPI, 2, 1, 4>(a, s);
-  return run<DT, EPI, 1, 1, 4>(a, s);
+  const int tile = EPI == kProductGate ? kKeepGroup : kProdN;
+  switch (product_rows(a.E, a.S, (a.N + tile - 1) / tile)) {
+    case 256: return run<DT, EPI, 4, 2, 4>(a, s);
+    case 128: return run<DT, EPI, 2, 2, 4>(a, s);
+    case 64: return run<DT, EPI, 2, 1, 4>(a, s);
+    default: return run<DT, EPI, 1, 1, 4>(a, s);
+  }
 }
 
 template <int DT>

@@ -11,7 +11,7 @@ namespace pw {
 namespace {
 
 constexpr int kFewWaves = 8;
-constexpr int kFewAhead = 4;   // pieces of 64 steps in flight
+constexpr int kFewAhead = 2;   // pieces of 64 steps in flight
 
 // RT: tiles of 16 rows of x
 template <int DT, int EPI, int RT>
@@ -25,7 +25,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void few_kernel(ProductArgs a) {
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
   const int n0 = t.nt * 16, r = lane & 15;
   const int K = a.K;
-  // lane l holds row l % 16 and 16 neighbouring steps of a piece, in two operands: the same ones of x and of W
+  // lane l holds row l % 16 and steps 8 (l / 16) .. + 7 and 32 more of a piece, the same ones of x and of W
   const char* w[NF];
   const char* x[RT];
   const int col = min(n0 + r, a.N - 1);
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void few_kernel(ProductArgs a) {
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const s16x8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int own = (lane >> 4) * 16;
+  const int own = (lane >> 4) * 8;
   constexpr int kStep = kFewWaves * 64;
   for (int base = wave * 64; base < K; base += kStep * kFewAhead) {
     s16x8 wf[kFewAhead][NF][2], xf[kFewAhead][RT][2];
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void few_kernel(ProductArgs a) {
     for (int u = 0; u < kFewAhead; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int k = base + u * kStep + own + 8 * h;
+        const int k = base + u * kStep + own + 32 * h;
         const bool in = k < K;
         const int at = in ? k * 2 : 0;
 #pragma unroll
@@ -63,6 +63,7 @@ __global__ __launch_bounds__(kFewWaves * kWave) void few_kernel(ProductArgs a) {
           if (!in) xf[u][i][h] = zero;
         }
       }
+    __builtin_amdgcn_sched_barrier(0);   // every load before the first product
 #pragma unroll
     for (int u = 0; u < kFewAhead; ++u)
 #pragma unroll
@@ -130,12 +131,11 @@ hipError_t pick(const ProductArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Rows that the tiles of pw_product.hip would mostly be empty for, and no 8-bit
-// copies (a block has 16 columns of a group of 128).
+// No 8-bit copies: a block has 16 columns of a group of 128.
 bool few_rows(const ProductArgs& a, int kind) {
   if ((kind != kProductAct && kind != kProductGate) || a.z8) return false;
-  const int64_t experts = a.S < a.E ? a.S : a.E;
-  return a.S <= 48 * experts;
+  const int64_t experts = a.S < a.E ? a.S : a.E, S = a.S;
+  return S <= kFewRows * experts || (S <= 64 * experts && S * a.N * a.K * (kind == kProductGate ? 2 : 1) <= kFewWork);
 }
 
 hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s) {

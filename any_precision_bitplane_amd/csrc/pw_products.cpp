@@ -70,15 +70,18 @@ size_t dz_bytes(int64_t S, int64_t N) { return align_up((size_t)S * (size_t)N * 
 size_t dz_sum_bytes(int E, int64_t S, int N) { return align_up(sizeof(float) * dz_part_floats(E, S, N), kAlign); }
 size_t h_bytes(int64_t S, int64_t I) { return align_up((size_t)S * (size_t)I * 2 + 1, kAlign); }
 
-// The scratch of cut tiles at `at`, or null where none is set apart for S rows.
-float* parts_at(uint8_t* at, int E, int64_t S) { return product_part_bytes(E, S) ? reinterpret_cast<float*>(at) : nullptr; }
+// Scratch of a forward call's cut tiles: none for the few rows whose products have no tiles.
+size_t forward_part_bytes(int E, int64_t S) { return S > (int64_t)kFewRows * E ? product_part_bytes(E, S) : 0; }
+float* forward_parts(uint8_t* at, int E, int64_t S) {
+  return forward_part_bytes(E, S) ? reinterpret_cast<float*>(at) : nullptr;
+}
 
 }  // namespace
 
 extern "C" {
 
 size_t pw_moe_product_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
-  return check_product(E, S_max, N, K) == PW_OK ? kAlign + product_part_bytes(E, S_max) : 0;
+  return check_product(E, S_max, N, K) == PW_OK ? kAlign + forward_part_bytes(E, S_max) : 0;
 }
 
 size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
@@ -111,7 +114,7 @@ pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dty
   a.pre = pre; a.pre_stride = pre_stride;
   a.y = y; a.y_stride = y_stride;
   a.act = act;
-  a.part = parts_at(static_cast<uint8_t*>(workspace), E, S);
+  a.part = forward_parts(static_cast<uint8_t*>(workspace), E, S);
   return run_product(a, dtype, kProductAct, stream);
 }
 
@@ -156,7 +159,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
     a.x = dz; a.x_stride = dz_stride;
     a.w = w; a.w_expert = (int64_t)N * K;
     a.y = dx; a.y_stride = dx_stride;
-    a.part = parts_at(ws + dz_bytes(S, N) + dz_sum_bytes(E, S, N), E, S);
+    a.part = reinterpret_cast<float*>(ws + dz_bytes(S, N) + dz_sum_bytes(E, S, N));
     PW_TRY(run_product(a, dtype, kProductBack, stream));
   }
   if (!dw) return PW_OK;
@@ -171,7 +174,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
 
 size_t pw_moe_ffn_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
   if (check_ffn(shape, S_max) != PW_OK) return 0;
-  return h_bytes(S_max, shape->inter) + product_part_bytes(shape->num_experts, S_max);
+  return h_bytes(S_max, shape->inter) + forward_part_bytes(shape->num_experts, S_max);
 }
 
 size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
@@ -205,7 +208,7 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const 
   a.z = z; a.z_stride = z_stride;
   a.z_scale = z_scale; a.groups = kept_groups(I);
   a.z8 = z && z_dtype == PW_E4M3;
-  a.part = parts_at(static_cast<uint8_t*>(workspace) + h_bytes(S, I), E, S);
+  a.part = forward_parts(static_cast<uint8_t*>(workspace) + h_bytes(S, I), E, S);
   PW_TRY(run_product(a, dtype, kProductGate, stream));
   ProductArgs d{};
   d.E = E; d.S = S; d.N = H; d.K = I;
@@ -242,7 +245,7 @@ pw_status pw_moe_ffn_backward(const pw_moe_shape* shape, int32_t S, int32_t dtyp
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* dz = static_cast<uint8_t*>(workspace);
   uint8_t* h = dz + dz_bytes(S, 2 * (int64_t)I);
-  float* const part = parts_at(h + h_bytes(S, I), E, S);
+  float* const part = reinterpret_cast<float*>(h + h_bytes(S, I));
   if (S > 0 && (dx || dw_gate_up || dw_down)) {
     ProductArgs a{};
     a.E = E; a.S = S; a.N = I; a.K = H;
