@@ -495,8 +495,7 @@ struct OuterArgs {
   const void* q;              // [S][N]
   int64_t q_stride;
   void* out;                  // [E][M][N]
-  int MT, NT;                 // set by the launch
-  unsigned tiles;
+  int MT, NT;                 // set by the launch: tiles of rows and of columns
 };
 hipError_t launch_outer(const OuterArgs& a, int dtype, hipStream_t s);
 

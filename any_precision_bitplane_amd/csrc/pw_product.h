@@ -221,12 +221,12 @@ struct RowsOperand {
   }
 };
 
-// The same of a tile of 64 reduction rows of C contiguous columns; a copy of a
+// The same of a tile of KS reduction rows of C contiguous columns; a copy of a
 // wave covers 512 / C rows.
 __device__ __forceinline__ int cols_place(int k) { return 2 * (k & 3) + (k & 8); }   // piece c of row k lies at place c ^ this
-template <int C, int WAVES>
+template <int C, int WAVES, int KS = kProdK>
 struct ColsOperand {
-  static constexpr int kCopies = kProdK * C / 512 / WAVES, kApart = WAVES * 1024;
+  static constexpr int kCopies = KS * C / 512 / WAVES, kApart = WAVES * 1024;
   uint32_t at[kCopies];
   int first, K;
   const char* base;
@@ -236,7 +236,7 @@ struct ColsOperand {
   __device__ __forceinline__ void init(const char* base_, int K_, int wave, int lane, int64_t row_bytes, int pieces) {
     base = base_;
     K = K_;
-    step_bytes = kProdK * row_bytes;
+    step_bytes = KS * row_bytes;
     first = wave * (512 / C) + lane / (C / 8);
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
@@ -245,9 +245,9 @@ struct ColsOperand {
     }
   }
   __device__ __forceinline__ void begin(int t) {
-    const int left = K - t * kProdK;
+    const int left = K - t * KS;
     rs = copy_rsrc(base + t * step_bytes);
-    if (left < kProdK)
+    if (left < KS)
 #pragma unroll
       for (int i = 0; i < kCopies; ++i) at[i] = first + i * WAVES * (512 / C) < left ? at[i] : kOutOfRange;
   }
@@ -414,6 +414,86 @@ __device__ __forceinline__ void sum_steps(f32x4 (&acc)[RI][CJ], char* lds, int s
   else
     sum_live<DT, 0, RI, CJ, TM, TN, HALVES, XC, WC, XB>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
   step_barrier<0>();   // no copy is under way when LDS is used otherwise or the block ends
+}
+
+// The same for two operands that are both read transposed, over steps of 32 in
+// three buffers, so that two blocks of half the size fit a CU and one's first
+// copies and stores pass under the other's products.  (Lines of memory are whole
+// in a step of any length here: its rows are the reduction's.)
+template <int DT, int LIVE, int RI, int CJ, int TM, int TN, class XOperand, class WOperand>
+__device__ __forceinline__ void sum_short_live(f32x4 (&acc)[RI][CJ], char* lds, int steps, int wave, int wm, int wn,
+                                               int lane, XOperand& xo, WOperand& wo) {
+  constexpr int XN = XOperand::kCopies, WN = WOperand::kCopies, kCopies = XN + WN;
+  constexpr int kProducts = LIVE * CJ, kReads = LIVE ? LIVE + CJ : 0, kSlots = LIVE ? kProducts : 1;
+  constexpr int kXBytes = XN * XOperand::kApart, kBytes = kXBytes + WN * WOperand::kApart;   // of a step
+  constexpr int kReadEvery = kSlots / (kReads + 2), kCopyEvery = kSlots < kCopies ? 1 : kSlots / kCopies;
+  constexpr int kTogether = (kCopies + kSlots - 1) / kSlots;
+  const uint32_t base = lds_at(lds) + (uint32_t)wave * 1024u;
+  constexpr int kOnce = LIVE / 2, kTwice = LIVE - kOnce;
+  s16x8 xa[kOnce + 1], xb[2][kTwice + 1], w[2][CJ];
+  auto read = [&](const char* at, int set, int j) {
+    if (j < CJ) {
+      w[set][j] = read_cols<TN>(at + kXBytes, (wn * CJ + j) * 16, 0, lane);
+    } else {
+      const int i = j < CJ + kTwice ? j - CJ + kOnce : j - CJ - kTwice, r = (wm * RI + i) * 16;
+      (i < kOnce ? xa[i < kOnce ? i : 0] : xb[set][i < kOnce ? 0 : i - kOnce]) = read_cols<TM>(at, r, 0, lane);
+    }
+  };
+  step_barrier<2 * kCopies>();
+#pragma unroll
+  for (int j = 0; j < kReads; ++j) read(lds, 0, j);
+  int now = 0;   // buffer of the step
+  for (int t = 0; t < steps; t += 2)   // a last step past the end multiplies zeros
+    each<0, 2>([&](auto set) {
+      const uint32_t freed = base + (uint32_t)(now * kBytes);
+      now = now == 2 ? 0 : now + 1;
+      const char* const then = lds + now * kBytes;
+      xo.begin(t + set + 3);
+      wo.begin(t + set + 3);
+      step_barrier<kCopies>();
+      __builtin_amdgcn_sched_barrier(0);
+      each<0, kSlots>([&](auto j) {
+        constexpr int row = j / CJ;
+        if constexpr (LIVE > 0)
+          acc[row][j % CJ] = Mma<DT>::mma(w[set][j % CJ], row < kOnce ? xa[row < kOnce ? row : 0] : xb[set][row < kOnce ? 0 : row - kOnce],
+                                          acc[row][j % CJ]);
+        each<0, kReads>([&](auto i) {
+          constexpr int own = i - CJ - kTwice, slot = own >= 0 && (own + 1) * CJ - 1 > i * kReadEvery ? (own + 1) * CJ - 1 : i * kReadEvery;
+          static_assert(slot < kSlots, "a product for every read");
+          if constexpr (slot == j) read(then, 1 - set, i);
+        });
+        if constexpr (j % kCopyEvery == 0)
+          each<j / kCopyEvery * kTogether, (j / kCopyEvery + 1) * kTogether>([&](auto i) {
+            if constexpr (i < XN) xo.template copy<i>(freed);
+            else if constexpr (i < kCopies) wo.template copy<i - XN>(freed + kXBytes);
+          });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+}
+
+template <int DT, int RI, int CJ, int TM, int TN, class XOperand, class WOperand>
+__device__ __forceinline__ void sum_short_steps(f32x4 (&acc)[RI][CJ], char* lds, int steps, int live, int wave, int wm,
+                                                int wn, int lane, XOperand& xo, WOperand& wo) {
+#pragma unroll
+  for (int r = 0; r < RI; ++r)
+#pragma unroll
+    for (int c = 0; c < CJ; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (steps <= 0) return;
+  constexpr int XN = XOperand::kCopies, WN = WOperand::kCopies;
+  constexpr int kXBytes = XN * XOperand::kApart, kBytes = kXBytes + WN * WOperand::kApart;
+  const uint32_t base = lds_at(lds) + (uint32_t)wave * 1024u;
+#pragma unroll
+  for (int t = 0; t < 3; ++t) {
+    xo.begin(t);
+    wo.begin(t);
+    each<0, XN>([&](auto i) { xo.template copy<i>(base + t * kBytes); });
+    each<0, WN>([&](auto i) { wo.template copy<i>(base + t * kBytes + kXBytes); });
+  }
+  if (live > RI / 2) sum_short_live<DT, RI, RI, CJ, TM, TN>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+  else if (live > 0) sum_short_live<DT, RI / 2, RI, CJ, TM, TN>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+  else sum_short_live<DT, 0, RI, CJ, TM, TN>(acc, lds, steps, wave, wm, wn, lane, xo, wo);
+  step_barrier<0>();
 }
 
 // ----- activations ------------------------------------------------------------

@@ -13,24 +13,30 @@ namespace pw {
 
 namespace {
 
-// Tiles of T x T: 256, of eight waves, one block a CU; or 128, of four, two a CU.
-template <int T>
+// Tiles of 256 x 256 of eight waves, one block a CU; or of TM x 128 of four, in
+// steps of 32, two or more blocks a CU, which is faster for few rows an expert,
+// where a tile is mostly its first copies and its stores (E 60, 17 rows each,
+// H 2048, I 1408: 440 us for the whole gradient against 466), and where there are
+// few tiles, and slower otherwise (its tiles read half as much again: E 8, 1024
+// rows each, H 4096, I 14336 5.53 ms against 5.31).
+template <int TM, int TN>
 struct OuterShape {
-  static constexpr int WM = 2, WN = T / 64, kWaves = WM * WN, RI = T / 16 / WM, CJ = T / 16 / WN;
-  static constexpr int kBuffers = T == 256 ? 3 : 2, kLds = (kBuffers + 2) * T * kProdK * 2;
+  static constexpr bool kShort = TN == 128;
+  static constexpr int WM = 2, WN = TN / 64, kWaves = WM * WN, RI = TM / 16 / WM, CJ = TN / 16 / WN;
+  static constexpr int kStep = kShort ? 32 : kProdK, kLds = (kShort ? 3 * (TM + TN) : 3 * TM + 2 * TN) * kStep * 2;
+  static_assert(CJ == 4 && kWaves * Sums::kBytes <= kLds, "64 columns a wave");
 };
 
-template <int DT, int T>
-__global__ __launch_bounds__((OuterShape<T>::kWaves * kWave), 2) void outer_kernel(OuterArgs a) {
+template <int DT, int TM, int TN>
+__global__ __launch_bounds__((OuterShape<TM, TN>::kWaves * kWave), 2) void outer_kernel(OuterArgs a) {
   using R = Row<DT>;
   using elem = typename R::elem;
-  using Sh = OuterShape<T>;
-  static_assert(Sh::CJ == 4 && Sh::kWaves * Sums::kBytes <= Sh::kLds, "64 columns a wave");
+  using Sh = OuterShape<TM, TN>;
   __shared__ __align__(1024) char lds[Sh::kLds];
-  const unsigned each_xcd = (a.tiles + 7) / 8, i = blockIdx.x / 8, id = (blockIdx.x % 8) * each_xcd + i;
-  if (i >= each_xcd || id >= a.tiles) return;
-  const unsigned per = (unsigned)(a.MT * a.NT);
-  const int e = (int)(id / per), local = (int)(id - e * per);
+  // Every expert's tiles are dealt to the eight XCDs, in a contiguous stretch each: experts differ in their rows.
+  const unsigned per = (unsigned)(a.MT * a.NT), share = (per + 7) / 8, i = blockIdx.x / 8;
+  const int e = (int)(i / share), local = (int)(blockIdx.x % 8 * share + i - (unsigned)e * share);
+  if (local >= (int)per) return;
   const int group = local / (kProdGroup * a.NT), rem = local - group * kProdGroup * a.NT;
   const int here = min(kProdGroup, a.MT - group * kProdGroup);
   const int nt = rem / here, mt = group * kProdGroup + rem - nt * here;
@@ -40,24 +46,28 @@ __global__ __launch_bounds__((OuterShape<T>::kWaves * kWave), 2) void outer_kern
   rows = uniform(rows);
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
-  ColsOperand<T, Sh::kWaves> po, qo;
-  po.init(static_cast<const char*>(a.p) + ((int64_t)row0 * a.p_stride + mt * T) * 2, rows, wave, lane, a.p_stride * 2,
-          (a.M - mt * T + 7) / 8);
-  qo.init(static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * T) * 2, rows, wave, lane, a.q_stride * 2,
-          (a.N - nt * T + 7) / 8);
+  ColsOperand<TM, Sh::kWaves, Sh::kStep> po;
+  ColsOperand<TN, Sh::kWaves, Sh::kStep> qo;
+  po.init(static_cast<const char*>(a.p) + ((int64_t)row0 * a.p_stride + mt * TM) * 2, rows, wave, lane, a.p_stride * 2,
+          (a.M - mt * TM + 7) / 8);
+  qo.init(static_cast<const char*>(a.q) + ((int64_t)row0 * a.q_stride + nt * TN) * 2, rows, wave, lane, a.q_stride * 2,
+          (a.N - nt * TN + 7) / 8);
   f32x4 acc[Sh::RI][Sh::CJ];
-  sum_steps<DT, Sh::RI, Sh::CJ, T, T, false, true, true, Sh::kBuffers>(
-      acc, lds, (rows + kProdK - 1) / kProdK, nt * T + wn * 64 < a.N ? (a.M - mt * T - wm * Sh::RI * 16 + 15) / 16 : 0, wave,
-      wm, wn, lane, po, qo);
+  const int steps = (rows + Sh::kStep - 1) / Sh::kStep;
+  const int live = nt * TN + wn * 64 < a.N ? (a.M - mt * TM - wm * Sh::RI * 16 + 15) / 16 : 0;
+  if constexpr (Sh::kShort)
+    sum_short_steps<DT, Sh::RI, Sh::CJ, TM, TN>(acc, lds, steps, live, wave, wm, wn, lane, po, qo);
+  else
+    sum_steps<DT, Sh::RI, Sh::CJ, TM, TN, false, true, true, 3>(acc, lds, steps, live, wave, wm, wn, lane, po, qo);
   elem* out = static_cast<elem*>(a.out) + (int64_t)e * a.M * a.N;
   Sums sums(lds, wave, lane);
-  const int n = nt * T + wn * 64 + (lane & 7) * 8;
+  const int n = nt * TN + wn * 64 + (lane & 7) * 8;
 #pragma unroll
   for (int mi = 0; mi < Sh::RI / 2; ++mi) {
     sums.put(acc[2 * mi], acc[2 * mi + 1]);
 #pragma unroll
     for (int r = lane / 8; r < 32; r += 8) {
-      const int m = mt * T + (wm * (Sh::RI / 2) + mi) * 32 + r;
+      const int m = mt * TM + (wm * (Sh::RI / 2) + mi) * 32 + r;
       const floatx8 v = sums.get(r, lane & 7);
       if (m < a.M && n < a.N) R::store_once(out + (int64_t)m * a.N + n, R::narrow(v));
     }
@@ -118,22 +128,21 @@ __global__ __launch_bounds__(kDzThreads) void bias_grad_kernel(DzArgs a) {
   static_cast<elem*>(a.dbias)[(int64_t)e * a.N + c] = (elem)s;
 }
 
-template <int DT, int T>
+template <int DT, int TM, int TN>
 hipError_t run_outer(OuterArgs a, hipStream_t s) {
-  a.MT = (a.M + T - 1) / T;
-  a.NT = (a.N + T - 1) / T;
-  const int64_t tiles = (int64_t)a.E * a.MT * a.NT;
-  if (tiles > 0x7FFFFFF0) return hipErrorInvalidValue;
-  a.tiles = (unsigned)tiles;
-  hipLaunchKernelGGL((outer_kernel<DT, T>), dim3((unsigned)product_grid(tiles, 1)), dim3(OuterShape<T>::kWaves * kWave), 0,
-                     s, a);
+  a.MT = (a.M + TM - 1) / TM;
+  a.NT = (a.N + TN - 1) / TN;
+  const int64_t grid = ((int64_t)a.MT * a.NT + 7) / 8 * 8 * a.E;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((outer_kernel<DT, TM, TN>), dim3((unsigned)grid), dim3(OuterShape<TM, TN>::kWaves * kWave), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t pick_outer(const OuterArgs& a, hipStream_t s) {
-  const int64_t tiles = (int64_t)a.E * ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  return tiles >= kNumCUs ? run_outer<DT, 256>(a, s) : run_outer<DT, 128>(a, s);
+  const int64_t wide = (int64_t)a.E * ((a.M + 255) / 256) * ((a.N + 255) / 256);
+  if (wide < kNumCUs) return run_outer<DT, 128, 128>(a, s);
+  return a.S < 128ll * a.E ? run_outer<DT, 256, 128>(a, s) : run_outer<DT, 256, 256>(a, s);
 }
 
 template <int DT>
