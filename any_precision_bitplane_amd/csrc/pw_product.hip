@@ -22,14 +22,47 @@ struct Shape {
   static constexpr int kThreads = kWaves * kWave;
   static constexpr int kABytes = kRows * kProdK * 2;
   static constexpr int kXBuffers = MI * WM == 2 ? 2 : 3;   // two blocks a CU with tiles of 32 and 64 rows
-  static constexpr int kLds = kXBuffers * kABytes + 2 * kProdN * kProdK * 2;
-  static_assert(WN == 4 && kWaves * Sums::kBytes + 2 * kRows * 16 <= kLds, "LDS of what follows the products");
+  static constexpr int kCopied = kXBuffers * kABytes + 2 * kProdN * kProdK * 2;
+  static constexpr int kAfter = kWaves * (Sums::kBytes + 8 * kWave * 16);   // what follows the products
+  static constexpr int kLds = kCopied > kAfter ? kCopied : kAfter;
+  static_assert(WN == 4 && 2 * kRows * 16 <= kWaves * 8 * kWave * 16, "rows' maxima fit what waits elsewhere");
 };
+
+// What eight columns from n on of a row need besides their sums: the residual, or
+// gate and up (8 bits: their codes, and their scales).
+struct Besides {
+  uint4 first, second;
+};
+template <int EPI>
+__device__ __forceinline__ bool wants(const ProductArgs& a) {
+  return EPI == kProductGateGrad || (EPI == kProductAct && a.residual);
+}
+template <int DT, int EPI>
+__device__ __forceinline__ Besides besides(const ProductArgs& a, int64_t row, int n) {
+  Besides b{};
+  if constexpr (EPI == kProductAct) {
+    b.first = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.residual) + (row * a.residual_stride + n) * 2);
+  } else if constexpr (EPI == kProductGateGrad) {
+    if (a.z8) {
+      const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
+      const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
+      const uint2 g = *reinterpret_cast<const uint2*>(z), u = *reinterpret_cast<const uint2*>(z + a.N);
+      b.first = uint4{g.x, g.y, u.x, u.y};
+      b.second.x = __float_as_uint(s[0]);
+      b.second.y = __float_as_uint(s[a.groups]);
+    } else {
+      const char* z = static_cast<const char*>(a.z) + (row * a.z_stride + n) * 2;
+      b.first = *reinterpret_cast<const uint4*>(z);
+      b.second = *reinterpret_cast<const uint4*>(z + (int64_t)a.N * 2);
+    }
+  }
+  return b;
+}
 
 // What becomes of eight columns from n on of a row's sums v (gated: of g, and u).
 template <int DT, int EPI>
-__device__ __forceinline__ void emit(const ProductArgs& a, int e, int64_t row, int n, floatx8 v, floatx8 u, float sv,
-                                     float su) {
+__device__ __forceinline__ void emit(const ProductArgs& a, int64_t row, int n, floatx8 v, floatx8 u, float sv, float su,
+                                     floatx8 bias, const Besides& b) {
   using R = Row<DT>;
   using elem = typename R::elem;
   elem* const y = static_cast<elem*>(a.y) + row * a.y_stride + n;
@@ -55,14 +88,11 @@ __device__ __forceinline__ void emit(const ProductArgs& a, int e, int64_t row, i
   } else if constexpr (EPI == kProductGateGrad) {
     floatx8 g, dg, du, h;
     if (a.z8) {
-      const uint8_t* z = static_cast<const uint8_t*>(a.z) + row * a.z_stride + n;
-      const float* s = a.z_scale + row * 2 * a.groups + n / kKeepGroup;
-      g = values_of(*reinterpret_cast<const uint2*>(z), s[0]);
-      u = values_of(*reinterpret_cast<const uint2*>(z + a.N), s[a.groups]);
+      g = values_of(uint2{b.first.x, b.first.y}, __uint_as_float(b.second.x));
+      u = values_of(uint2{b.first.z, b.first.w}, __uint_as_float(b.second.y));
     } else {
-      const elem* z = static_cast<const elem*>(a.z) + row * a.z_stride + n;
-      g = R::wide(R::load(z));
-      u = R::wide(R::load(z + a.N));
+      g = R::wide(__builtin_bit_cast(typename R::chunk, b.first));
+      u = R::wide(__builtin_bit_cast(typename R::chunk, b.second));
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -77,15 +107,23 @@ __device__ __forceinline__ void emit(const ProductArgs& a, int e, int64_t row, i
     if (a.y) R::store(y, R::narrow(h));
   } else {
     if constexpr (EPI == kProductAct) {
-      if (a.bias) v += R::wide(R::load(static_cast<const elem*>(a.bias) + (int64_t)e * a.N + n));
+      if (a.bias) v += bias;
       if (a.pre) R::store_once(static_cast<elem*>(a.pre) + row * a.pre_stride + n, R::narrow(v));
       if (a.act != PW_ACT_NONE)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = act_of(v[j], a.act);
-      if (a.residual) v += R::wide(R::load(static_cast<const elem*>(a.residual) + row * a.residual_stride + n));
+      if (a.residual) v += R::wide(__builtin_bit_cast(typename R::chunk, b.first));
     }
     R::store(y, R::narrow(v));
   }
+}
+
+template <int DT, int EPI>
+__device__ __forceinline__ floatx8 bias_of(const ProductArgs& a, int e, int n) {
+  using R = Row<DT>;
+  if (EPI == kProductAct && a.bias && n < a.N)
+    return R::wide(R::load(static_cast<const typename R::elem*>(a.bias) + (int64_t)e * a.N + n));
+  return floatx8{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 }
 
 // A tile's sums, on their way to `part` (fp32 [kRows][256], gated g's 128 columns
@@ -118,11 +156,35 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x
       }
     __syncthreads();
   }
+  // What 32 rows need besides is requested while the 32 before are worked on, and
+  // waits in LDS, each lane's own (requested row by row, the residual and pre took
+  // the 8194 x 8192 x 2048 bf16 product from 254 us to 348).
+  constexpr bool kBesides = EPI == kProductAct || EPI == kProductGateGrad;
+  const bool want = wants<EPI>(a) && !part;
+  const floatx8 bias = bias_of<DT, EPI>(a, t.e, n);
+  uint4* const waiting = reinterpret_cast<uint4*>(lds + S::kWaves * Sums::kBytes) + wave * (8 * kWave) + lane;
+  Besides next[4];
+  auto request = [&](int mi) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int r = (wm * MI + mi) * 32 + lane / 8 + 8 * q;
+      if (r < t.rows && n < a.N) next[q] = besides<DT, EPI>(a, t.row0 + r, n);
+    }
+  };
+  if (kBesides && want) request(0);
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
     sums.put(acc[2 * mi], acc[2 * mi + 1]);
+    if (kBesides && want) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        waiting[2 * q * kWave] = next[q].first;
+        if (EPI == kProductGateGrad) waiting[(2 * q + 1) * kWave] = next[q].second;
+      }
+      if (mi + 1 < MI) request(mi + 1);
+    }
 #pragma unroll 1
-    for (int i = lane / kLanes; i < 32; i += kWave / kLanes) {
+    for (int i = lane / kLanes, q = 0; i < 32; i += kWave / kLanes, ++q) {
       const int r = (wm * MI + mi) * 32 + i;
       if (r >= t.rows || n >= a.N) continue;
       const floatx8 v = sums.get(i, own);
@@ -140,7 +202,12 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x
         sv = scale_of(fmaxf(fmaxf(mg.x, mg.y), fmaxf(mg.z, mg.w)));
         su = scale_of(fmaxf(fmaxf(mu.x, mu.y), fmaxf(mu.z, mu.w)));
       }
-      emit<DT, EPI>(a, t.e, t.row0 + r, n, v, u, sv, su);
+      Besides b{};
+      if (kBesides && want) {
+        b.first = waiting[2 * q * kWave];
+        if (EPI == kProductGateGrad) b.second = waiting[(2 * q + 1) * kWave];
+      }
+      emit<DT, EPI>(a, t.row0 + r, n, v, u, sv, su, bias, b);
     }
   }
 }
@@ -231,12 +298,14 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
       sv = scale_of(sv);
       su = scale_of(su);
     }
-    if (in) emit<DT, EPI>(a, t.e, t.row0 + r, n, v[0], v[1], sv, su);
+    if (in) emit<DT, EPI>(a, t.row0 + r, n, v[0], v[1], sv, su, v[0], Besides{});
   } else {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int n = t.nt * kProdN + half * 128 + lane * 8;
-      if (n < a.N) emit<DT, EPI>(a, t.e, t.row0 + r, n, v[half], v[half], 0.f, 0.f);
+      if (n >= a.N) continue;
+      const Besides b = wants<EPI>(a) ? besides<DT, EPI>(a, t.row0 + r, n) : Besides{};
+      emit<DT, EPI>(a, t.row0 + r, n, v[half], v[half], 0.f, 0.f, bias_of<DT, EPI>(a, t.e, n), b);
     }
   }
 }
