@@ -483,6 +483,10 @@ hipError_t launch_product(const ProductArgs& a, int dtype, int kind, hipStream_t
 // 128 rows 748 of 487.
 constexpr int kFewRows = 2;
 constexpr int64_t kFewWork = (int64_t)1 << 30;   // rows times an expert's matrix
+inline bool few_rows_for(int E, int64_t S, int64_t matrix) {   // matrix: elements of an expert's
+  const int64_t experts = S < E ? S : E;
+  return S <= kFewRows * experts || (S <= 64 * experts && S * matrix <= kFewWork);
+}
 bool few_rows(const ProductArgs& a, int kind);
 hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s);
 

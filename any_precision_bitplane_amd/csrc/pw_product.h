@@ -182,7 +182,7 @@ __device__ __forceinline__ void copy16(rsrc_t rs, uint32_t to, uint32_t at, uint
   asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
                :
                : "s"(to), "n"(AWAY), "v"(at), "s"(rs), "s"(more)
-               : "memory", "scc");
+               : "memory", "scc", "m0");
 }
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;

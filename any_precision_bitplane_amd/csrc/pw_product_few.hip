@@ -134,8 +134,7 @@ hipError_t pick(const ProductArgs& a, hipStream_t s) {
 // No 8-bit copies: a block has 16 columns of a group of 128.
 bool few_rows(const ProductArgs& a, int kind) {
   if ((kind != kProductAct && kind != kProductGate) || a.z8) return false;
-  const int64_t experts = a.S < a.E ? a.S : a.E, S = a.S;
-  return S <= kFewRows * experts || (S <= 64 * experts && S * a.N * a.K * (kind == kProductGate ? 2 : 1) <= kFewWork);
+  return few_rows_for(a.E, a.S, (int64_t)a.N * a.K * (kind == kProductGate ? 2 : 1));
 }
 
 hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s) {

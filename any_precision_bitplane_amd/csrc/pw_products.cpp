@@ -24,7 +24,9 @@ pw_status check_ffn(const pw_moe_shape* shape, int32_t S) {
   if (!shape) return PW_ERR_INVALID_ARG;
   pw_moe_shape one = *shape;
   one.top_k = 1;
-  return pw_check_shape(&one, S);
+  PW_TRY(pw_check_shape(&one, S));
+  // rows of h and of the gradient of gate and up are a tile's rows too
+  return shape->hidden > kMaxRowStride || 2 * (int64_t)shape->inter > kMaxRowStride ? PW_ERR_UNSUPPORTED_SHAPE : PW_OK;
 }
 
 pw_status check_wide_rows(const void* p, int64_t stride, int64_t S, int64_t n, int64_t bytes, bool written) {
@@ -70,10 +72,13 @@ size_t dz_bytes(int64_t S, int64_t N) { return align_up((size_t)S * (size_t)N * 
 size_t dz_sum_bytes(int E, int64_t S, int N) { return align_up(sizeof(float) * dz_part_floats(E, S, N), kAlign); }
 size_t h_bytes(int64_t S, int64_t I) { return align_up((size_t)S * (size_t)I * 2 + 1, kAlign); }
 
-// Scratch of a forward call's cut tiles: none for the few rows whose products have no tiles.
-size_t forward_part_bytes(int E, int64_t S) { return S > (int64_t)kFewRows * E ? product_part_bytes(E, S) : 0; }
-float* forward_parts(uint8_t* at, int E, int64_t S) {
-  return forward_part_bytes(E, S) ? reinterpret_cast<float*>(at) : nullptr;
+// Scratch of a forward call's cut tiles, whose largest matrix has so many elements:
+// none for the few rows whose products have no tiles (no more rows have tiles then).
+size_t forward_part_bytes(int E, int64_t S, int64_t matrix) {
+  return few_rows_for(E, S, matrix) ? 0 : product_part_bytes(E, S);
+}
+float* forward_parts(uint8_t* at, int E, int64_t S, int64_t matrix) {
+  return forward_part_bytes(E, S, matrix) ? reinterpret_cast<float*>(at) : nullptr;
 }
 
 }  // namespace
@@ -81,7 +86,7 @@ float* forward_parts(uint8_t* at, int E, int64_t S) {
 extern "C" {
 
 size_t pw_moe_product_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
-  return check_product(E, S_max, N, K) == PW_OK ? kAlign + forward_part_bytes(E, S_max) : 0;
+  return check_product(E, S_max, N, K) == PW_OK ? kAlign + forward_part_bytes(E, S_max, (int64_t)N * K) : 0;
 }
 
 size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
@@ -114,7 +119,7 @@ pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dty
   a.pre = pre; a.pre_stride = pre_stride;
   a.y = y; a.y_stride = y_stride;
   a.act = act;
-  a.part = forward_parts(static_cast<uint8_t*>(workspace), E, S);
+  a.part = forward_parts(static_cast<uint8_t*>(workspace), E, S, (int64_t)N * K);
   return run_product(a, dtype, kProductAct, stream);
 }
 
@@ -174,7 +179,8 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
 
 size_t pw_moe_ffn_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
   if (check_ffn(shape, S_max) != PW_OK) return 0;
-  return h_bytes(S_max, shape->inter) + forward_part_bytes(shape->num_experts, S_max);
+  return h_bytes(S_max, shape->inter) +
+         forward_part_bytes(shape->num_experts, S_max, 2 * (int64_t)shape->inter * shape->hidden);
 }
 
 size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
@@ -208,7 +214,7 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const 
   a.z = z; a.z_stride = z_stride;
   a.z_scale = z_scale; a.groups = kept_groups(I);
   a.z8 = z && z_dtype == PW_E4M3;
-  a.part = forward_parts(static_cast<uint8_t*>(workspace) + h_bytes(S, I), E, S);
+  a.part = forward_parts(static_cast<uint8_t*>(workspace) + h_bytes(S, I), E, S, 2 * (int64_t)I * H);
   PW_TRY(run_product(a, dtype, kProductGate, stream));
   ProductArgs d{};
   d.E = E; d.S = S; d.N = H; d.K = I;

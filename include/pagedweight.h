@@ -516,7 +516,8 @@ pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, co
 #define PW_ACT_GELU 2
 
 /* Workspace of pw_moe_product and of pw_moe_product_backward for up to S_max
- * rows (0 on a bad size). */
+ * rows (0 on a bad size).  From some rows on it holds 16 to 64 MB, whatever their
+ * number, for the sums of products that are cut along their reduction. */
 size_t pw_moe_product_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K);
 size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K);
 
@@ -528,7 +529,7 @@ size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t
  *   residual  [S][N] or NULL; may be y itself (same pointer and stride)
  *   pre       [S][N] or NULL: receives z for the gradient
  *   y         [S][N], overwritten
- * S == 0 returns PW_OK and enqueues nothing. */
+ * One or two launches.  S == 0 returns PW_OK and enqueues nothing. */
 pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* x, int64_t x_stride,
                          const int32_t* offsets, const void* w, const void* bias, int32_t act, const void* residual,
                          int64_t residual_stride, void* pre, int64_t pre_stride, void* y, int64_t y_stride,
@@ -541,7 +542,7 @@ pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dty
  *   dw     [E][N][K], zero for an expert without rows, or NULL: not wanted (x
  *          may be NULL then)
  *   dbias  [E][N], the same, or NULL
- * S == 0 sets dw and dbias to zero. */
+ * Up to five launches.  S == 0 sets dw and dbias to zero. */
 pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* dy,
                                   int64_t dy_stride, const void* x, int64_t x_stride, const int32_t* offsets,
                                   const void* w, int32_t act, const void* pre, int64_t pre_stride, void* dx,
@@ -557,7 +558,8 @@ size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape /* host */,
  *     [gate | up] = w_gate_up[e] x[s],   h = act(gate) * up,   y[s] = w_down[e] h
  * (the expert product of pw_moe_forward with matrices of 16 bits and without
  * the routing weights, which pw_moe_unpermute applies).
- *   shape      host; hidden H, inter I and num_experts are used
+ *   shape      host; hidden H, inter I and num_experts are used; H at most 2^22,
+ *              I at most 2^21
  *   x          [S][H];  w_gate_up  [E][2I][H], gate rows first;  w_down  [E][H][I]
  *   act        PW_ACT_SILU or PW_ACT_GELU
  *   z          NULL, or the gradient's checkpoint [S][2I]: gate and up in

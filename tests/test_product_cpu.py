@@ -69,6 +69,8 @@ def test_ffn_refusals(lib):
 
     assert call(S=0) == B.PW_OK and call(S=-1) == BAD
     assert call(shape=B.shape(60, 96, 3, 2)) == SHAPE and call(shape=B.shape(64, 96, 300, 2)) == SHAPE
+    assert call(shape=B.shape(32, 1 << 22, 3, 2)) == SHAPE and call(shape=B.shape(1 << 23, 32, 3, 2)) == SHAPE
+    assert B.pw_moe_ffn_backward_workspace_bytes(B.shape(32, 1 << 22, 3, 2), 4) == 0
     assert call(dt=B.PW_F32) == BAD and call(act=0) == BAD and call(act=3) == BAD and call(off=None) == BAD
     for name in ("x", "wg", "wd", "y", "ws"):
         assert call(**{name: None}) == BAD, name
