@@ -44,6 +44,12 @@ __global__ __launch_bounds__((OuterShape<TM, TN>::kWaves * kWave), 2) void outer
   expert_rows(a.offsets, e, a.S, row0, rows);
   row0 = uniform(row0);
   rows = uniform(rows);
+  if (a.parts > 1) {   // this block's stretch of the rows
+    const int all = (rows + Sh::kStep - 1) / Sh::kStep, p = (int)blockIdx.y;
+    const int from = (int)((int64_t)all * p / a.parts) * Sh::kStep, to = (int)((int64_t)all * (p + 1) / a.parts) * Sh::kStep;
+    row0 += from;
+    rows = min(rows, to) - from;
+  }
   const int wave = uniform((int)threadIdx.x / kWave), lane = (int)threadIdx.x & (kWave - 1);
   const int wm = wave / Sh::WN, wn = wave % Sh::WN;
   ColsOperand<TM, Sh::kWaves, Sh::kStep> po;
@@ -69,9 +75,31 @@ __global__ __launch_bounds__((OuterShape<TM, TN>::kWaves * kWave), 2) void outer
     for (int r = lane / 8; r < 32; r += 8) {
       const int m = mt * TM + (wm * (Sh::RI / 2) + mi) * 32 + r;
       const floatx8 v = sums.get(r, lane & 7);
+      if (a.parts > 1) {
+        float* const to = a.part + (((int64_t)blockIdx.y * a.E + e) * per + local) * (TM * TN);
+        *reinterpret_cast<floatx8*>(to + (m - mt * TM) * TN + n - nt * TN) = v;
+        continue;
+      }
       if (m < a.M && n < a.N) R::store_once(out + (int64_t)m * a.N + n, R::narrow(v));
     }
   }
+}
+
+// Adds the stretches' sums, in their order: sixteen lanes a row of a tile.
+template <int DT>
+__global__ __launch_bounds__(256) void outer_join_kernel(OuterArgs a) {
+  using R = Row<DT>;
+  constexpr int T = 128;
+  const unsigned per = (unsigned)(a.MT * a.NT), e = blockIdx.x / per, local = blockIdx.x - e * per;
+  // as outer_kernel numbers them
+  const int group = (int)local / (kProdGroup * a.NT), rem = (int)local - group * kProdGroup * a.NT;
+  const int here = min(kProdGroup, a.MT - group * kProdGroup), nt = rem / here, mt = group * kProdGroup + rem - nt * here;
+  const int r = (int)blockIdx.y * 16 + (int)threadIdx.x / 16, c = ((int)threadIdx.x & 15) * 8;
+  if (mt * T + r >= a.M || nt * T + c >= a.N) return;
+  const float* from = a.part + ((int64_t)e * per + local) * (T * T) + r * T + c;
+  floatx8 v = *reinterpret_cast<const floatx8*>(from);
+  for (int p = 1; p < a.parts; ++p) v += *reinterpret_cast<const floatx8*>(from + (int64_t)p * a.E * per * (T * T));
+  R::store_once(static_cast<typename R::elem*>(a.out) + ((int64_t)e * a.M + mt * T + r) * a.N + nt * T + c, R::narrow(v));
 }
 
 // dz and the columns' sums of stretches of kDzRows rows of one expert: a block
@@ -134,14 +162,17 @@ hipError_t run_outer(OuterArgs a, hipStream_t s) {
   a.NT = (a.N + TN - 1) / TN;
   const int64_t grid = ((int64_t)a.MT * a.NT + 7) / 8 * 8 * a.E;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((outer_kernel<DT, TM, TN>), dim3((unsigned)grid), dim3(OuterShape<TM, TN>::kWaves * kWave), 0, s, a);
+  a.parts = TM == 128 ? outer_parts(a.E, a.S, a.M, a.N) : 1;
+  hipLaunchKernelGGL((outer_kernel<DT, TM, TN>), dim3((unsigned)grid, (unsigned)a.parts),
+                     dim3(OuterShape<TM, TN>::kWaves * kWave), 0, s, a);
+  if (a.parts > 1)
+    hipLaunchKernelGGL(outer_join_kernel<DT>, dim3((unsigned)(a.MT * a.NT * a.E), 8), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT>
 hipError_t pick_outer(const OuterArgs& a, hipStream_t s) {
-  const int64_t wide = (int64_t)a.E * ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (wide < kNumCUs) return run_outer<DT, 128, 128>(a, s);
+  if (outer_is_small(a.E, a.M, a.N)) return run_outer<DT, 128, 128>(a, s);
   return a.S < 128ll * a.E ? run_outer<DT, 256, 128>(a, s) : run_outer<DT, 256, 256>(a, s);
 }
 

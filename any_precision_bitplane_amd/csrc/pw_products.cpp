@@ -81,6 +81,14 @@ float* forward_parts(uint8_t* at, int E, int64_t S, int64_t matrix) {
   return forward_part_bytes(E, S, matrix) ? reinterpret_cast<float*>(at) : nullptr;
 }
 
+// Scratch of a backward call's cut products, one after another in the same place.
+size_t backward_part_bytes(int E, int64_t S, int64_t M, int64_t N, int64_t M2 = 0, int64_t N2 = 0) {
+  size_t bytes = product_part_bytes(E, S);
+  const size_t outer = outer_part_bytes(E, S, M, N), second = M2 ? outer_part_bytes(E, S, M2, N2) : 0;
+  if (outer > bytes) bytes = outer;
+  return second > bytes ? second : bytes;
+}
+
 }  // namespace
 
 extern "C" {
@@ -91,7 +99,7 @@ size_t pw_moe_product_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32
 
 size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t N, int32_t K) {
   if (check_product(E, S_max, N, K) != PW_OK) return 0;
-  return dz_bytes(S_max, N) + dz_sum_bytes(E, S_max, N) + product_part_bytes(E, S_max);
+  return dz_bytes(S_max, N) + dz_sum_bytes(E, S_max, N) + backward_part_bytes(E, S_max, N, K);
 }
 
 pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* x, int64_t x_stride,
@@ -155,6 +163,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
   z.part = dbias ? reinterpret_cast<float*>(ws + dz_bytes(S, N)) : nullptr;
   z.dbias = dbias;
   if (through || dbias) PW_TRY(hip_status(launch_dz(z, dtype, s)));
+  float* const part = reinterpret_cast<float*>(ws + dz_bytes(S, N) + dz_sum_bytes(E, S, N));
   const void* dz = through ? ws : dy;
   const int64_t dz_stride = through ? N : dy_stride;
   if (dx && S > 0) {
@@ -164,7 +173,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
     a.x = dz; a.x_stride = dz_stride;
     a.w = w; a.w_expert = (int64_t)N * K;
     a.y = dx; a.y_stride = dx_stride;
-    a.part = reinterpret_cast<float*>(ws + dz_bytes(S, N) + dz_sum_bytes(E, S, N));
+    a.part = part;
     PW_TRY(run_product(a, dtype, kProductBack, stream));
   }
   if (!dw) return PW_OK;
@@ -174,6 +183,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
   o.p = dz; o.p_stride = dz_stride;
   o.q = x; o.q_stride = x_stride;
   o.out = dw;
+  o.part = part;
   return hip_status(launch_outer(o, dtype, s));
 }
 
@@ -186,7 +196,7 @@ size_t pw_moe_ffn_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
 size_t pw_moe_ffn_backward_workspace_bytes(const pw_moe_shape* shape, int32_t S_max) {
   if (check_ffn(shape, S_max) != PW_OK) return 0;
   return dz_bytes(S_max, 2 * (int64_t)shape->inter) + h_bytes(S_max, shape->inter) +
-         product_part_bytes(shape->num_experts, S_max);
+         backward_part_bytes(shape->num_experts, S_max, shape->hidden, shape->inter, 2 * (int64_t)shape->inter, shape->hidden);
 }
 
 pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const void* x, int64_t x_stride,
@@ -270,6 +280,7 @@ pw_status pw_moe_ffn_backward(const pw_moe_shape* shape, int32_t S, int32_t dtyp
   OuterArgs o{};
   o.E = E; o.S = S;
   o.offsets = offsets;
+  o.part = part;
   if (dw_down) {
     o.M = H; o.N = I;
     o.p = dy; o.p_stride = dy_stride;

@@ -542,7 +542,7 @@ pw_status pw_moe_product(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dty
  *   dw     [E][N][K], zero for an expert without rows, or NULL: not wanted (x
  *          may be NULL then)
  *   dbias  [E][N], the same, or NULL
- * Up to five launches.  S == 0 sets dw and dbias to zero. */
+ * Up to six launches.  S == 0 sets dw and dbias to zero. */
 pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, int32_t dtype, const void* dy,
                                   int64_t dy_stride, const void* x, int64_t x_stride, const int32_t* offsets,
                                   const void* w, int32_t act, const void* pre, int64_t pre_stride, void* dx,
@@ -589,7 +589,7 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape /* host */, int32_t S, int32_t dt
  *              (x may be NULL then)
  *   dw_down    [E][H][I], the same, or NULL
  *   w_gate_up  may be NULL without dx
- * Up to six launches.  S == 0 sets dw_gate_up and dw_down to zero. */
+ * Up to eight launches.  S == 0 sets dw_gate_up and dw_down to zero. */
 pw_status pw_moe_ffn_backward(const pw_moe_shape* shape /* host */, int32_t S, int32_t dtype, const void* dy,
                               int64_t dy_stride, const void* x, int64_t x_stride, const int32_t* offsets,
                               const void* w_gate_up, const void* w_down, int32_t act, int32_t z_dtype, const void* z,

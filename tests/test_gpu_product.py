@@ -106,7 +106,7 @@ SIZES = [  # E, S, N, K, offsets
     (1, 1, 8, 8, False), (1, 3, 264, 72, False), (1, 17, 48, 264, True), (1, 40, 1032, 136, False),
     (1, 49, 264, 64, False), (1, 100, 520, 200, False), (1, 129, 256, 320, True), (1, 513, 776, 72, False),
     (5, 4, 64, 64, True), (60, 16, 96, 544, True), (60, 300, 136, 128, True), (8, 500, 264, 72, True),
-    (7, 630, 504, 136, True), (2, 600, 328, 2696, True), (1, 4100, 4104, 2568, False), (3, 1000, 248, 1000, True), (256, 700, 40, 56, True), (2, 1537, 1024, 136, True),
+    (7, 630, 504, 136, True), (2, 600, 328, 2696, True), (1, 4100, 4104, 2568, False), (1, 1355, 496, 48, True), (3, 3100, 136, 264, True), (3, 1000, 248, 1000, True), (256, 700, 40, 56, True), (2, 1537, 1024, 136, True),
 ]
 IDS = [f"E{e}-S{s}-N{n}-K{k}" for e, s, n, k, _ in SIZES]
 
