@@ -3,7 +3,10 @@
 // (gated: 16 of g and the same 16 of u) and up to 64 rows of x of one expert;
 // its eight waves take every eighth 64 steps of the reduction each, with the
 // loads of several such pieces in flight, straight into the operands of the
-// matrix cores, and add their sums through LDS in the order of the waves.
+// matrix cores, and add their sums through LDS in the order of the waves.  H 2048,
+// I 1408, E 60, 16 rows over 14 experts: 240 MB in 49 us, 5 TB/s; one row through
+// one expert of I 5632, 69 MB in 21 us, of which two launches and their first
+// loads are some 8.
 #include "pw_product.h"
 
 namespace pw {
@@ -11,7 +14,7 @@ namespace pw {
 namespace {
 
 constexpr int kFewWaves = 8;
-constexpr int kFewAhead = 2;   // pieces of 64 steps in flight
+constexpr int kFewAhead = 2;   // pieces of 64 steps in flight (4: 52 us for 49, 4 rows each 167 for 154)
 
 // RT: tiles of 16 rows of x
 template <int DT, int EPI, int RT>
