@@ -498,9 +498,31 @@ __device__ __forceinline__ void sum_short_steps(f32x4 (&acc)[RI][CJ], char* lds,
 
 // ----- activations ------------------------------------------------------------
 
+// Phi(z), the normal distribution function, to some digits of itself below zero
+// too: in 32 bits 1 + erf(z / sqrt 2) has lost half of its digits at z = -3.7 and
+// all of them from -5.6 on, where z Phi(z) is still a number of 16 bits' range.
+// With a = |z| and t = 1 / (1 + 0.3 a), Phi(-a) = exp(-a^2 / 2) t P(t); P is a
+// least-maximum fit (iteratively reweighted least squares) to exp(a^2 / 2) Phi(-a) / t
+// for a up to 14.5, off by 2^-22.5 of it at most.  Below -13.2, where the
+// exponential leaves the normal numbers, it is zero.  (8192 x 2048 bf16, 8194
+// rows over 8, with GELU, residual and kept sum: 349 us with erff, 377 with erfcf,
+// 324 so.)
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, __builtin_fabsf(z), 1.f));
+  float p = 0.035423707f;
+  p = __builtin_fmaf(p, t, -0.15615834f);
+  p = __builtin_fmaf(p, t, 0.20455663f);
+  p = __builtin_fmaf(p, t, -0.052033883f);
+  p = __builtin_fmaf(p, t, 0.12769172f);
+  p = __builtin_fmaf(p, t, 0.10017596f);
+  p = __builtin_fmaf(p, t, 0.12071213f);
+  p = __builtin_fmaf(p, t, 0.11963201f);
+  const float below = t * p * __expf(-0.5f * z * z);
+  return z < 0.f ? below : 1.f - below;
+}
 __device__ __forceinline__ float act_of(float z, int act) {
   if (act == PW_ACT_SILU) return silu_f32(z);
-  if (act == PW_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (act == PW_ACT_GELU) return z * normal_cdf(z);
   return z;
 }
 __device__ __forceinline__ float act_slope(float z, int act) {
@@ -508,8 +530,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     const float q = __builtin_amdgcn_rcpf(1.f + __expf(-z));
     return q * (1.f + z * (1.f - q));
   }
-  if (act == PW_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
+  if (act == PW_ACT_GELU) return normal_cdf(z) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
   return 1.f;
 }
 

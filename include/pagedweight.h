@@ -509,7 +509,8 @@ pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, co
  * to dtype, as the matrix cores take them.
  *
  * Activations: act(z) = z, z / (1 + exp(-z)), or z Phi(z) with the normal
- * distribution function Phi(z) = (1 + erf(z / sqrt 2)) / 2.
+ * distribution function Phi(z) = erfc(-z / sqrt 2) / 2; values of act and of its
+ * slope smaller than 2^-119 may come as zero.
  * ---------------------------------------------------------------------- */
 #define PW_ACT_NONE 0
 #define PW_ACT_SILU 1

@@ -14,14 +14,14 @@ GROUP = 128
 E4M3_MAX = 448.0
 SCALE_MIN = 2.0 ** -100
 
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])   # Phi(z) = erfc(-z / sqrt 2) / 2 keeps its digits far below 0
 
 
 def act(z, name):
     if name == "silu":
         return z / (1 + np.exp(-z))
     if name == "gelu":
-        return z * (1 + _erf(z / math.sqrt(2))) / 2
+        return z * _erfc(-z / math.sqrt(2)) / 2
     return z
 
 
@@ -30,7 +30,7 @@ def slope(z, name):
         q = 1 / (1 + np.exp(-z))
         return q + z * q * (1 - q)
     if name == "gelu":
-        return (1 + _erf(z / math.sqrt(2))) / 2 + z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        return _erfc(-z / math.sqrt(2)) / 2 + z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     return np.ones_like(z)
 
 

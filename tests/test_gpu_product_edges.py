@@ -1,0 +1,68 @@
+"""The expert products in 16 bits at the edges of what their calls take, on the GPU.
+
+Tolerances count roundings: U = 2^-24 is half a step of fp32, a stored value is
+off by half a step of its type relative to itself and half a subnormal step.
+Every case prints what it runs first.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from any_precision_bitplane_amd import binding as B
+from test_gpu_product import DEV, DTYPES, U, dtype_of, f64, half_step, near, rand, say, scratch, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def gelu64(z):
+    """GELU, its slope, and by how much fp32 may be off from either, at z < -2.
+
+    exp(-z^2 / 2): three roundings of the exponent (z^2, the constant log2 e, their product), each z^2 / 2 times as
+    large in the result, and the function 1 ulp (2 U).  Phi is that times t P(t), t = 1 / (1 + 0.3 |z|) off by 4 U and
+    P by at most 2 times as much of it, P's fit 3 U, its coefficients' roundings and seven steps of magnitudes up to
+    1.85 times its value 2 and 14 U, the two products 2 U: with exp's 2 below 44 U.  Its product with z is one rounding
+    more; the slope's other part has four (with z and 1 / sqrt(2 pi)), and the sum one.
+    """
+    phi = np.vectorize(lambda v: math.erfc(-v / math.sqrt(2)) / 2, otypes=[np.float64])(z)
+    bell = z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    of_phi = phi * (1.5 * z * z + 44) * U
+    return z * phi, phi + bell, np.abs(z) * of_phi, of_phi + np.abs(bell) * (1.5 * z * z + 8) * U + np.abs(phi + bell) * U
+
+
+@pytest.mark.parametrize("S", [9, 300])
+@pytest.mark.parametrize("name", DTYPES)
+def test_gelu_far_below_zero(torch, name, S):  # noqa: F811
+    """z from -12.5 on, where z Phi(z) is some 1e-35: off by so much relative to itself, as bf16 holds it."""
+    say(f"GELU of -12.5 .. -3, {name}, S={S}")
+    t, I = dtype_of(torch, name), 64
+    z = torch.linspace(-12.5, -3, S * I).reshape(S, I).to(t).to(DEV)
+    act, slope, ea, es = gelu64(f64(z))
+    rel, ab = half_step(torch, name)
+    ok = lambda got, ref, e, what: near(f64(got), ref, e + rel * (np.abs(ref) + e) + ab, what)
+    eye = torch.eye(I, dtype=t, device=DEV)
+
+    # the product with the unit matrix
+    y = torch.empty((S, I), dtype=t, device=DEV)
+    B.pw_moe_product(1, S, I, I, z, eye, y, scratch(torch, B.pw_moe_product_workspace_bytes(1, S, I, I)), act=B.PW_ACT_GELU)
+    ok(y, act, ea, "act")
+    one, dx = torch.ones_like(z), torch.empty_like(z)
+    ws = scratch(torch, B.pw_moe_product_backward_workspace_bytes(1, S, I, I))
+    B.pw_moe_product_backward(1, S, I, I, one, None, eye, ws, act=B.PW_ACT_GELU, pre=z, dx=dx)
+    ok(dx, slope, es, "slope")
+
+    # the block with gate = z, up = 1 and h taken as it is
+    H, shp = 2 * I, B.shape(2 * I, I, 1, 1)
+    x = torch.cat([z, one], dim=1)
+    w_gate_up = torch.eye(H, dtype=t, device=DEV)
+    w_down = torch.cat([eye, 0 * eye])
+    y, kept = torch.empty((S, H), dtype=t, device=DEV), torch.empty((S, 2 * I), dtype=t, device=DEV)
+    B.pw_moe_ffn(shp, S, x, w_gate_up, w_down, y, scratch(torch, B.pw_moe_ffn_workspace_bytes(shp, S)), act=B.PW_ACT_GELU,
+                 z=kept)
+    assert torch.equal(kept, x) and not bool(y[:, I:].any())
+    ok(y[:, :I], act, ea, "h")
+    dx = torch.empty_like(x)
+    B.pw_moe_ffn_backward(shp, S, torch.cat([one, one], dim=1), None, w_gate_up, w_down, kept,
+                          scratch(torch, B.pw_moe_ffn_backward_workspace_bytes(shp, S)), act=B.PW_ACT_GELU, dx=dx)
+    ok(dx[:, :I], slope, es, "dgate")
+    ok(dx[:, I:], act, ea, "dup")

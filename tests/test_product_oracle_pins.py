@@ -26,6 +26,14 @@ def test_activations_by_hand():
     assert po.slope(np.zeros(1), "silu")[0] == 0.5 and po.slope(np.zeros(1), "gelu")[0] == 0.5
 
 
+def test_gelu_far_below_zero_by_hand():
+    z = np.array([-10.0, -6.0])
+    phi = np.array([7.619853024160527e-24, 9.865876450376946e-10])      # tables of the normal distribution function
+    assert np.allclose(po.act(z, "gelu"), z * phi, rtol=1e-12, atol=0)
+    bell = np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    assert np.allclose(po.slope(z, "gelu"), phi + z * bell, rtol=1e-12, atol=0)
+
+
 @pytest.mark.parametrize("name", ["silu", "gelu"])
 def test_gradients_against_differences(name):
     rng = np.random.default_rng(5)
