@@ -137,8 +137,8 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
                                   int64_t dx_stride, void* dw, void* dbias, void* workspace, size_t workspace_bytes,
                                   void* stream) {
   PW_TRY(check_product(E, S, N, K));
-  if (!sixteen(dtype) || act < PW_ACT_NONE || act > PW_ACT_GELU || (act != PW_ACT_NONE && S > 0) != (pre != nullptr))
-    return PW_ERR_INVALID_ARG;
+  if (!sixteen(dtype) || act < PW_ACT_NONE || act > PW_ACT_GELU) return PW_ERR_INVALID_ARG;
+  if (act == PW_ACT_NONE ? pre != nullptr : S > 0 && !pre) return PW_ERR_INVALID_ARG;
   PW_TRY(check_offsets(offsets, E));
   if (!aligned(dw, 16) || !aligned(dbias, 16)) return PW_ERR_ALIGNMENT;
   const hipStream_t s = (hipStream_t)stream;
@@ -153,7 +153,7 @@ pw_status pw_moe_product_backward(int32_t E, int32_t S, int32_t N, int32_t K, in
     PW_TRY(check_scratch(workspace, workspace_bytes, pw_moe_product_backward_workspace_bytes(E, S, N, K)));
   }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const bool through = pre && (dx || dw);   // dz differs from dy and is read again
+  const bool through = S > 0 && pre && (dx || dw);   // dz differs from dy and is read again
   DzArgs z{};
   z.E = E; z.S = S; z.N = N; z.act = act;
   z.offsets = offsets;

@@ -66,3 +66,19 @@ def test_gelu_far_below_zero(torch, name, S):  # noqa: F811
                           scratch(torch, B.pw_moe_ffn_backward_workspace_bytes(shp, S)), act=B.PW_ACT_GELU, dx=dx)
     ok(dx[:, :I], slope, es, "dgate")
     ok(dx[:, I:], act, ea, "dup")
+
+
+@pytest.mark.parametrize("act", [B.PW_ACT_SILU, B.PW_ACT_GELU], ids=["silu", "gelu"])
+def test_gradient_of_no_rows_with_an_activation(torch, act):  # noqa: F811
+    say("product backward of no rows, the sum's buffer there or not")
+    E, N, K = 3, 64, 72
+    none = torch.empty((0, N), dtype=torch.float16, device=DEV), torch.empty((0, K), dtype=torch.float16, device=DEV)
+    w, pre = rand(torch, 1, (E, N, K), "f16"), rand(torch, 2, (40, N), "f16")
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    ws = scratch(torch, B.pw_moe_product_backward_workspace_bytes(E, 0, N, K))
+    for kept in (None, pre):
+        dx, dw, db = torch.full((8, K), 7.0, device=DEV).half(), torch.full_like(w, 7.0), torch.full((E, N), 7.0, dtype=w.dtype, device=DEV)
+        B.pw_moe_product_backward(E, 0, N, K, *none, w, ws, offsets=off, act=act, pre=kept, dx=dx, dw=dw, dbias=db)
+        B.pw_moe_product_backward(E, 0, N, K, *none, w, None, offsets=off, act=act, pre=kept, dx=dx)
+        torch.cuda.synchronize()
+        assert not bool(dw.any()) and not bool(db.any()) and bool((dx == 7.0).all())

@@ -60,6 +60,17 @@ def test_product_backward_refusals(lib):
     assert B.pw_moe_product_backward_workspace_bytes(3, -4, 64, 72) == 0
 
 
+def test_gradient_of_no_rows_with_an_activation(lib):
+    """pre is needed where there are rows; without rows it may be there (a buffer for the largest step) or not."""
+    def call(act, pre, S=0):
+        return lib.pw_moe_product_backward(3, S, 64, 72, B.PW_BF16, P, 64, P, 72, P, P, act, pre, 64, P, 72, None, None, P,
+                                           HUGE, None)
+
+    for act in (B.PW_ACT_SILU, B.PW_ACT_GELU):
+        assert call(act, None) == B.PW_OK and call(act, P) == B.PW_OK and call(act, None, 4) == BAD
+    assert call(B.PW_ACT_NONE, None) == B.PW_OK and call(B.PW_ACT_NONE, P) == BAD
+
+
 def test_ffn_refusals(lib):
     shp = B.shape(64, 96, 3, 2)
 
