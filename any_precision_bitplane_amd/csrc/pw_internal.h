@@ -461,6 +461,26 @@ struct ProductArgs {
 constexpr int kWideRows = 160, kMidRows = 56, kNarrowRows = 32;
 constexpr int kProdParts = 16;   // most parts of a tile
 constexpr unsigned product_blocks(int rows) { return rows <= 64 ? 2 * kNumCUs : kNumCUs; }
+// Parts that a tile of the unfilled last round is cut into along its reduction of
+// `steps` steps of 64, where `rest` tiles of BM rows are left for `together` blocks
+// (1: it is not cut).  The launch that adds the parts takes some 5 us, a part of
+// 256 rows 0.1 (256 KB written and read), a step 1.3: the number of parts that
+// saves most, fewer where two save the same, in units of 1/2560 us.  In whole
+// numbers, since the products and the launch that adds them work it out apart.
+constexpr unsigned product_parts(unsigned BM, unsigned rest, unsigned steps, unsigned together) {
+  unsigned most = rest ? together / rest : 1, parts = 1;
+  if (most > steps / 2) most = steps / 2;
+  if (most > kProdParts) most = kProdParts;
+  int best = 5 * 2560;
+  for (unsigned p = 2; p <= most; ++p) {
+    const int saved = 13 * 256 * (int)(steps - (steps + p - 1) / p) - (int)(BM * rest * p);
+    if (saved > best) {
+      best = saved;
+      parts = p;
+    }
+  }
+  return parts;
+}
 inline int product_mean_rows(int E, int64_t S) {
   return S >= (int64_t)kWideRows * E ? 256 : S > (int64_t)kMidRows * E ? 128 : S > (int64_t)kNarrowRows * E ? 64 : 32;
 }

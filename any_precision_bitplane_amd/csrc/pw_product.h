@@ -130,27 +130,14 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int E, int S, 
 
 // The tiles that do not fill a last round of the CUs are cut along the reduction,
 // so that they do: each of the last `rest` tiles into `parts`, whose sums go to
-// memory and are added, in their order, by a launch of their own.  That launch
-// takes some 5 us, and a part of 256 rows 0.1 (256 KB written and read); a step
-// of 64 about 1.3: the number of parts that saves most is taken.
+// memory and are added, in their order, by a launch of their own.
 template <int BM>
 struct Rounds {
   static constexpr unsigned kTogether = product_blocks(BM);
   unsigned whole, rest, parts;
   __device__ __forceinline__ Rounds(unsigned total, int steps, bool cut) {
     rest = cut ? total % kTogether : 0;
-    parts = 1;
-    if (rest) {
-      const unsigned most = min(kTogether / rest, min((unsigned)steps / 2, (unsigned)kProdParts));
-      float best = 5.f;
-      for (unsigned p = 2; p <= most; ++p) {
-        const float saved = 1.3f * (float)(steps - (steps + p - 1) / p) - (0.1f * BM / 256) * (float)(rest * p);
-        if (saved > best) {
-          best = saved;
-          parts = p;
-        }
-      }
-    }
+    parts = product_parts(BM, rest, (unsigned)steps, kTogether);
     if (parts == 1) rest = 0;
     whole = total - rest;
   }

@@ -3,10 +3,12 @@ entry points by made-up pointers, the binding by tensors that are not on a GPU.
 No GPU needed."""
 import ctypes
 import os
+import subprocess
 
 import pytest
 
 from any_precision_bitplane_amd import binding as B
+from any_precision_bitplane_amd import build
 
 P = 1 << 20     # a made-up aligned address: every call below ends before it is used
 HUGE = 1 << 60
@@ -120,6 +122,16 @@ def test_workspaces_grow_with_rows(lib):
                  lambda S: B.pw_moe_product_backward_workspace_bytes(8, S, 4096, 2048)):
         sizes = [size(S) for S in list(range(0, 700)) + [1000, 4095, 4096, 100000, 1 << 24]]
         assert all(a <= b for a, b in zip(sizes, sizes[1:])) and all(s % 256 == 0 and s > 0 for s in sizes)
+
+
+@pytest.mark.parametrize("fuse", ["off", "fast"])
+def test_parts_of_a_cut_tile_are_the_same_however_the_compiler_fuses(tmp_path, fuse):
+    """The products and the launch that joins their parts work the number out apart: it has ties, and no rounding may break them."""
+    exe = str(tmp_path / "parts_test")
+    subprocess.run([build.hipcc(), "-x", "hip", "--offload-host-only", "-O2", "-mfma", f"-ffp-contract={fuse}", "-std=c++17",
+                    "-I", build.CSRC, os.path.join(build.ROOT, "tests", "cpp", "product_parts_test.cpp"), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
 
 
 def test_binding_refuses_tensors_that_are_on_no_gpu():
