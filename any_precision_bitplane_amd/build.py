@@ -47,6 +47,9 @@ def _compile(src: str) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    seen = [line for line in r.stderr.splitlines() if "warning:" in line]
+    if seen:
+        print("\n".join(seen), file=sys.stderr)
     return obj
 
 

@@ -163,13 +163,14 @@ __device__ __forceinline__ rsrc_t copy_rsrc(const void* base) {
   const uint64_t p = (uint64_t)base;
   return rsrc_t{(uint32_t)p, (uint32_t)(p >> 32) & 0xFFFFu, kRsrcBytes, 0x00020000u};
 }
-// `to` + AWAY: the wave's place, `more`: bytes that every lane adds
+// `to` + AWAY: the wave's place, `more`: bytes that every lane adds.  The place is
+// handed over in m0, so that the compiler knows what m0 holds.
 template <int AWAY>
 __device__ __forceinline__ void copy16(rsrc_t rs, uint32_t to, uint32_t at, uint32_t more) {
-  asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, %4 offen lds"
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :
-               : "s"(to), "n"(AWAY), "v"(at), "s"(rs), "s"(more)
-               : "memory", "scc", "m0");
+               : "{m0}"(to + AWAY), "v"(at), "s"(rs), "s"(more)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;

@@ -134,6 +134,24 @@ def test_parts_of_a_cut_tile_are_the_same_however_the_compiler_fuses(tmp_path, f
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
 
 
+def test_copies_to_lds_compile_without_a_warning(tmp_path):
+    """Inline assembly that changes a register behind the compiler's back is warned of, and is no behaviour to build on."""
+    src = tmp_path / "copy.hip"
+    src.write_text("""#include "pw_product.h"
+__global__ void copy(const char* p, char* q) {
+  __shared__ char lds[2048];
+  pw::copy16<1024>(pw::copy_rsrc(p), pw::lds_at(lds), threadIdx.x * 16, 64);
+  pw::step_barrier<0>();
+  q[threadIdx.x] = lds[1024 + threadIdx.x];
+}
+""")
+    r = subprocess.run([build.hipcc(), *build.COMMON, "-Werror", "-I", build.CSRC, "-x", "hip", "--cuda-device-only", "-S",
+                        str(src), "-o", str(tmp_path / "copy.s")], capture_output=True, text=True)
+    assert r.returncode == 0 and "warning" not in r.stderr, r.stderr
+    text = (tmp_path / "copy.s").read_text()
+    assert "offen lds" in text and "m0" in text
+
+
 def test_binding_refuses_tensors_that_are_on_no_gpu():
     import torch
     x, w = torch.zeros((4, 64), dtype=torch.float16), torch.zeros((1, 64, 64), dtype=torch.float16)
