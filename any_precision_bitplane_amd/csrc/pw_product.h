@@ -151,6 +151,8 @@ inline int64_t product_row_tiles(const int32_t* offsets, int E, int64_t S, int B
   return S / BM + with_rows < S ? S / BM + with_rows : S;
 }
 inline int64_t product_grid(int64_t row_tiles, int64_t NT) { return (row_tiles * NT + 7) / 8 * 8; }
+// A launch has less than 2^32 threads.
+inline bool launch_fits(int64_t blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }
 
 // ----- a tile's operands ------------------------------------------------------
 

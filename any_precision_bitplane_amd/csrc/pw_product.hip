@@ -327,7 +327,7 @@ hipError_t run(ProductArgs a, hipStream_t s) {
   const bool cut = a.part && (a.offsets ? steps >= 40 || (tiles <= most && steps >= 8) : tiles % most && steps >= 6);
   if (!cut) a.part = nullptr;
   const int64_t grid = (tiles + 7) / 8 * 8 + (cut ? most : 0);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launch_fits(grid, Sh::kThreads)) return hipErrorInvalidValue;
   hipLaunchKernelGGL((product_kernel<DT, EPI, MI, WM, WN>), dim3((unsigned)grid), dim3(Sh::kThreads), 0, s, a);
   if (cut) {
     const int64_t joined = tiles < most / 2 ? tiles : most / 2;

@@ -115,29 +115,40 @@ __global__ __launch_bounds__(kFewWaves * kWave) void few_kernel(ProductArgs a) {
   }
 }
 
+// Tiles of 16 rows of x that a block takes.
+int row_pieces(int E, int64_t S) {
+  const int64_t experts = S < E ? S : E, mean = S / experts;
+  return mean > 16 ? 4 : mean > 4 ? 2 : 1;
+}
+int64_t blocks_of(const ProductArgs& a, int pieces) {
+  return product_grid(product_row_tiles(a.offsets, a.E, a.S, pieces * 16), (a.N + 15) / 16);
+}
+
 template <int DT, int EPI, int RT>
 hipError_t run(ProductArgs a, hipStream_t s) {
   a.NT = (a.N + 15) / 16;
-  const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, RT * 16), a.NT);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t grid = blocks_of(a, RT);
   hipLaunchKernelGGL((few_kernel<DT, EPI, RT>), dim3((unsigned)grid), dim3(kFewWaves * kWave), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT, int EPI>
 hipError_t pick(const ProductArgs& a, hipStream_t s) {
-  const int64_t experts = a.S < a.E ? a.S : a.E, mean = a.S / experts;
-  if (mean > 16) return run<DT, EPI, 4>(a, s);
-  if (mean > 4) return run<DT, EPI, 2>(a, s);
-  return run<DT, EPI, 1>(a, s);
+  switch (row_pieces(a.E, a.S)) {
+    case 4: return run<DT, EPI, 4>(a, s);
+    case 2: return run<DT, EPI, 2>(a, s);
+    default: return run<DT, EPI, 1>(a, s);
+  }
 }
 
 }  // namespace
 
-// No 8-bit copies: a block has 16 columns of a group of 128.
+// No 8-bit copies: a block has 16 columns of a group of 128.  Matrices so long that
+// their blocks are more than a launch has (256 rows over 256 experts, N 2^20) take tiles.
 bool few_rows(const ProductArgs& a, int kind) {
   if ((kind != kProductAct && kind != kProductGate) || a.z8) return false;
-  return few_rows_for(a.E, a.S, (int64_t)a.N * a.K * (kind == kProductGate ? 2 : 1));
+  return few_rows_for(a.E, a.S, (int64_t)a.N * a.K * (kind == kProductGate ? 2 : 1)) &&
+         launch_fits(blocks_of(a, row_pieces(a.E, a.S)), kFewWaves * kWave);
 }
 
 hipError_t launch_few(const ProductArgs& a, int dtype, int kind, hipStream_t s) {

@@ -163,7 +163,7 @@ hipError_t run_outer(OuterArgs a, hipStream_t s) {
   a.MT = (a.M + TM - 1) / TM;
   a.NT = (a.N + TN - 1) / TN;
   const int64_t grid = ((int64_t)a.MT * a.NT + 7) / 8 * 8 * a.E;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (!launch_fits(grid, OuterShape<TM, TN>::kWaves * kWave)) return hipErrorInvalidValue;
   a.parts = TM == 128 ? outer_parts(a.E, a.S, a.M, a.N) : 1;
   hipLaunchKernelGGL((outer_kernel<DT, TM, TN>), dim3((unsigned)grid, (unsigned)a.parts),
                      dim3(OuterShape<TM, TN>::kWaves * kWave), 0, s, a);
@@ -182,7 +182,7 @@ template <int DT>
 hipError_t run_dz(const DzArgs& a, hipStream_t s) {
   if (a.S > 0) {
     const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, kDzRows), (a.N + 255) / 256);
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_fits(grid, kDzThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(dz_kernel<DT>, dim3((unsigned)grid), dim3(kDzThreads), 0, s, a);
   }
   if (a.dbias)

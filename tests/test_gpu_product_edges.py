@@ -82,3 +82,19 @@ def test_gradient_of_no_rows_with_an_activation(torch, act):  # noqa: F811
         B.pw_moe_product_backward(E, 0, N, K, *none, w, None, offsets=off, act=act, pre=kept, dx=dx)
         torch.cuda.synchronize()
         assert not bool(dw.any()) and not bool(db.any()) and bool((dx == 7.0).all())
+
+
+def test_long_matrices_of_many_experts(torch):  # noqa: F811
+    """A row for every expert, and more blocks of 16 columns than one launch has threads for."""
+    E = S = 256
+    N, K = 1 << 20, 8
+    say(f"product E={E} S={S} N={N} K={K}")
+    g = torch.Generator(device=DEV)
+    g.manual_seed(1)
+    w = torch.randint(-3, 4, (E, N, K), dtype=torch.int8, generator=g, device=DEV).half()
+    x = torch.randint(-3, 4, (S, K), dtype=torch.int8, generator=g, device=DEV).half()
+    y = torch.full((S, N), 7.0, dtype=x.dtype, device=DEV)
+    off = torch.arange(E + 1, dtype=torch.int32, device=DEV)
+    B.pw_moe_product(E, S, N, K, x, w, y, scratch(torch, B.pw_moe_product_workspace_bytes(E, S, N, K)), offsets=off)
+    for e in range(E):     # whole numbers below 256: exact
+        assert torch.equal(y[e], (w[e].float() * x[e].float()).sum(1).half()), e
