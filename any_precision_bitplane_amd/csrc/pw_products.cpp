@@ -8,13 +8,14 @@ namespace {
 
 constexpr int64_t kMaxRowStride = (int64_t)1 << 22;   // a tile's rows are addressed with 31-bit byte offsets
 constexpr int64_t kMaxMatrix = (int64_t)1 << 30;
+constexpr int64_t kMaxRows = 0x7FFFFFFF - 255;           // rows rounded up to a tile's are 32-bit numbers
 
 bool sixteen(int32_t dtype) { return dtype == PW_F16 || dtype == PW_BF16; }
 
 // Sizes of a product; PW_OK if a call may have them.
 pw_status check_product(int32_t E, int64_t S, int64_t N, int64_t K) {
   if (E < 1 || S < 0 || N < 1 || K < 1) return PW_ERR_INVALID_ARG;
-  if (E > kMaxExperts || N % 8 || K % 8 || N > kMaxRowStride || K > kMaxRowStride || N * K > kMaxMatrix)
+  if (E > kMaxExperts || S > kMaxRows || N % 8 || K % 8 || N > kMaxRowStride || K > kMaxRowStride || N * K > kMaxMatrix)
     return PW_ERR_UNSUPPORTED_SHAPE;
   return PW_OK;
 }

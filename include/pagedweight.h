@@ -524,6 +524,7 @@ size_t pw_moe_product_backward_workspace_bytes(int32_t E, int32_t S_max, int32_t
 
 /* Product with bias, activation and residual:
  *     z[s] = w[e] x[s] + bias[e],   y[s] = act(z[s]) + residual[s]
+ *   S         at most 2^31 - 256, here and in the gradient
  *   N, K      multiples of 8, at most 2^22, N K at most 2^30
  *   x         [S][K];  w  [E][N][K];  bias  [E][N] or NULL
  *   act       PW_ACT_*

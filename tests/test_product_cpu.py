@@ -73,6 +73,18 @@ def test_gradient_of_no_rows_with_an_activation(lib):
     assert call(B.PW_ACT_NONE, None) == B.PW_OK and call(B.PW_ACT_NONE, P) == BAD
 
 
+def test_rows_that_tiles_cannot_count(lib):
+    """Rounded up to whole tiles of 256, the rows have to be a 32-bit number."""
+    most = (1 << 31) - 256
+    for size in (B.pw_moe_product_workspace_bytes, B.pw_moe_product_backward_workspace_bytes):
+        assert size(1, most, 8, 8) > 0
+        assert all(size(1, S, 8, 8) == 0 for S in (most + 1, (1 << 31) - 1))
+    for S in (most + 1, (1 << 31) - 1):
+        assert lib.pw_moe_product(1, S, 8, 8, B.PW_F16, P, 8, None, P, None, 0, None, 0, None, 0, P, 8, P, HUGE, None) == SHAPE
+        assert lib.pw_moe_product_backward(1, S, 8, 8, B.PW_F16, P, 8, P, 8, None, P, 0, None, 0, P, 8, P, P, P, HUGE,
+                                           None) == SHAPE
+
+
 def test_ffn_refusals(lib):
     shp = B.shape(64, 96, 3, 2)
 
