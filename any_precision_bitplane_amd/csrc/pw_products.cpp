@@ -31,7 +31,7 @@ pw_status check_ffn(const pw_moe_shape* shape, int32_t S) {
 }
 
 pw_status check_wide_rows(const void* p, int64_t stride, int64_t S, int64_t n, int64_t bytes, bool written) {
-  if (stride >= kMaxRowStride) return PW_ERR_UNSUPPORTED_SHAPE;
+  if (stride >= kMaxRowStride + (S == 1)) return PW_ERR_UNSUPPORTED_SHAPE;   // a row of the largest size, alone
   return check_rows(p, stride, S, n, bytes, written);
 }
 

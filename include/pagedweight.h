@@ -502,7 +502,8 @@ pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, co
  *               one expert (E = 1) with all S rows.
  *   Matrices and biases of the experts follow each other without gaps, 16-byte
  *   aligned.  E is 1..256, sizes of rows are as each call says, and a row
- *   stride is below 2^22 elements (else PW_ERR_UNSUPPORTED_SHAPE).
+ *   stride is below 2^22 elements, of a single row at most that (else
+ *   PW_ERR_UNSUPPORTED_SHAPE).
  *
  * Sums are fp32; an output is rounded once.  Between two products of one call
  * (h, and gradients of gate and up or of the product's sum) values are rounded

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 
 from any_precision_bitplane_amd import binding as B
-from test_gpu_product import DEV, DTYPES, U, dtype_of, f64, half_step, near, rand, say, scratch, torch  # noqa: F401
+from test_gpu_product import DEV, DTYPES, U, dtype_of, f64, half_step, near, rand, say, scratch, torch, whole  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,17 @@ def test_long_matrices_of_many_experts(torch):  # noqa: F811
     B.pw_moe_product(E, S, N, K, x, w, y, scratch(torch, B.pw_moe_product_workspace_bytes(E, S, N, K)), offsets=off)
     for e in range(E):     # whole numbers below 256: exact
         assert torch.equal(y[e], (w[e].float() * x[e].float()).sum(1).half()), e
+
+
+@pytest.mark.parametrize("N,K", [(1 << 22, 8), (8, 1 << 22)])
+def test_a_row_of_the_largest_size(torch, N, K):  # noqa: F811
+    say(f"one row, N={N} K={K}")
+    x, w = whole(torch, 1, (1, K), "f16", 1 << 22), whole(torch, 2, (1, N, K), "f16", 1 << 22)
+    dy = whole(torch, 3, (1, N), "f16", 1 << 22)
+    y, dx, dw = torch.empty_like(dy), torch.empty_like(x), torch.empty_like(w)
+    db = torch.empty_like(dy)
+    B.pw_moe_product(1, 1, N, K, x, w, y, scratch(torch, B.pw_moe_product_workspace_bytes(1, 1, N, K)))
+    B.pw_moe_product_backward(1, 1, N, K, dy, x, w, scratch(torch, B.pw_moe_product_backward_workspace_bytes(1, 1, N, K)), dx=dx,
+                              dw=dw, dbias=db)
+    assert np.array_equal(f64(y), f64(x) @ f64(w)[0].T) and np.array_equal(f64(dx), f64(dy) @ f64(w)[0])
+    assert np.array_equal(f64(dw)[0], f64(dy).T * f64(x)) and torch.equal(db, dy)

@@ -73,6 +73,17 @@ def test_gradient_of_no_rows_with_an_activation(lib):
     assert call(B.PW_ACT_NONE, None) == B.PW_OK and call(B.PW_ACT_NONE, P) == BAD
 
 
+def test_strides_of_single_rows(lib):
+    """One row of the largest size is no shape to refuse (the null matrix behind it is), two rows that far apart are."""
+    def call(S, N, K, xs, ys):
+        return lib.pw_moe_product(1, S, N, K, B.PW_F16, P, xs, None, P, None, 0, None, 0, None, 0, None if S == 1 else P, ys, P,
+                                  HUGE, None)
+
+    far = 1 << 22
+    assert call(1, far, 64, 64, far) == BAD and call(1, 64, far, far, 64) == BAD
+    assert call(1, 64, 64, far + 8, 64) == SHAPE and call(2, 64, 64, far, 64) == SHAPE and call(2, far, 64, 64, far) == SHAPE
+
+
 def test_rows_that_tiles_cannot_count(lib):
     """Rounded up to whole tiles of 256, the rows have to be a 32-bit number."""
     most = (1 << 31) - 256
