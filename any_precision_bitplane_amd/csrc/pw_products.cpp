@@ -205,10 +205,11 @@ pw_status pw_moe_ffn(const pw_moe_shape* shape, int32_t S, int32_t dtype, const 
                      void* z, int64_t z_stride, float* z_scale, void* y, int64_t y_stride, void* workspace,
                      size_t workspace_bytes, void* stream) {
   PW_TRY(check_ffn(shape, S));
-  if (!sixteen(dtype) || (act != PW_ACT_SILU && act != PW_ACT_GELU) || (!z && z_scale)) return PW_ERR_INVALID_ARG;
+  if (!sixteen(dtype) || (act != PW_ACT_SILU && act != PW_ACT_GELU)) return PW_ERR_INVALID_ARG;
   const int H = shape->hidden, I = shape->inter, E = shape->num_experts;
   PW_TRY(check_offsets(offsets, E));
   if (S == 0) return PW_OK;
+  if (!z && z_scale) return PW_ERR_INVALID_ARG;
   PW_TRY(check_wide_rows(x, x_stride, S, H, 2, false));
   PW_TRY(check_matrix(w_gate_up));
   PW_TRY(check_matrix(w_down));

@@ -119,6 +119,14 @@ def test_ffn_refusals(lib):
     assert B.pw_moe_ffn_workspace_bytes(B.shape(60, 96, 3, 2), 4) == 0
 
 
+def test_ffn_of_no_rows_with_a_checkpoint(lib):
+    """Of codes without rows the address is null; the scales' buffer may be one for the largest step."""
+    shp = B.shape(64, 96, 3, 2)
+    call = lambda S, z: lib.pw_moe_ffn(ctypes.byref(shp), S, B.PW_F16, P, 64, P, P, P, B.PW_ACT_SILU, B.PW_E4M3, z, 192, P, P, 64,
+                                       None, 0, None)
+    assert call(0, None) == B.PW_OK and call(0, P) == B.PW_OK and call(4, None) == BAD
+
+
 def test_ffn_backward_refusals(lib):
     shp = B.shape(64, 96, 3, 2)
 
