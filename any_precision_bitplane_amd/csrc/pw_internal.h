@@ -458,6 +458,8 @@ struct ProductArgs {
 // S 256, N = K = 4096 26 of 34; S 128 24 of 28), up to three eighths 128 rows
 // (S 1024 47 of 54).  As many blocks run together as have tiles cut into parts,
 // whose sums a call needs scratch for.
+constexpr int kProdN = 256;      // columns of a tile: two halves of 128
+constexpr int kProdK = 64;       // reduction steps that are copied together
 constexpr int kWideRows = 160, kMidRows = 56, kNarrowRows = 32;
 constexpr int kProdParts = 16;   // most parts of a tile
 constexpr unsigned product_blocks(int rows) { return rows <= 64 ? 2 * kNumCUs : kNumCUs; }
@@ -494,6 +496,25 @@ inline size_t product_part_bytes(int E, int64_t S) {
   const int rows = product_mean_rows(E, S);
   return (size_t)product_blocks(rows) * rows * 256 * sizeof(float);
 }
+// Column tiles of a result of N columns (gated: of either half).
+inline int product_col_tiles(int kind, int N) {
+  const int tile = kind == kProductGate ? kProdN / 2 : kProdN;
+  return (N + tile - 1) / tile;
+}
+// Blocks that cover every tile whatever the offsets: a row tile more per expert
+// with rows than the rows fill.
+inline int64_t product_row_tiles(bool ragged, int E, int64_t S, int BM) {
+  if (!ragged) return (S + BM - 1) / BM;
+  const int64_t with_rows = S < E ? S : E;
+  return S / BM + with_rows < S ? S / BM + with_rows : S;
+}
+// Whether tiles may be cut: where that can save what its launch costs, with one
+// round or less (the host sees no more than a bound of a ragged call's tiles), or a
+// long reduction.
+inline bool product_is_cut(bool ragged, int64_t tiles, int64_t steps, int rows) {
+  const int64_t most = product_blocks(rows);
+  return ragged ? steps >= 40 || (tiles <= most && steps >= 8) : tiles % most && steps >= 6;
+}
 hipError_t launch_product(const ProductArgs& a, int dtype, int kind, hipStream_t s);
 // Few rows take the form without tiles: up to kFewRows an expert on average, or up
 // to 64 with matrices so small that a call is as long as its launches.  Against
@@ -527,6 +548,8 @@ struct OuterArgs {
 // (one expert, 1355 rows, 496 x 48 bf16: 55 us in one piece).
 inline int64_t outer_small_tiles(int E, int64_t M, int64_t N) { return (int64_t)E * ((M + 127) / 128) * ((N + 127) / 128); }
 inline bool outer_is_small(int E, int64_t M, int64_t N) { return (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) < kNumCUs; }
+// Of the others, tiles of 256 x 128, two blocks a CU, take few rows an expert.
+inline bool outer_is_short(int E, int64_t S) { return S < 128ll * E; }
 inline int outer_parts(int E, int64_t S, int64_t M, int64_t N) {
   if (!outer_is_small(E, M, N)) return 1;
   const int64_t fill = 2 * kNumCUs / outer_small_tiles(E, M, N), by_rows = S / E / 256;

@@ -20,8 +20,6 @@
 
 namespace pw {
 
-constexpr int kProdN = 256;       // columns of a tile: two halves of 128
-constexpr int kProdK = 64;        // reduction steps that are copied together
 constexpr int kProdGroup = 8;     // row tiles that go through all columns together
 constexpr uint32_t kRsrcBytes = 0x80000000u;
 
@@ -143,13 +141,7 @@ struct Rounds {
   }
 };
 
-// Blocks that cover every tile whatever the offsets: a row tile more per expert
-// with rows than the rows fill.
-inline int64_t product_row_tiles(const int32_t* offsets, int E, int64_t S, int BM) {
-  if (!offsets) return (S + BM - 1) / BM;
-  const int64_t with_rows = S < E ? S : E;
-  return S / BM + with_rows < S ? S / BM + with_rows : S;
-}
+// The blocks are dealt to eight XCDs.
 inline int64_t product_grid(int64_t row_tiles, int64_t NT) { return (row_tiles * NT + 7) / 8 * 8; }
 // A launch has less than 2^32 threads.
 inline bool launch_fits(int64_t blocks, int threads) { return blocks * threads <= 0xFFFFFFFFll; }

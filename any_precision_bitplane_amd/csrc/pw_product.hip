@@ -319,12 +319,9 @@ __global__ __launch_bounds__(256) void join_kernel(ProductArgs a) {
 template <int DT, int EPI, int MI, int WM, int WN>
 hipError_t run(ProductArgs a, hipStream_t s) {
   using Sh = Shape<MI, WM, WN>;
-  a.NT = EPI == kProductGate ? (a.N + kKeepGroup - 1) / kKeepGroup : (a.N + kProdN - 1) / kProdN;
-  // Cut where it can save what its launch costs: with one round or less (the
-  // host sees no more than a bound of a ragged call's tiles), or a long reduction.
-  const int64_t tiles = product_row_tiles(a.offsets, a.E, a.S, Sh::kRows) * a.NT, most = product_blocks(Sh::kRows);
-  const int steps = (a.K + kProdK - 1) / kProdK;
-  const bool cut = a.part && (a.offsets ? steps >= 40 || (tiles <= most && steps >= 8) : tiles % most && steps >= 6);
+  a.NT = product_col_tiles(EPI, a.N);
+  const int64_t tiles = product_row_tiles(a.offsets != nullptr, a.E, a.S, Sh::kRows) * a.NT, most = product_blocks(Sh::kRows);
+  const bool cut = a.part && product_is_cut(a.offsets != nullptr, tiles, (a.K + kProdK - 1) / kProdK, Sh::kRows);
   if (!cut) a.part = nullptr;
   const int64_t grid = (tiles + 7) / 8 * 8 + (cut ? most : 0);
   if (!launch_fits(grid, Sh::kThreads)) return hipErrorInvalidValue;
@@ -338,8 +335,7 @@ hipError_t run(ProductArgs a, hipStream_t s) {
 
 template <int DT, int EPI>
 hipError_t pick(const ProductArgs& a, hipStream_t s) {
-  const int tile = EPI == kProductGate ? kKeepGroup : kProdN;
-  switch (product_rows(a.E, a.S, (a.N + tile - 1) / tile)) {
+  switch (product_rows(a.E, a.S, product_col_tiles(EPI, a.N))) {
     case 256: return run<DT, EPI, 4, 2, 4>(a, s);
     case 128: return run<DT, EPI, 2, 2, 4>(a, s);
     case 64: return run<DT, EPI, 2, 1, 4>(a, s);

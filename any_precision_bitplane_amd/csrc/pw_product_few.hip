@@ -121,7 +121,7 @@ int row_pieces(int E, int64_t S) {
   return mean > 16 ? 4 : mean > 4 ? 2 : 1;
 }
 int64_t blocks_of(const ProductArgs& a, int pieces) {
-  return product_grid(product_row_tiles(a.offsets, a.E, a.S, pieces * 16), (a.N + 15) / 16);
+  return product_grid(product_row_tiles(a.offsets != nullptr, a.E, a.S, pieces * 16), (a.N + 15) / 16);
 }
 
 template <int DT, int EPI, int RT>

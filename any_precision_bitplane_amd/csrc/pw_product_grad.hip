@@ -175,13 +175,13 @@ hipError_t run_outer(OuterArgs a, hipStream_t s) {
 template <int DT>
 hipError_t pick_outer(const OuterArgs& a, hipStream_t s) {
   if (outer_is_small(a.E, a.M, a.N)) return run_outer<DT, 128, 128>(a, s);
-  return a.S < 128ll * a.E ? run_outer<DT, 256, 128>(a, s) : run_outer<DT, 256, 256>(a, s);
+  return outer_is_short(a.E, a.S) ? run_outer<DT, 256, 128>(a, s) : run_outer<DT, 256, 256>(a, s);
 }
 
 template <int DT>
 hipError_t run_dz(const DzArgs& a, hipStream_t s) {
   if (a.S > 0) {
-    const int64_t grid = product_grid(product_row_tiles(a.offsets, a.E, a.S, kDzRows), (a.N + 255) / 256);
+    const int64_t grid = product_grid(product_row_tiles(a.offsets != nullptr, a.E, a.S, kDzRows), (a.N + 255) / 256);
     if (!launch_fits(grid, kDzThreads)) return hipErrorInvalidValue;
     hipLaunchKernelGGL(dz_kernel<DT>, dim3((unsigned)grid), dim3(kDzThreads), 0, s, a);
   }

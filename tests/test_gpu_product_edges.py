@@ -112,3 +112,27 @@ def test_a_row_of_the_largest_size(torch, N, K):  # noqa: F811
                               dw=dw, dbias=db)
     assert np.array_equal(f64(y), f64(x) @ f64(w)[0].T) and np.array_equal(f64(dx), f64(dy) @ f64(w)[0])
     assert np.array_equal(f64(dw)[0], f64(dy).T * f64(x)) and torch.equal(db, dy)
+
+
+def test_offsets_past_the_rows_count_as_the_nearer_end(torch):  # noqa: F811
+    E, S, N, K, I = 4, 300, 264, 136, 160
+    say(f"offsets below 0 and past S, E={E} S={S}")
+    off = torch.tensor([-7, 40, 40, 131, 1 << 30], dtype=torch.int32, device=DEV)
+    same = torch.tensor([0, 40, 40, 131, S], dtype=torch.int32, device=DEV)
+    x, w, dy = rand(torch, 1, (S, K), "f16"), rand(torch, 2, (E, N, K), "f16"), rand(torch, 3, (S, N), "f16")
+    ws = scratch(torch, B.pw_moe_product_backward_workspace_bytes(E, S, N, K))
+    shp = B.shape(K - 8, I, E, 1)
+    wg, wd, xs = rand(torch, 4, (E, 2 * I, K - 8), "f16", 0.1), rand(torch, 5, (E, K - 8, I), "f16", 0.1), x[:, :K - 8].contiguous()
+    wf = scratch(torch, B.pw_moe_ffn_backward_workspace_bytes(shp, S))
+    got = []
+    for o in (same, off):
+        t = [torch.full(s, 7.0, dtype=x.dtype, device=DEV) for s in
+             [(S, N), (S, K), (E, N, K), (E, N), (S, K - 8), (S, 2 * I), (S, K - 8), (E, 2 * I, K - 8), (E, K - 8, I)]]
+        B.pw_moe_product(E, S, N, K, x, w, t[0], ws, offsets=o)
+        B.pw_moe_product_backward(E, S, N, K, dy, x, w, ws, offsets=o, dx=t[1], dw=t[2], dbias=t[3])
+        B.pw_moe_ffn(shp, S, xs, wg, wd, t[4], wf, offsets=o, z=t[5])
+        B.pw_moe_ffn_backward(shp, S, xs, xs, wg, wd, t[5], wf, offsets=o, dx=t[6], dw_gate_up=t[7], dw_down=t[8])
+        got.append(t)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert not bool(got[0][2][1].any()) and not any(bool((t == 7.0).any()) for t in got[0][:2])
