@@ -507,7 +507,9 @@ pw_status pw_router_backward(const pw_moe_shape* shape /* host */, int32_t T, co
  *
  * Sums are fp32; an output is rounded once.  Between two products of one call
  * (h, and gradients of gate and up or of the product's sum) values are rounded
- * to dtype, as the matrix cores take them.
+ * to dtype, as the matrix cores take them, and past the type's largest value
+ * (fp16: 65504) they are infinities there, whatever the sum that follows would
+ * have made of them.
  *
  * Activations: act(z) = z, z / (1 + exp(-z)), or z Phi(z) with the normal
  * distribution function Phi(z) = erfc(-z / sqrt 2) / 2; values of act and of its

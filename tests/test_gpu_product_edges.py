@@ -137,3 +137,29 @@ def test_offsets_past_the_rows_count_as_the_nearer_end(torch):  # noqa: F811
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(*got))
     # all of every output is written (a number of the inputs' size could be any fill but NaN), zero for no rows
     assert not bool(got[0][2][1].any()) and not any(bool(t.isnan().any()) for t in got[0])
+
+
+@pytest.mark.parametrize("S", [3, 200])
+def test_overflow_between_two_products(torch, S):  # noqa: F811
+    """act(gate) up past the largest fp16 is an infinity, in its row alone; bf16 holds it, and so does the checkpoint."""
+    H, I = 64, 32
+    say(f"h of 90000 in a row of S={S}")
+    shp = B.shape(H, I, 1, 1)
+    for name in DTYPES:
+        t = dtype_of(torch, name)
+        x = torch.zeros((S, H), dtype=t, device=DEV)
+        x[:, 0] = 1
+        x[S - 2, 0] = 300
+        wg, wd = torch.zeros((1, 2 * I, H), dtype=t, device=DEV), torch.full((1, H, I), 2.0 ** -10, dtype=t, device=DEV)
+        wg[:, :, 0] = 1
+        y, z = torch.empty((S, H), dtype=t, device=DEV), torch.empty((S, 2 * I), dtype=t, device=DEV)
+        B.pw_moe_ffn(shp, S, x, wg, wd, y, scratch(torch, B.pw_moe_ffn_workspace_bytes(shp, S)), z=z)
+        one = 1 / (1 + math.exp(-1))
+        want = np.full((S, H), one * I / 1024)
+        want[S - 2] = math.inf if name == "f16" else 90000 * I / 1024
+        rel = half_step(torch, name)[0]
+        got = f64(y)
+        far = np.isinf(want)
+        assert np.array_equal(np.isinf(got), far) and bool((z[S - 2] == 300).all())
+        # h and y are rounded, sums of equal values are exact but for fp32's rounding, SiLU is off by at most 64 U of itself
+        near(got[~far], want[~far], (2 * rel + rel * rel + (64 + I) * U) * want[~far] * (1 + rel), name)
