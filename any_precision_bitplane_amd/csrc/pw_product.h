@@ -4,7 +4,8 @@
 //
 // Tiles.  A block takes a tile of BM rows by 256 columns of one expert and walks
 // the reduction in steps of 64, a cache line of every row (with steps of 32 the
-// L2s serve every line twice: 8192 x 8192 x 8192 bf16 907 us against 760).  A
+// L2s serve every line twice: 8192 x 8192 x 8192 bf16 907 us against 850 when this
+// was changed, 760 now).  A
 // step's operands are copied from memory to LDS without passing registers, ahead
 // of the products.  An operand whose reduction index is contiguous in memory lies
 // in LDS as rows of 64 (eight 16-byte pieces, piece c of row r at place c ^ (r /

@@ -9,10 +9,16 @@
 // u, so that a wave holds both for its columns).
 //
 // What bounds it: with many rows the matrix cores and the power they draw (8192 x
-// 8192 x 8192 bf16 771 us, 1427 TFLOP/s, three quarters of the cycles busy at 1.77
-// GHz; H 4096, I 14336, 8190 rows over 8 experts, gate and up 1.79 ms, back to x
-// 1.49); with few rows reading the matrices (E 8, H 4096, I 14336, 128 rows, 2.8
-// GB in 488 us, 5.8 TB/s).
+// 8192 x 8192 bf16 760 us, 1447 TFLOP/s, three quarters of the cycles busy at 1.77
+// GHz; H 4096, I 14336, some 8190 rows over 8 experts, gate and up bf16 with 8-bit
+// copies 1.84 ms, back to x fp16 1.52); with few rows reading the matrices (E 8, H
+// 4096, I 14336, 128 rows, 2.8 GB in 488 to 515 us, 5.5 to 5.8 TB/s).
+//
+// h, dg and du are rounded to the rows' type: they are operands of the next
+// product, and the matrix cores take 16 bits (two parts of 16 bits a value would
+// be a third more products in the block, five sixths more in its gradient).  It makes the block's error
+// against 64 bits sqrt 2 times as large (fp16 2.9e-4 for 2.1e-4, bf16 2.3e-3 for
+// 1.7e-3), and in fp16 a value past 65504 an infinity.
 #include "pw_product.h"
 
 namespace pw {
@@ -163,8 +169,8 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const Tile& t, f32x
     __syncthreads();
   }
   // What 32 rows need besides is requested while the 32 before are worked on, and
-  // waits in LDS, each lane's own (requested row by row, the residual and pre took
-  // the 8194 x 8192 x 2048 bf16 product from 254 us to 348).
+  // waits in LDS, each lane's own (8194 rows, 8192 x 2048 bf16 with GELU, residual
+  // and pre: 387 us requested row by row, 343 so).
   constexpr bool kBesides = EPI == kProductAct || EPI == kProductGateGrad;
   const bool want = wants<EPI>(a) && !part;
   const floatx8 bias = bias_of<DT, EPI>(a, t.e, n);

@@ -4,9 +4,10 @@
 // its eight waves take every eighth 64 steps of the reduction each, with the
 // loads of several such pieces in flight, straight into the operands of the
 // matrix cores, and add their sums through LDS in the order of the waves.  H 2048,
-// I 1408, E 60, 16 rows over 14 experts: 240 MB in 49 us, 5 TB/s; one row through
-// one expert of I 5632, 69 MB in 21 us, of which two launches and their first
-// loads are some 8.
+// I 1408, E 60, 16 rows over 14 experts: 240 MB in 49 us, 5 TB/s.  One row through
+// one expert of I 5632: gate and up, 46 MB, 12.5 us, down, 23 MB, 9.3 (2.5 TB/s: its
+// 128 blocks leave half of the CUs without one, and the loads of a round of pieces
+// are waited for before the next round's are asked for).
 #include "pw_product.h"
 
 namespace pw {

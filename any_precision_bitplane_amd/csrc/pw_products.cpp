@@ -74,7 +74,9 @@ size_t dz_sum_bytes(int E, int64_t S, int N) { return align_up(sizeof(float) * d
 size_t h_bytes(int64_t S, int64_t I) { return align_up((size_t)S * (size_t)I * 2 + 1, kAlign); }
 
 // Scratch of a forward call's cut tiles, whose largest matrix has so many elements:
-// none for the few rows whose products have no tiles (no more rows have tiles then).
+// none for few rows, whose products have no tiles (no more rows have tiles then).
+// Gate and up of few rows with 8-bit copies do have tiles, which are not cut (one
+// expert, H 2048, I 1408, 8 rows fp16 28.6 us where 14.7 without copies).
 size_t forward_part_bytes(int E, int64_t S, int64_t matrix) {
   return few_rows_for(E, S, matrix) ? 0 : product_part_bytes(E, S);
 }
