@@ -548,7 +548,11 @@ struct OuterArgs {
 // (one expert, 1355 rows, 496 x 48 bf16: 55 us in one piece).
 inline int64_t outer_small_tiles(int E, int64_t M, int64_t N) { return (int64_t)E * ((M + 127) / 128) * ((N + 127) / 128); }
 inline bool outer_is_small(int E, int64_t M, int64_t N) { return (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) < kNumCUs; }
-// Of the others, tiles of 256 x 128, two blocks a CU, take few rows an expert.
+// Of the others, tiles of 256 x 128, two blocks a CU, take few rows an expert.  The
+// two cross at some 64 rows for 60 experts of 2816 x 2048 and between 128 and 256
+// for 8 of 14336 x 4096 (bf16, dx and dW, 256 x 128 against 256 x 256, us: E 60, 17
+// rows 293 and 307, 64 334 and 334, 128 424 and 412, 239 500 and 493; E 8, 32 rows
+// 420 and 444, 128 521 and 538, 256 657 and 655, 512 988 and 979).
 inline bool outer_is_short(int E, int64_t S) { return S < 128ll * E; }
 inline int outer_parts(int E, int64_t S, int64_t M, int64_t N) {
   if (!outer_is_small(E, M, N)) return 1;
